@@ -13,6 +13,7 @@
 #include <mutex>
 #include <string.h>
 
+#include "emu_block_launch.h"
 #include "emu_launch.h"
 #include "emu_sgemm.h"
 
@@ -462,6 +463,29 @@ int mode_bands(emu_mode_t mode)
 }
 
 }  // namespace
+
+// What the transformer-block operators use of this file (emu_block_launch.h).
+namespace emu {
+
+bool api_current_device(DeviceInfo& info) { return current_device(info); }
+
+int api_select_mode(int64_t M, int64_t N, int64_t K) { return (int)select_mode(M, N, K); }
+
+GemmPlan api_plan(int64_t M, int64_t N, int64_t K, bool split, int num_cu)
+{
+    Plan pl;
+    if (split) {
+        pl = choose_plan(M, N, K);
+        const int64_t tiles = (M + pl.tile_m - 1) / pl.tile_m * ((N + 127) / 128);
+        const int64_t round = tiles < num_cu ? tiles : num_cu;
+        if (pl.split_from % round != 0) pl.split_from = 0;
+    } else {
+        pl.tile_m = choose_tile_m(M, N, K, 1);
+    }
+    return GemmPlan{pl.split, pl.tile_m, pl.split_from};
+}
+
+}  // namespace emu
 
 extern "C" {
 

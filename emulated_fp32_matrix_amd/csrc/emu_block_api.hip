@@ -1,0 +1,410 @@
+// C ABI of the transformer-block operators (declarations and full contract in
+// include/emu_block.h): argument checks, the choice of route and the launches
+// on the caller's stream.  Nothing is allocated here: workspaces come from
+// the caller.
+#include <hip/hip_runtime.h>
+
+#include "emu_block.h"
+#include "emu_block_launch.h"
+
+namespace {
+
+using emu::BlockEpilogue;
+
+int64_t max1(int64_t v) { return v > 1 ? v : 1; }
+bool valid_act(int a) { return a >= EMU_ACT_IDENTITY && a <= EMU_ACT_TANH; }
+bool valid_op(int op) { return op == EMU_OP_N || op == EMU_OP_T; }
+bool valid_mode(int m) { return m >= EMU_MODE_NATIVE_F32 && m <= EMU_MODE_BF16X1; }
+// an array argument of `rows` rows that has to be there
+bool bad_array(const void* p, int64_t rows, int64_t cols, int64_t ld)
+{
+    return ld < max1(cols) || (rows > 0 && cols > 0 && p == nullptr);
+}
+bool bad_optional(const void* p, int64_t cols, int64_t ld) { return p != nullptr && ld < max1(cols); }
+bool bad_workspace(const void* ws, size_t have, size_t need)
+{
+    return need > 0 && (ws == nullptr || have < need || ((uintptr_t)ws & 255u) != 0);
+}
+
+emu_status_t from_hip(hipError_t e)
+{
+    if (e == hipSuccess) return EMU_STATUS_SUCCESS;
+    if (e == hipErrorOutOfMemory || e == hipErrorMemoryAllocation) return EMU_STATUS_ALLOC_FAILED;
+    return EMU_STATUS_LAUNCH_FAILED;
+}
+
+hipStream_t stream_of(void* s) { return static_cast<hipStream_t>(s); }
+
+// Columns of the element-wise passes are indexed with 32 bits.
+constexpr int64_t kMaxCols = (int64_t)1 << 30;
+
+int bands_of(emu_mode_t mode)
+{
+    switch (mode) {
+    case EMU_MODE_BF16X9: return 5;
+    case EMU_MODE_BF16X6: return 3;
+    case EMU_MODE_BF16X3: return 2;
+    case EMU_MODE_BF16X1: return 1;
+    default: return 0;
+    }
+}
+
+// Where EMU_MODE_AUTO takes the one-launch FP32 kernel.
+bool few_rows(int64_t M, int64_t N, int64_t K)
+{
+    (void)N;
+    (void)K;
+    return M <= 64;
+}
+
+size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+// How one product with its epilogue runs.
+struct Route {
+    bool rows;                 // the one-launch FP32 kernel
+    emu_mode_t mode;           // else: the product's mode,
+    emu::GemmPlan plan;        // its plan,
+    size_t gemm_bytes, t_bytes;   // and the workspace: the product's own, then t
+    int64_t ldt;
+};
+
+// N: columns of the product (gated: 2 F).
+Route route_of(const emu::GemmArgs& g, emu_mode_t mode, bool have_planes, int num_cu)
+{
+    Route r{};
+    const bool automatic = mode == EMU_MODE_AUTO;
+    r.rows = g.K == 0 || (automatic && !have_planes && few_rows(g.M, g.N, g.K));
+    if (r.rows) return r;
+    r.mode = !automatic ? mode : have_planes ? EMU_MODE_BF16X9 : (emu_mode_t)emu::api_select_mode(g.M, g.N, g.K);
+    if (r.mode == EMU_MODE_NATIVE_F32) {
+        r.gemm_bytes = round256(emu::gemm_native_f32_workspace_bytes(g));
+    } else {
+        r.plan = emu::api_plan(g.M, g.N, g.K, automatic && emu::fused_a_path(g), num_cu);
+        r.gemm_bytes = round256(
+            emu::gemm_bf16_workspace_bytes(g, bands_of(r.mode), r.plan.split, r.plan.tile_m, r.plan.split_from));
+    }
+    r.ldt = (g.N + 3) & ~(int64_t)3;
+    r.t_bytes = (size_t)g.M * (size_t)r.ldt * sizeof(float);
+    return r;
+}
+
+// The workspace query's device: sizes do not depend on it but through the
+// compute units of the plan; without a gfx950 the full chip's count.
+int query_cus()
+{
+    emu::DeviceInfo d;
+    return emu::api_current_device(d) ? d.num_cu : 256;
+}
+
+emu::GemmArgs gemm_args(bool trans_b, int64_t M, int64_t N, int64_t K, const float* A, int64_t lda,
+                        const float* B, int64_t ldb, const void* planes)
+{
+    emu::GemmArgs g{};
+    g.trans_a = false;
+    g.trans_b = trans_b;
+    g.M = M;
+    g.N = N;
+    g.K = K;
+    g.alpha = 1.0f;
+    g.beta = 0.0f;
+    g.A = A;
+    g.lda = lda;
+    g.B = B;
+    g.ldb = ldb;
+    g.bias = nullptr;
+    g.Bplanes = static_cast<const uint16_t*>(planes);
+    return g;
+}
+
+// The product A . op(B) (columns g.N) and its epilogue (columns n_out).
+emu_status_t product(emu::GemmArgs g, int64_t n_out, const BlockEpilogue& ep, emu_mode_t mode, void* ws,
+                     size_t ws_bytes, hipStream_t s)
+{
+    emu::DeviceInfo dev;
+    if (!emu::api_current_device(dev)) return EMU_STATUS_NOT_SUPPORTED;
+    const Route r = route_of(g, mode, g.Bplanes != nullptr, dev.num_cu);
+    if (r.rows)
+        return from_hip(emu::launch_rows_gemm(g.trans_b, g.M, n_out, g.K, g.A, g.lda, g.B, g.ldb, ep, s));
+    if (bad_workspace(ws, ws_bytes, r.gemm_bytes + r.t_bytes)) return EMU_STATUS_INVALID_VALUE;
+    float* t = reinterpret_cast<float*>(static_cast<char*>(ws) + r.gemm_bytes);
+    g.C = t;
+    g.ldc = r.ldt;
+    void* gws = r.gemm_bytes > 0 ? ws : nullptr;
+    hipError_t e = r.mode == EMU_MODE_NATIVE_F32
+                       ? emu::launch_gemm_native_f32(g, dev, gws, s)
+                       : emu::launch_gemm_bf16(g, bands_of(r.mode), r.plan.split, r.plan.split_from,
+                                               r.plan.tile_m, dev, gws, s);
+    if (e == hipSuccess) e = emu::launch_epilogue(g.M, n_out, t, r.ldt, ep, s);
+    return from_hip(e);
+}
+
+emu_status_t product_workspace(const emu::GemmArgs& g, emu_mode_t mode, bool have_planes, size_t* bytes)
+{
+    *bytes = 0;
+    if (g.M == 0 || g.N == 0) return EMU_STATUS_SUCCESS;
+    const Route r = route_of(g, mode, have_planes, query_cus());
+    if (!r.rows) *bytes = r.gemm_bytes + r.t_bytes;
+    return EMU_STATUS_SUCCESS;
+}
+
+// A planes pointer that a workspace query stands in for.
+const void* const kSomePlanes = reinterpret_cast<const void*>((uintptr_t)256);
+
+bool bad_planes(const void* planes, emu_mode_t mode)
+{
+    return planes != nullptr && (((uintptr_t)planes & 15u) != 0 || mode == EMU_MODE_NATIVE_F32);
+}
+
+}  // namespace
+
+extern "C" {
+
+int emu_block_version(void) { return 100; }
+
+// ---- layer norm -----------------------------------------------------------------
+
+emu_status_t emu_layer_norm(int64_t rows, int64_t cols, const float* x, int64_t ldx, const float* weight,
+                            const float* bias, float eps, float* y, int64_t ldy, float* mean, float* rstd,
+                            void* stream)
+{
+    if (rows < 0 || cols < 1 || !(eps >= 0.0f) || bad_array(x, rows, cols, ldx) || bad_array(y, rows, cols, ldy))
+        return EMU_STATUS_INVALID_VALUE;
+    if (cols > EMU_LAYER_NORM_MAX_COLS) return EMU_STATUS_NOT_SUPPORTED;
+    if (rows == 0) return EMU_STATUS_SUCCESS;
+    emu::DeviceInfo dev;
+    if (!emu::api_current_device(dev)) return EMU_STATUS_NOT_SUPPORTED;
+    return from_hip(emu::launch_norm(rows, cols, x, ldx, weight, bias, eps, y, ldy, mean, rstd, stream_of(stream)));
+}
+
+emu_status_t emu_layer_norm_backward_workspace(int64_t rows, int64_t cols, size_t* bytes)
+{
+    if (rows < 0 || cols < 1 || bytes == nullptr) return EMU_STATUS_INVALID_VALUE;
+    if (cols > EMU_LAYER_NORM_MAX_COLS) return EMU_STATUS_NOT_SUPPORTED;
+    *bytes = emu::norm_backward_workspace(rows, cols);
+    return EMU_STATUS_SUCCESS;
+}
+
+emu_status_t emu_layer_norm_backward(int64_t rows, int64_t cols, const float* dy, int64_t lddy, const float* x,
+                                     int64_t ldx, const float* weight, const float* mean, const float* rstd,
+                                     float* dx, int64_t lddx, float* dweight, float* dbias, void* workspace,
+                                     size_t workspace_bytes, void* stream)
+{
+    if (rows < 0 || cols < 1 || bad_array(dy, rows, cols, lddy) || bad_array(x, rows, cols, ldx) ||
+        bad_optional(dx, cols, lddx) || (rows > 0 && (mean == nullptr || rstd == nullptr)))
+        return EMU_STATUS_INVALID_VALUE;
+    if (cols > EMU_LAYER_NORM_MAX_COLS) return EMU_STATUS_NOT_SUPPORTED;
+    const bool sums = dweight != nullptr || dbias != nullptr;
+    if (sums && bad_workspace(workspace, workspace_bytes, emu::norm_backward_workspace(rows, cols)))
+        return EMU_STATUS_INVALID_VALUE;
+    if (!sums && (rows == 0 || dx == nullptr)) return EMU_STATUS_SUCCESS;
+    emu::DeviceInfo dev;
+    if (!emu::api_current_device(dev)) return EMU_STATUS_NOT_SUPPORTED;
+    hipStream_t s = stream_of(stream);
+    if (rows == 0) {
+        hipError_t e = emu::launch_zero(dweight, cols, s);
+        if (e == hipSuccess) e = emu::launch_zero(dbias, cols, s);
+        return from_hip(e);
+    }
+    return from_hip(emu::launch_norm_backward(rows, cols, dy, lddy, x, ldx, weight, mean, rstd, dx, lddx, dweight,
+                                              dbias, static_cast<float*>(workspace), s));
+}
+
+emu_status_t emu_layer_norm_backward2(int64_t rows, int64_t cols, const float* v, int64_t ldv, const float* p,
+                                      const float* q, const float* dy, int64_t lddy, const float* x,
+                                      int64_t ldx, const float* weight, const float* mean, const float* rstd,
+                                      float* gdy, int64_t ldgdy, float* gx, int64_t ldgx, float* gw,
+                                      void* workspace, size_t workspace_bytes, void* stream)
+{
+    if (rows < 0 || cols < 1 || bad_optional(v, cols, ldv) || bad_array(dy, rows, cols, lddy) ||
+        bad_array(x, rows, cols, ldx) || bad_optional(gdy, cols, ldgdy) || bad_optional(gx, cols, ldgx) ||
+        (rows > 0 && (mean == nullptr || rstd == nullptr)))
+        return EMU_STATUS_INVALID_VALUE;
+    if (cols > EMU_LAYER_NORM_MAX_COLS) return EMU_STATUS_NOT_SUPPORTED;
+    if (gw != nullptr && bad_workspace(workspace, workspace_bytes, emu::norm_backward_workspace(rows, cols)))
+        return EMU_STATUS_INVALID_VALUE;
+    if (gw == nullptr && (rows == 0 || (gdy == nullptr && gx == nullptr))) return EMU_STATUS_SUCCESS;
+    emu::DeviceInfo dev;
+    if (!emu::api_current_device(dev)) return EMU_STATUS_NOT_SUPPORTED;
+    hipStream_t s = stream_of(stream);
+    if (rows == 0) return from_hip(emu::launch_zero(gw, cols, s));
+    return from_hip(emu::launch_norm_backward2(rows, cols, v, ldv, p, q, dy, lddy, x, ldx, weight, mean, rstd, gdy,
+                                               ldgdy, gx, ldgx, gw, static_cast<float*>(workspace), s));
+}
+
+// ---- activations ------------------------------------------------------------------
+
+emu_status_t emu_act_backward(int64_t rows, int64_t cols, const float* dy, int64_t lddy, const float* z,
+                              int64_t ldz, emu_act_t act, float* dz, int64_t lddz, void* stream)
+{
+    if (rows < 0 || cols < 0 || !valid_act(act) || bad_array(dy, rows, cols, lddy) ||
+        bad_array(z, rows, cols, ldz) || bad_array(dz, rows, cols, lddz))
+        return EMU_STATUS_INVALID_VALUE;
+    if (cols > kMaxCols) return EMU_STATUS_NOT_SUPPORTED;
+    if (rows == 0 || cols == 0) return EMU_STATUS_SUCCESS;
+    emu::DeviceInfo dev;
+    if (!emu::api_current_device(dev)) return EMU_STATUS_NOT_SUPPORTED;
+    return from_hip(emu::launch_act_backward(rows, cols, dy, lddy, z, ldz, act, dz, lddz, stream_of(stream)));
+}
+
+emu_status_t emu_act_backward2(int64_t rows, int64_t cols, const float* v, int64_t ldv, const float* dy,
+                               int64_t lddy, const float* z, int64_t ldz, emu_act_t act, float* gdy,
+                               int64_t ldgdy, float* gz, int64_t ldgz, void* stream)
+{
+    if (rows < 0 || cols < 0 || !valid_act(act) || bad_array(v, rows, cols, ldv) ||
+        bad_array(dy, rows, cols, lddy) || bad_array(z, rows, cols, ldz) || bad_optional(gdy, cols, ldgdy) ||
+        bad_optional(gz, cols, ldgz))
+        return EMU_STATUS_INVALID_VALUE;
+    if (cols > kMaxCols) return EMU_STATUS_NOT_SUPPORTED;
+    if (rows == 0 || cols == 0 || (gdy == nullptr && gz == nullptr)) return EMU_STATUS_SUCCESS;
+    emu::DeviceInfo dev;
+    if (!emu::api_current_device(dev)) return EMU_STATUS_NOT_SUPPORTED;
+    return from_hip(emu::launch_act_backward2(rows, cols, v, ldv, dy, lddy, z, ldz, act, gdy, ldgdy, gz, ldgz,
+                                              stream_of(stream)));
+}
+
+// ---- linear layer with activation and residual --------------------------------------
+
+emu_status_t emu_sgemm_act_route(emu_op_t transB, int64_t M, int64_t N, int64_t K, int* few)
+{
+    if (!valid_op(transB) || M < 0 || N < 0 || K < 0 || few == nullptr) return EMU_STATUS_INVALID_VALUE;
+    *few = few_rows(M, N, K) ? 1 : 0;
+    return EMU_STATUS_SUCCESS;
+}
+
+emu_status_t emu_sgemm_act_workspace(emu_op_t transB, int64_t M, int64_t N, int64_t K, const float* A,
+                                     int64_t lda, int has_planes, emu_mode_t mode, size_t* bytes)
+{
+    if (!valid_op(transB) || !valid_mode(mode) || M < 0 || N < 0 || K < 0 || lda < max1(K) || bytes == nullptr ||
+        (has_planes && mode == EMU_MODE_NATIVE_F32))
+        return EMU_STATUS_INVALID_VALUE;
+    return product_workspace(gemm_args(transB == EMU_OP_T, M, N, K, A, lda, nullptr, 0,
+                                       has_planes ? kSomePlanes : nullptr),
+                             mode, has_planes != 0, bytes);
+}
+
+emu_status_t emu_sgemm_act(emu_op_t transB, int64_t M, int64_t N, int64_t K, const float* A, int64_t lda,
+                           const float* B, int64_t ldb, const void* planes, const float* bias, emu_act_t act,
+                           float* Z, int64_t ldz, const float* R, int64_t ldr, float* C, int64_t ldc,
+                           emu_mode_t mode, void* workspace, size_t workspace_bytes, void* stream)
+{
+    if (!valid_op(transB) || !valid_mode(mode) || !valid_act(act) || M < 0 || N < 0 || K < 0)
+        return EMU_STATUS_INVALID_VALUE;
+    const bool has_c = M > 0 && N > 0;
+    if (lda < max1(K) || (planes == nullptr && ldb < (transB == EMU_OP_N ? max1(N) : max1(K))) ||
+        bad_array(C, M, N, ldc) || bad_optional(Z, N, ldz) || bad_optional(R, N, ldr) || bad_planes(planes, mode) ||
+        (has_c && K > 0 && (A == nullptr || (B == nullptr && planes == nullptr))))
+        return EMU_STATUS_INVALID_VALUE;
+    if (N > kMaxCols || K > kMaxCols) return EMU_STATUS_NOT_SUPPORTED;
+    if (!has_c) return EMU_STATUS_SUCCESS;
+    const BlockEpilogue ep{(int)act, 0, bias, Z, ldz, R, ldr, C, ldc};
+    return product(gemm_args(transB == EMU_OP_T, M, N, K, A, lda, B, ldb, planes), N, ep, mode, workspace,
+                   workspace_bytes, stream_of(stream));
+}
+
+// ---- gated feed-forward projection -----------------------------------------------------
+
+emu_status_t emu_sgemm_gated_workspace(int64_t M, int64_t F, int64_t K, const float* A, int64_t lda,
+                                       int has_planes, emu_mode_t mode, size_t* bytes)
+{
+    if (!valid_mode(mode) || M < 0 || F < 0 || K < 0 || lda < max1(K) || bytes == nullptr ||
+        (has_planes && mode == EMU_MODE_NATIVE_F32) || F > kMaxCols)
+        return EMU_STATUS_INVALID_VALUE;
+    return product_workspace(gemm_args(true, M, 2 * F, K, A, lda, nullptr, 0, has_planes ? kSomePlanes : nullptr),
+                             mode, has_planes != 0, bytes);
+}
+
+emu_status_t emu_sgemm_gated(int64_t M, int64_t F, int64_t K, const float* A, int64_t lda, const float* W,
+                             int64_t ldw, const void* planes, const float* bias, emu_act_t act, float* Z,
+                             int64_t ldz, float* C, int64_t ldc, emu_mode_t mode, void* workspace,
+                             size_t workspace_bytes, void* stream)
+{
+    if (!valid_mode(mode) || !valid_act(act) || M < 0 || F < 0 || K < 0) return EMU_STATUS_INVALID_VALUE;
+    if (F > kMaxCols || K > kMaxCols) return EMU_STATUS_NOT_SUPPORTED;
+    const bool has_c = M > 0 && F > 0;
+    if (lda < max1(K) || (planes == nullptr && ldw < max1(K)) || bad_array(C, M, F, ldc) ||
+        bad_optional(Z, 2 * F, ldz) || bad_planes(planes, mode) ||
+        (has_c && K > 0 && (A == nullptr || (W == nullptr && planes == nullptr))))
+        return EMU_STATUS_INVALID_VALUE;
+    if (!has_c) return EMU_STATUS_SUCCESS;
+    const BlockEpilogue ep{(int)act, 1, bias, Z, ldz, nullptr, 0, C, ldc};
+    return product(gemm_args(true, M, 2 * F, K, A, lda, W, ldw, planes), F, ep, mode, workspace, workspace_bytes,
+                   stream_of(stream));
+}
+
+emu_status_t emu_presplit_gated_bytes(int64_t F, int64_t K, emu_mode_t mode, size_t* bytes)
+{
+    if (F < 0 || F > kMaxCols) return EMU_STATUS_INVALID_VALUE;
+    return emu_presplit_b_bytes(2 * F, K, mode, bytes);
+}
+
+emu_status_t emu_presplit_gated(int64_t F, int64_t K, const float* W, int64_t ldw, emu_mode_t mode, void* planes,
+                                void* stream)
+{
+    if (F < 0 || F > kMaxCols) return EMU_STATUS_INVALID_VALUE;
+    return emu_presplit_b(EMU_OP_T, 2 * F, K, W, ldw, mode, planes, stream);
+}
+
+emu_status_t emu_gated_backward(int64_t M, int64_t F, const float* dh, int64_t lddh, const float* Z, int64_t ldz,
+                                emu_act_t act, float* dZ, int64_t lddz, void* stream)
+{
+    if (M < 0 || F < 0 || F > kMaxCols || !valid_act(act) || bad_array(dh, M, F, lddh) ||
+        bad_array(Z, M, 2 * F, ldz) || bad_array(dZ, M, 2 * F, lddz))
+        return EMU_STATUS_INVALID_VALUE;
+    if (M == 0 || F == 0) return EMU_STATUS_SUCCESS;
+    emu::DeviceInfo dev;
+    if (!emu::api_current_device(dev)) return EMU_STATUS_NOT_SUPPORTED;
+    return from_hip(emu::launch_gated_backward(M, F, dh, lddh, Z, ldz, act, dZ, lddz, stream_of(stream)));
+}
+
+emu_status_t emu_gated_backward2(int64_t M, int64_t F, const float* V, int64_t ldv, const float* dh, int64_t lddh,
+                                 const float* Z, int64_t ldz, emu_act_t act, float* gdh, int64_t ldgdh, float* gZ,
+                                 int64_t ldgz, void* stream)
+{
+    if (M < 0 || F < 0 || F > kMaxCols || !valid_act(act) || bad_array(V, M, 2 * F, ldv) ||
+        bad_array(dh, M, F, lddh) || bad_array(Z, M, 2 * F, ldz) || bad_optional(gdh, F, ldgdh) ||
+        bad_optional(gZ, 2 * F, ldgz))
+        return EMU_STATUS_INVALID_VALUE;
+    if (M == 0 || F == 0 || (gdh == nullptr && gZ == nullptr)) return EMU_STATUS_SUCCESS;
+    emu::DeviceInfo dev;
+    if (!emu::api_current_device(dev)) return EMU_STATUS_NOT_SUPPORTED;
+    return from_hip(emu::launch_gated_backward2(M, F, V, ldv, dh, lddh, Z, ldz, act, gdh, ldgdh, gZ, ldgz,
+                                                stream_of(stream)));
+}
+
+// ---- weight gradient ----------------------------------------------------------------------
+
+emu_status_t emu_wgrad_workspace(int64_t rows, int64_t M, int64_t N, size_t* bytes)
+{
+    if (rows < 0 || M < 0 || N < 0 || bytes == nullptr) return EMU_STATUS_INVALID_VALUE;
+    *bytes = rows == 0 || M == 0 ? 0 : emu::wgrad_workspace(rows, M, N);
+    return EMU_STATUS_SUCCESS;
+}
+
+emu_status_t emu_wgrad(int64_t rows, int64_t M, int64_t N, const float* dZ, int64_t lddz, const float* X,
+                       int64_t ldx, float* dW, int64_t lddw, float* db, void* workspace, size_t workspace_bytes,
+                       void* stream)
+{
+    if (rows < 0 || M < 0 || N < 0 || bad_array(dZ, rows, M, lddz) || bad_array(X, rows, N, ldx) ||
+        bad_array(dW, M, N, lddw))
+        return EMU_STATUS_INVALID_VALUE;
+    if (M > kMaxCols || N > kMaxCols) return EMU_STATUS_NOT_SUPPORTED;
+    if (M == 0 || (N == 0 && db == nullptr)) return EMU_STATUS_SUCCESS;
+    if (rows > 0 && bad_workspace(workspace, workspace_bytes, emu::wgrad_workspace(rows, M, N)))
+        return EMU_STATUS_INVALID_VALUE;
+    emu::DeviceInfo dev;
+    if (!emu::api_current_device(dev)) return EMU_STATUS_NOT_SUPPORTED;
+    hipStream_t s = stream_of(stream);
+    if (rows == 0) {
+        hipError_t e = hipSuccess;
+        if (lddw == N || M == 1) {
+            e = emu::launch_zero(dW, M * N, s);
+        } else {
+            for (int64_t m = 0; m < M && e == hipSuccess; ++m) e = emu::launch_zero(dW + m * lddw, N, s);
+        }
+        if (e == hipSuccess) e = emu::launch_zero(db, M, s);
+        return from_hip(e);
+    }
+    return from_hip(emu::launch_wgrad(rows, M, N, dZ, lddz, X, ldx, dW, lddw, db, workspace, s));
+}
+
+}  // extern "C"

@@ -1,0 +1,153 @@
+// The product of few rows with its epilogue in one launch (emu_sgemm_act and
+// emu_sgemm_gated of include/emu_block.h in EMU_MODE_AUTO): one token, or the
+// tokens of a few atoms, where a launch and one memory latency are most of
+// the time.
+//
+// FP32 on v_mfma_f32_16x16x4_f32, operands read from memory to registers as
+// they are: no split of the weights, no LDS tiles, no second launch.  A
+// workgroup owns 16 columns (gated: 16 gate and the same 16 up columns) of
+// 16 MT rows; its 8 waves take every eighth 16-wide slice of k, so that the
+// weights, which are what has to be read, stream with 8 waves' loads in
+// flight, and their sums are added in LDS in wave order.  The instruction
+// sums over 4 k per lane group; a lane's 16-byte load covers k = 16 c + 4 (l /
+// 16) .. +3 and feeds one element to each of four instructions (both operands
+// in the same order).
+#include "emu_block_device.h"
+#include "emu_block_launch.h"
+
+namespace emu {
+namespace {
+
+constexpr int WAVES = 8;
+
+template <bool TB, bool GATED, int MT>
+__global__ __launch_bounds__(64 * WAVES) void rows_gemm_kernel(int64_t M, int N, int K, const float* __restrict__ A,
+                                                               int64_t lda, const float* __restrict__ B,
+                                                               int64_t ldb, BlockEpilogue ep)
+{
+    static_assert(TB || !GATED, "the gated projection's weights are stored N x K");
+    constexpr int G = GATED ? 2 : 1;
+    constexpr int U = MT == 4 ? 2 : 4;   // slices of k in flight per wave
+    __shared__ __attribute__((aligned(16))) f32x4_t part[WAVES][MT * G][64];
+
+    const int lane = threadIdx.x & 63;
+    const int wave = threadIdx.x >> 6;
+    const int64_t m0 = (int64_t)blockIdx.y * (16 * MT);
+    const int n0 = blockIdx.x * 16;
+    const int kq = (lane >> 4) * 4;
+    // rows and columns past the end repeat the last one; they are not stored
+    const int n = n0 + (lane & 15) < N ? n0 + (lane & 15) : N - 1;
+    const float* arow[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        const int64_t m = m0 + 16 * i + (lane & 15);
+        arow[i] = A + (m < M ? m : M - 1) * lda;
+    }
+    auto load_b = [&](int k, int col) __attribute__((always_inline)) {
+        if constexpr (TB) {
+            return load4(B + (int64_t)col * ldb, k, K);
+        } else {
+            f32x4_t v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = k + e < K ? B[(int64_t)(k + e) * ldb + col] : 0.0f;
+            return v;
+        }
+    };
+
+    f32x4_t acc[MT][G];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int g = 0; g < G; ++g) acc[i][g] = f32x4_t{};
+
+    const int slices = (K + 15) / 16;
+    for (int c0 = wave; c0 < slices; c0 += WAVES * U) {
+        f32x4_t b[U][G], a[U][MT];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int k = (c0 + u * WAVES) * 16 + kq;   // past the end: zeros
+#pragma unroll
+            for (int g = 0; g < G; ++g) b[u][g] = load_b(k, n + g * N);
+#pragma unroll
+            for (int i = 0; i < MT; ++i) a[u][i] = load4(arow[i], k, K);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int g = 0; g < G; ++g)
+                        // B first: lane l then holds row l % 16 and columns
+                        // 4 (l / 16) .. +3
+                        acc[i][g] = __builtin_amdgcn_mfma_f32_16x16x4f32(b[u][g][e], a[u][i][e], acc[i][g], 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int g = 0; g < G; ++g) part[wave][i * G + g][lane] = acc[i][g];
+    __syncthreads();
+
+    if (threadIdx.x >= 64 * MT) return;
+    const int i = threadIdx.x >> 6;
+    const int64_t m = m0 + 16 * i + (lane & 15);
+    if (m >= M) return;
+    const int c = n0 + 4 * (lane >> 4);
+    if (c >= N) return;
+    f32x4_t z[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        z[g] = part[0][i * G + g][lane];
+#pragma unroll
+        for (int w = 1; w < WAVES; ++w) z[g] = z[g] + part[w][i * G + g][lane];
+        if (ep.bias != nullptr) z[g] = z[g] + load4(ep.bias + (int64_t)g * N, c, N);
+        if (ep.Z != nullptr) store4(ep.Z + m * ep.ldz + (int64_t)g * N, c, N, z[g]);
+    }
+    f32x4_t o;
+    with_act(ep.act, [&]<int ACT>() {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = act_value<ACT>(z[0][e]);
+    });
+    if constexpr (GATED)
+        o = o * z[G - 1];
+    else if (ep.R != nullptr)
+        o = o + load4(ep.R + m * ep.ldr, c, N);
+    store4(ep.C + m * ep.ldc, c, N, o);
+}
+
+template <bool TB, bool GATED>
+void launch(int64_t M, int64_t N, int64_t K, const float* A, int64_t lda, const float* B, int64_t ldb,
+            const BlockEpilogue& ep, hipStream_t s)
+{
+    const int gx = (int)((N + 15) / 16);
+    auto go = [&]<int MT>() {
+        hipLaunchKernelGGL((rows_gemm_kernel<TB, GATED, MT>), dim3(gx, (int)((M + 16 * MT - 1) / (16 * MT))),
+                           dim3(64 * WAVES), 0, s, M, (int)N, (int)K, A, lda, B, ldb, ep);
+    };
+    if (M <= 16)
+        go.template operator()<1>();
+    else if (M <= 32)
+        go.template operator()<2>();
+    else
+        go.template operator()<4>();
+}
+
+}  // namespace
+
+hipError_t launch_rows_gemm(bool trans_b, int64_t M, int64_t N, int64_t K, const float* A, int64_t lda,
+                            const float* B, int64_t ldb, const BlockEpilogue& ep, hipStream_t s)
+{
+    // (gridDim.y holds the row blocks)
+    if ((M + 63) / 64 > 65535 || 2 * N >= ((int64_t)1 << 31) || K >= ((int64_t)1 << 30) || (ep.gated && !trans_b))
+        return hipErrorInvalidValue;
+    if (ep.gated)
+        launch<true, true>(M, N, K, A, lda, B, ldb, ep, s);
+    else if (trans_b)
+        launch<true, false>(M, N, K, A, lda, B, ldb, ep, s);
+    else
+        launch<false, false>(M, N, K, A, lda, B, ldb, ep, s);
+    return hipGetLastError();
+}
+
+}  // namespace emu
