@@ -387,7 +387,7 @@ emu_status_t emu_wgrad(int64_t rows, int64_t M, int64_t N, const float* dZ, int6
     if (rows < 0 || M < 0 || N < 0 || bad_array(dZ, rows, M, lddz) || bad_array(X, rows, N, ldx) ||
         bad_array(dW, M, N, lddw))
         return EMU_STATUS_INVALID_VALUE;
-    if (M > kMaxCols || N > kMaxCols) return EMU_STATUS_NOT_SUPPORTED;
+    if (lddz > emu::kWgradMaxLd || ldx > emu::kWgradMaxLd) return EMU_STATUS_NOT_SUPPORTED;
     if (M == 0 || (N == 0 && db == nullptr)) return EMU_STATUS_SUCCESS;
     if (rows > 0 && bad_workspace(workspace, workspace_bytes, emu::wgrad_workspace(rows, M, N)))
         return EMU_STATUS_INVALID_VALUE;

@@ -72,6 +72,9 @@ hipError_t launch_gated_backward2(int64_t M, int64_t F, const float* V, int64_t 
 hipError_t launch_rows_gemm(bool trans_b, int64_t M, int64_t N, int64_t K, const float* A, int64_t lda,
                             const float* B, int64_t ldb, const BlockEpilogue& ep, hipStream_t s);
 
+// Leading dimensions of the weight-gradient product: its 32-row slabs are
+// addressed with 32-bit byte offsets.
+constexpr int64_t kWgradMaxLd = ((int64_t)1 << 31) / (4 * 32) - 128;
 size_t wgrad_workspace(int64_t rows, int64_t M, int64_t N);
 hipError_t launch_wgrad(int64_t rows, int64_t M, int64_t N, const float* dZ, int64_t lddz, const float* X,
                         int64_t ldx, float* dW, int64_t lddw, float* db, void* ws, hipStream_t s);
