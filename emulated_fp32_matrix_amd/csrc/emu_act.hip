@@ -78,6 +78,54 @@ __global__ __launch_bounds__(256) void epilogue_kernel(int64_t M, int N, const f
     });
 }
 
+// Workgroup (i, y): rows of split tile i, 256 threads with one 4-column group
+// of C each; parts as ksplit_reduce_kernel's ws.
+template <bool GATED>
+__global__ __launch_bounds__(256) void split_epilogue_kernel(const float* __restrict__ parts, int segs, int nsplit,
+                                                             int split_from, int tiles_n, int th, int64_t M, int64_t N,
+                                                             BlockEpilogue ep)
+{
+    constexpr int TILE = 128, CW = GATED ? 64 : 128, PER_ROW = CW / 4, ROWS = 256 / PER_ROW;
+    const int tile = split_from + blockIdx.x;
+    const int tm = tile / tiles_n, tn = tile - tm * tiles_n;
+    const int r = blockIdx.y * ROWS + (int)threadIdx.x / PER_ROW;
+    const int cg = (int)(threadIdx.x % PER_ROW) * 4;
+    const int64_t row = (int64_t)tm * th + r, n0 = (int64_t)tn * CW;
+    if (row >= M || n0 + cg >= N) return;
+    const int cols = N - n0 < CW ? (int)(N - n0) : CW;
+    const int64_t stride = (int64_t)nsplit * th * TILE;
+    const float* src = parts + ((int64_t)blockIdx.x * th + r) * TILE + (GATED ? (cg >> 4) * 32 + (cg & 15) : cg);
+    auto total = [&](const float* q) {
+        f32x4_t t = *reinterpret_cast<const f32x4_t*>(q);
+        for (int s = 1; s < segs; ++s) t = t + *reinterpret_cast<const f32x4_t*>(q + s * stride);
+        return t;
+    };
+    f32x4_t z = add_bias(ep, total(src), n0, cg, cols);
+    f32x4_t u = {};
+    if (GATED) u = add_bias(ep, total(src + 16), n0 + N, cg, cols);
+    if (ep.Z != nullptr) {
+        store4(ep.Z + row * ep.ldz + n0, cg, cols, z);
+        if (GATED) store4(ep.Z + row * ep.ldz + n0 + N, cg, cols, u);
+    }
+    with_act(ep.act, [&]<int ACT>() {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) z[e] = act_value<ACT>(z[e]);
+    });
+    if (GATED)
+        z = z * u;
+    else if (ep.R != nullptr)
+        z = z + load4(ep.R + row * ep.ldr + n0, cg, cols);
+    store4(ep.C + row * ep.ldc + n0, cg, cols, z);
+}
+
+__global__ __launch_bounds__(256) void copy_rows_kernel(int64_t M, int K, const float* __restrict__ A, int64_t lda,
+                                                        float* __restrict__ dst, int64_t ldd, int groups,
+                                                        int rows_per_wg)
+{
+    each_group(M, groups, rows_per_wg,
+               [&](int64_t r, int c) { *reinterpret_cast<f32x4_t*>(dst + r * ldd + c) = load4(A + r * lda, c, K); });
+}
+
 __global__ __launch_bounds__(256) void act_backward_kernel(int64_t rows, int cols, const float* dy,
                                                            int64_t lddy, const float* z, int64_t ldz, int act,
                                                            float* dz, int64_t lddz, int groups,
@@ -180,6 +228,27 @@ hipError_t launch_epilogue(int64_t M, int64_t N, const float* t, int64_t ldt, co
 {
     const RowsPlan p = plan_rows(M, N);
     hipLaunchKernelGGL(epilogue_kernel, dim3(grid_of(p)), dim3(256), 0, s, M, (int)N, t, ldt, ep, p.groups,
+                       p.rows_per_wg);
+    return hipGetLastError();
+}
+
+hipError_t launch_split_epilogue(const float* parts, int segs, int nsplit, int split_from, int tiles_n, int tile_m,
+                                 int64_t M, int64_t N, const BlockEpilogue& ep, hipStream_t s)
+{
+    if (ep.gated)
+        hipLaunchKernelGGL(split_epilogue_kernel<true>, dim3(nsplit, tile_m / 16), dim3(256), 0, s, parts, segs,
+                           nsplit, split_from, tiles_n, tile_m, M, N, ep);
+    else
+        hipLaunchKernelGGL(split_epilogue_kernel<false>, dim3(nsplit, tile_m / 8), dim3(256), 0, s, parts, segs,
+                           nsplit, split_from, tiles_n, tile_m, M, N, ep);
+    return hipGetLastError();
+}
+
+hipError_t launch_copy_rows(int64_t M, int64_t K, const float* A, int64_t lda, float* dst, int64_t ldd,
+                            hipStream_t s)
+{
+    const RowsPlan p = plan_rows(M, K);
+    hipLaunchKernelGGL(copy_rows_kernel, dim3(grid_of(p)), dim3(256), 0, s, M, (int)K, A, lda, dst, ldd, p.groups,
                        p.rows_per_wg);
     return hipGetLastError();
 }

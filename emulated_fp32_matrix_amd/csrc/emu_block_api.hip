@@ -64,9 +64,25 @@ struct Route {
     bool rows;                 // the one-launch FP32 kernel
     emu_mode_t mode;           // else: the product's mode,
     emu::GemmPlan plan;        // its plan,
-    size_t gemm_bytes, t_bytes;   // and the workspace: the product's own, then t
-    int64_t ldt;
+    size_t gemm_bytes;         // and the workspace: the product's own, then
+    size_t more_bytes;         // NATIVE_F32: t; else A with 16-byte aligned rows, where it has none
+    int64_t ld;                // (leading dimension of either)
 };
+
+// g with A as the emulated kernel takes it: 16-byte aligned rows of whole
+// 16-byte groups, copied to the workspace where the caller's are not.
+bool needs_copy(const emu::GemmArgs& g) { return !emu::fused_a_path(g); }
+
+emu::GemmArgs with_copy(emu::GemmArgs g, const float* copy, int64_t ld)
+{
+    g.A = copy;
+    g.lda = ld;
+    g.a_whole_groups = true;
+    return g;
+}
+
+// (stands for the copy in a workspace query: 16-byte aligned)
+const float* const kSomeRows = reinterpret_cast<const float*>((uintptr_t)256);
 
 // N: columns of the product (gated: 2 F).
 Route route_of(const emu::GemmArgs& g, emu_mode_t mode, bool have_planes, int num_cu)
@@ -78,13 +94,19 @@ Route route_of(const emu::GemmArgs& g, emu_mode_t mode, bool have_planes, int nu
     r.mode = !automatic ? mode : have_planes ? EMU_MODE_BF16X9 : (emu_mode_t)emu::api_select_mode(g.M, g.N, g.K);
     if (r.mode == EMU_MODE_NATIVE_F32) {
         r.gemm_bytes = round256(emu::gemm_native_f32_workspace_bytes(g));
+        r.ld = (g.N + 3) & ~(int64_t)3;
+        r.more_bytes = (size_t)g.M * (size_t)r.ld * sizeof(float);
     } else {
-        r.plan = emu::api_plan(g.M, g.N, g.K, automatic && emu::fused_a_path(g), num_cu);
+        emu::GemmArgs f = g;
+        if (needs_copy(g)) {
+            r.ld = (g.K + 3) & ~(int64_t)3;
+            r.more_bytes = (size_t)g.M * (size_t)r.ld * sizeof(float);
+            f = with_copy(g, kSomeRows, r.ld);
+        }
+        r.plan = emu::api_plan(g.M, g.N, g.K, automatic, num_cu);
         r.gemm_bytes = round256(
-            emu::gemm_bf16_workspace_bytes(g, bands_of(r.mode), r.plan.split, r.plan.tile_m, r.plan.split_from));
+            emu::gemm_bf16_workspace_bytes(f, bands_of(r.mode), r.plan.split, r.plan.tile_m, r.plan.split_from));
     }
-    r.ldt = (g.N + 3) & ~(int64_t)3;
-    r.t_bytes = (size_t)g.M * (size_t)r.ldt * sizeof(float);
     return r;
 }
 
@@ -125,16 +147,23 @@ emu_status_t product(emu::GemmArgs g, int64_t n_out, const BlockEpilogue& ep, em
     const Route r = route_of(g, mode, g.Bplanes != nullptr, dev.num_cu);
     if (r.rows)
         return from_hip(emu::launch_rows_gemm(g.trans_b, g.M, n_out, g.K, g.A, g.lda, g.B, g.ldb, ep, s));
-    if (bad_workspace(ws, ws_bytes, r.gemm_bytes + r.t_bytes)) return EMU_STATUS_INVALID_VALUE;
-    float* t = reinterpret_cast<float*>(static_cast<char*>(ws) + r.gemm_bytes);
-    g.C = t;
-    g.ldc = r.ldt;
+    if (bad_workspace(ws, ws_bytes, r.gemm_bytes + r.more_bytes)) return EMU_STATUS_INVALID_VALUE;
+    float* more = reinterpret_cast<float*>(static_cast<char*>(ws) + r.gemm_bytes);
     void* gws = r.gemm_bytes > 0 ? ws : nullptr;
-    hipError_t e = r.mode == EMU_MODE_NATIVE_F32
-                       ? emu::launch_gemm_native_f32(g, dev, gws, s)
-                       : emu::launch_gemm_bf16(g, bands_of(r.mode), r.plan.split, r.plan.split_from,
-                                               r.plan.tile_m, dev, gws, s);
-    if (e == hipSuccess) e = emu::launch_epilogue(g.M, n_out, t, r.ldt, ep, s);
+    hipError_t e = hipSuccess;
+    if (r.mode == EMU_MODE_NATIVE_F32) {
+        g.C = more;
+        g.ldc = r.ld;
+        e = emu::launch_gemm_native_f32(g, dev, gws, s);
+        if (e == hipSuccess) e = emu::launch_epilogue(g.M, n_out, more, r.ld, ep, s);
+        return from_hip(e);
+    }
+    if (needs_copy(g)) {
+        e = emu::launch_copy_rows(g.M, g.K, g.A, g.lda, more, r.ld, s);
+        g = with_copy(g, more, r.ld);
+    }
+    if (e == hipSuccess)
+        e = emu::launch_gemm_bf16(g, bands_of(r.mode), r.plan.split, r.plan.split_from, r.plan.tile_m, dev, gws, s, &ep);
     return from_hip(e);
 }
 
@@ -143,7 +172,7 @@ emu_status_t product_workspace(const emu::GemmArgs& g, emu_mode_t mode, bool hav
     *bytes = 0;
     if (g.M == 0 || g.N == 0) return EMU_STATUS_SUCCESS;
     const Route r = route_of(g, mode, have_planes, query_cus());
-    if (!r.rows) *bytes = r.gemm_bytes + r.t_bytes;
+    if (!r.rows) *bytes = r.gemm_bytes + r.more_bytes;
     return EMU_STATUS_SUCCESS;
 }
 
@@ -340,8 +369,13 @@ emu_status_t emu_presplit_gated_bytes(int64_t F, int64_t K, emu_mode_t mode, siz
 emu_status_t emu_presplit_gated(int64_t F, int64_t K, const float* W, int64_t ldw, emu_mode_t mode, void* planes,
                                 void* stream)
 {
-    if (F < 0 || F > kMaxCols) return EMU_STATUS_INVALID_VALUE;
-    return emu_presplit_b(EMU_OP_T, 2 * F, K, W, ldw, mode, planes, stream);
+    if (F < 0 || F > kMaxCols || K < 0 || bands_of(mode) == 0 || ldw < max1(K)) return EMU_STATUS_INVALID_VALUE;
+    if (F == 0 || K == 0) return EMU_STATUS_SUCCESS;
+    if (W == nullptr || planes == nullptr || ((uintptr_t)planes & 15u) != 0) return EMU_STATUS_INVALID_VALUE;
+    emu::DeviceInfo dev;
+    if (!emu::api_current_device(dev)) return EMU_STATUS_NOT_SUPPORTED;
+    return from_hip(emu::launch_presplit_gated(W, ldw, F, K, bands_of(mode), static_cast<uint16_t*>(planes),
+                                               stream_of(stream)));
 }
 
 emu_status_t emu_gated_backward(int64_t M, int64_t F, const float* dh, int64_t lddh, const float* Z, int64_t ldz,

@@ -56,6 +56,13 @@ hipError_t launch_column_join(const float* part, int64_t parts, int64_t stride, 
 // C from the product t (M x N, gated: M x 2N; ldt).
 hipError_t launch_epilogue(int64_t M, int64_t N, const float* t, int64_t ldt, const BlockEpilogue& ep,
                            hipStream_t s);
+// The epilogue of a K-split launch's split tiles (emu_launch.h): t is the sum of
+// the segments' partial tiles, in order.  N: columns of C.
+hipError_t launch_split_epilogue(const float* parts, int segs, int nsplit, int split_from, int tiles_n, int tile_m,
+                                 int64_t M, int64_t N, const BlockEpilogue& ep, hipStream_t s);
+// A (M x K, lda) to dst (rows of ldd floats).
+hipError_t launch_copy_rows(int64_t M, int64_t K, const float* A, int64_t lda, float* dst, int64_t ldd,
+                            hipStream_t s);
 hipError_t launch_act_backward(int64_t rows, int64_t cols, const float* dy, int64_t lddy, const float* z,
                                int64_t ldz, int act, float* dz, int64_t lddz, hipStream_t s);
 hipError_t launch_act_backward2(int64_t rows, int64_t cols, const float* v, int64_t ldv, const float* dy,

@@ -22,7 +22,12 @@ struct GemmArgs {
     // op(B) already split by launch_presplit_b (same N, K and plane count),
     // or null: the call splits op(B) into its workspace
     const uint16_t* Bplanes = nullptr;
+    // the 16-byte groups of A's rows lie inside the rows' leading dimension
+    // even where K is not a multiple of 4 (what they hold past K is ignored)
+    bool a_whole_groups = false;
 };
+
+struct BlockEpilogue;   // emu_block_launch.h
 
 struct DeviceInfo {
     int device;          // HIP device index
@@ -48,8 +53,13 @@ bool fused_a_path(const GemmArgs& g);
 // used in stream order only.
 size_t gemm_bf16_workspace_bytes(const GemmArgs& g, int nbands, int ksplit, int tile_m,
                                  int64_t split_from);
+// ep: the epilogue of a transformer-block operator instead of C = alpha t +
+// beta C + bias (then C, alpha, beta and bias of g are not used, the A path
+// must be the fused one, and a gated epilogue's planes are those of
+// launch_presplit_gated); null: the plain one.
 hipError_t launch_gemm_bf16(const GemmArgs& g, int nbands, int ksplit, int64_t split_from, int tile_m,
-                            const DeviceInfo& dev, void* workspace, hipStream_t stream);
+                            const DeviceInfo& dev, void* workspace, hipStream_t stream,
+                            const BlockEpilogue* ep = nullptr);
 // The native FP32 GEMM: its device workspace (bytes, a multiple of 256; 0
 // when the call takes the kernel that needs none) and the launch with it
 // (`workspace` 16-byte aligned, used in stream order only).
@@ -63,6 +73,11 @@ hipError_t launch_gemm_native_f32(const GemmArgs& g, const DeviceInfo& dev, void
 size_t gemm_bf16_planes_bytes(int64_t N, int64_t K, int nbands);
 hipError_t launch_presplit_b(const float* B, int64_t ldb, bool trans_b, int64_t N, int64_t K,
                              int nbands, uint16_t* planes, hipStream_t stream);
+// The planes of a gated projection's weight (2 F x K, gate rows above up rows)
+// in the order its epilogue takes: emu_gemm_pp.h, gated_plane_row.  Their size
+// is that of a K x 2 F op(B).
+hipError_t launch_presplit_gated(const float* W, int64_t ldw, int64_t F, int64_t K, int nbands,
+                                 uint16_t* planes, hipStream_t stream);
 // C = beta * C + bias over M x N (C not read when beta == 0; bias may be null).
 hipError_t launch_scale_c(int64_t M, int64_t N, float beta, float* C, int64_t ldc,
                           const float* bias, hipStream_t stream);
