@@ -67,6 +67,11 @@ _SIGNATURES = {
     "emu_gated_backward2": [_i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _int, _vp, _i64, _vp, _i64, _vp],
     "emu_wgrad_workspace": [_i64, _i64, _i64, _psize],
     "emu_wgrad": [_i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _size, _vp],
+    "emu_wgrad_act": [_i64, _i64, _i64, _vp, _i64, _vp, _i64, _int, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _size,
+                      _vp],
+    "emu_wgrad_gated_workspace": [_i64, _i64, _i64, _psize],
+    "emu_wgrad_gated": [_i64, _i64, _i64, _vp, _i64, _vp, _i64, _int, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _size,
+                        _vp],
 }
 EXPORTS = tuple(_SIGNATURES)
 for _name, _types in _SIGNATURES.items():
@@ -229,6 +234,28 @@ def _wgrad(dz, x, want_db):
         _done(_lib.emu_wgrad(rows, M, N, _ptr(dz), _ld(dz), _ptr(x), _ld(x), _ptr(dw), max(N, 1), _ptr(db), _ptr(ws),
                              0 if ws is None else ws.numel(), stream), "emu_wgrad")
     return dw, db
+
+
+def _wgrad_from(dy, z, act, x, want_db, gated):
+    """(dz, dz^T x, column sums of dz or None), dz the activation's (gated:
+    the gated product's) backward pass."""
+    rows, M = dy.shape
+    N, wide = x.shape[1], z.shape[1]
+    dz, dw = _empty(rows, wide, dy), _empty(wide, N, dy)
+    db = torch.empty(wide, dtype=torch.float32, device=dy.device) if want_db else None
+    asked, run = (_lib.emu_wgrad_gated_workspace, _lib.emu_wgrad_gated) if gated \
+        else (_lib.emu_wgrad_workspace, _lib.emu_wgrad_act)
+    with _on(dy.device) as stream:
+        ws = _workspace(_asked_bytes(asked, rows, M, N), dy.device)
+        _done(run(rows, M, N, _ptr(dy), _ld(dy), _ptr(z), _ld(z), act, _ptr(dz), max(wide, 1), _ptr(x), _ld(x),
+                  _ptr(dw), max(N, 1), _ptr(db), _ptr(ws), 0 if ws is None else ws.numel(), stream), run.__name__)
+    return dz, dw, db
+
+
+def _fuse_act(x):
+    """Whether the activation's backward pass runs inside the weight gradient:
+    every 128 columns of x repeat it, which pays for up to two such tiles."""
+    return x.shape[-1] <= 256
 
 
 class _GatedPlanes:
@@ -444,6 +471,18 @@ class _GatedBackward(torch.autograd.Function):
         return gdh, gz, None
 
 
+def _first_order_grads(ctx, gy, z, x, weight, gated):
+    """(dx, dW, db) where dW is asked for and nothing is differentiated again:
+    the activation's backward pass runs inside the weight gradient's."""
+    K = weight.shape[1]
+    g2 = _rows(gy, gy.shape[-1])
+    dz, gw, gb = _wgrad_from(g2, z, ctx.act, _rows(x, K), ctx.has_bias and ctx.needs_input_grad[2], gated)
+    gx = None
+    if ctx.needs_input_grad[0]:
+        gx = _Product.apply(dz, weight, False, ctx.mode, ctx.caches).reshape(ctx.x_shape)
+    return gx, gw, gb
+
+
 def _layer_grads(ctx, dz, x, weight, has_bias):
     """(dx, dW, db) of z = x W^T + b from dz, each where asked for."""
     gx = gw = gb = None
@@ -484,6 +523,9 @@ class _LinearAct(torch.autograd.Function):
     def backward(ctx, gy, gz):
         x, weight, z = ctx.saved_tensors
         N = weight.shape[0]
+        if gz is None and z is not None and ctx.needs_input_grad[1] and not torch.is_grad_enabled() and _fuse_act(x):
+            gx, gw, gb = _first_order_grads(ctx, gy, z, x, weight, False)
+            return gx, gw, gb, gy if ctx.needs_input_grad[3] else None, None, None, None
         dz = None
         if gy is not None:
             g2 = gy.reshape(math.prod(ctx.x_shape[:-1]), N)
@@ -554,6 +596,8 @@ class _GatedLinear(torch.autograd.Function):
     @staticmethod
     def backward(ctx, gh, gz):
         x, weight, z = ctx.saved_tensors
+        if gz is None and ctx.needs_input_grad[1] and not torch.is_grad_enabled() and _fuse_act(x):
+            return (*_first_order_grads(ctx, gh, z, x, weight, True), None, None, None)
         dz = None
         if gh is not None:
             dz = _GatedBackward.apply(gh.reshape(z.shape[0], z.shape[1] // 2), z, ctx.act)

@@ -178,8 +178,10 @@ __global__ __launch_bounds__(256) void gated_backward_kernel(int64_t M, int F, c
             f32x4_t dg, du;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                dg[e] = d[e] * u[e] * act_slope<ACT, 1>(g[e]);
-                du[e] = d[e] * act_value<ACT>(g[e]);
+                float a, s;
+                act_both<ACT>(g[e], a, s);
+                dg[e] = d[e] * u[e] * s;
+                du[e] = d[e] * a;
             }
             store4(dZ + r * lddz, c, F, dg);
             store4(dZ + r * lddz + F, c, F, du);

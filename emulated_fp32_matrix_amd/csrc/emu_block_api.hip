@@ -410,35 +410,81 @@ emu_status_t emu_gated_backward2(int64_t M, int64_t F, const float* V, int64_t l
 emu_status_t emu_wgrad_workspace(int64_t rows, int64_t M, int64_t N, size_t* bytes)
 {
     if (rows < 0 || M < 0 || N < 0 || bytes == nullptr) return EMU_STATUS_INVALID_VALUE;
-    *bytes = rows == 0 || M == 0 ? 0 : emu::wgrad_workspace(rows, M, N);
+    *bytes = rows == 0 || M == 0 ? 0 : emu::wgrad_workspace(rows, M, N, false);
     return EMU_STATUS_SUCCESS;
 }
 
-emu_status_t emu_wgrad(int64_t rows, int64_t M, int64_t N, const float* dZ, int64_t lddz, const float* X,
-                       int64_t ldx, float* dW, int64_t lddw, float* db, void* workspace, size_t workspace_bytes,
-                       void* stream)
+emu_status_t emu_wgrad_gated_workspace(int64_t rows, int64_t F, int64_t N, size_t* bytes)
 {
-    if (rows < 0 || M < 0 || N < 0 || bad_array(dZ, rows, M, lddz) || bad_array(X, rows, N, ldx) ||
-        bad_array(dW, M, N, lddw))
+    if (rows < 0 || F < 0 || N < 0 || bytes == nullptr) return EMU_STATUS_INVALID_VALUE;
+    *bytes = rows == 0 || F == 0 ? 0 : emu::wgrad_workspace(rows, F, N, true);
+    return EMU_STATUS_SUCCESS;
+}
+
+}  // extern "C"
+
+namespace {
+
+emu_status_t wgrad(int64_t rows, int64_t M, int64_t N, const emu::WgradSource& src, const float* X, int64_t ldx,
+                   float* dW, int64_t lddw, float* db, void* workspace, size_t workspace_bytes, void* stream)
+{
+    const int64_t out = src.gated ? 2 * M : M;
+    if (rows < 0 || M < 0 || N < 0 || bad_array(X, rows, N, ldx) || bad_array(dW, out, N, lddw))
         return EMU_STATUS_INVALID_VALUE;
-    if (lddz > emu::kWgradMaxLd || ldx > emu::kWgradMaxLd) return EMU_STATUS_NOT_SUPPORTED;
-    if (M == 0 || (N == 0 && db == nullptr)) return EMU_STATUS_SUCCESS;
-    if (rows > 0 && bad_workspace(workspace, workspace_bytes, emu::wgrad_workspace(rows, M, N)))
+    for (int64_t ld : {src.ldz, src.ldy, src.ldd, ldx})
+        if (ld > emu::kWgradMaxLd) return EMU_STATUS_NOT_SUPPORTED;
+    if (M == 0 || (N == 0 && db == nullptr && src.dZ == nullptr)) return EMU_STATUS_SUCCESS;
+    if (rows > 0 && bad_workspace(workspace, workspace_bytes, emu::wgrad_workspace(rows, M, N, src.gated)))
         return EMU_STATUS_INVALID_VALUE;
     emu::DeviceInfo dev;
     if (!emu::api_current_device(dev)) return EMU_STATUS_NOT_SUPPORTED;
     hipStream_t s = stream_of(stream);
     if (rows == 0) {
         hipError_t e = hipSuccess;
-        if (lddw == N || M == 1) {
-            e = emu::launch_zero(dW, M * N, s);
+        if (lddw == N || out == 1) {
+            e = emu::launch_zero(dW, out * N, s);
         } else {
-            for (int64_t m = 0; m < M && e == hipSuccess; ++m) e = emu::launch_zero(dW + m * lddw, N, s);
+            for (int64_t m = 0; m < out && e == hipSuccess; ++m) e = emu::launch_zero(dW + m * lddw, N, s);
         }
-        if (e == hipSuccess) e = emu::launch_zero(db, M, s);
+        if (e == hipSuccess) e = emu::launch_zero(db, out, s);
         return from_hip(e);
     }
-    return from_hip(emu::launch_wgrad(rows, M, N, dZ, lddz, X, ldx, dW, lddw, db, workspace, s));
+    return from_hip(emu::launch_wgrad(rows, M, N, src, X, ldx, dW, lddw, db, workspace, s));
+}
+
+}  // namespace
+
+extern "C" {
+
+emu_status_t emu_wgrad(int64_t rows, int64_t M, int64_t N, const float* dZ, int64_t lddz, const float* X,
+                       int64_t ldx, float* dW, int64_t lddw, float* db, void* workspace, size_t workspace_bytes,
+                       void* stream)
+{
+    if (bad_array(dZ, rows, M, lddz)) return EMU_STATUS_INVALID_VALUE;
+    emu::WgradSource src{dZ, lddz};
+    return wgrad(rows, M, N, src, X, ldx, dW, lddw, db, workspace, workspace_bytes, stream);
+}
+
+emu_status_t emu_wgrad_act(int64_t rows, int64_t M, int64_t N, const float* dY, int64_t lddy, const float* Z,
+                           int64_t ldz, emu_act_t act, float* dZ, int64_t lddz, const float* X, int64_t ldx,
+                           float* dW, int64_t lddw, float* db, void* workspace, size_t workspace_bytes, void* stream)
+{
+    if (!valid_act(act) || bad_array(dY, rows, M, lddy) || bad_array(Z, rows, M, ldz) || bad_array(dZ, rows, M, lddz))
+        return EMU_STATUS_INVALID_VALUE;
+    emu::WgradSource src{Z, ldz, dY, lddy, dZ, lddz, (int)act, false};
+    return wgrad(rows, M, N, src, X, ldx, dW, lddw, db, workspace, workspace_bytes, stream);
+}
+
+emu_status_t emu_wgrad_gated(int64_t rows, int64_t F, int64_t N, const float* dH, int64_t lddh, const float* Z,
+                             int64_t ldz, emu_act_t act, float* dZ, int64_t lddz, const float* X, int64_t ldx,
+                             float* dW, int64_t lddw, float* db, void* workspace, size_t workspace_bytes,
+                             void* stream)
+{
+    if (!valid_act(act) || F > kMaxCols || bad_array(dH, rows, F, lddh) || bad_array(Z, rows, 2 * F, ldz) ||
+        bad_array(dZ, rows, 2 * F, lddz))
+        return EMU_STATUS_INVALID_VALUE;
+    emu::WgradSource src{Z, ldz, dH, lddh, dZ, lddz, (int)act, true};
+    return wgrad(rows, F, N, src, X, ldx, dW, lddw, db, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

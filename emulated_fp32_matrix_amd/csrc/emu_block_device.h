@@ -89,8 +89,54 @@ __device__ __forceinline__ float exp_f32(float x)
 
 __device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.0f + exp_f32(-z)); }
 
-__device__ __forceinline__ float normal_cdf(float z) { return 0.5f * erfcf(z * -0.707106769084930419921875f); }
-__device__ __forceinline__ float normal_pdf(float z) { return 0.398942291736602783203125f * exp_f32(-0.5f * z * z); }
+// s = sigmoid(z) and t = 1 - s, both without cancellation.
+__device__ __forceinline__ void sigmoid_pair(float z, float& s, float& t)
+{
+    const float e = exp_f32(-z);
+    s = __builtin_amdgcn_rcpf(1.0f + e);
+    t = s < 0.5f ? 1.0f - s : e * s;   // (e <= 1 in the second)
+}
+
+// The normal distribution's density and cumulative function.  For z <= 0
+//   Phi(z) = e^(-z^2/2) G(|z|),  G(y) = erfcx(y / sqrt 2) / 2,
+// and Phi(z) = 1 - Phi(-z) above, so that both tails keep their relative
+// accuracy.  G is smooth in t = 1 / (1 + 0.35 y): t times a polynomial of
+// degree 8, fitted here to the least relative error over y <= 14 (3.2e-8; 5.3
+// units of 2^-24 with FP32 roundings), beyond which the exponential is zero.
+__device__ __forceinline__ void normal(float z, float& cdf, float& pdf)
+{
+    const float e = exp_f32(-0.5f * z * z);
+    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.35f, __builtin_fabsf(z), 1.0f));
+    float p = -0.029145918786525726f;
+    p = __builtin_fmaf(p, t, 0.14397163689136505f);
+    p = __builtin_fmaf(p, t, -0.2557141184806824f);
+    p = __builtin_fmaf(p, t, 0.15917402505874634f);
+    p = __builtin_fmaf(p, t, -0.023109741508960724f);
+    p = __builtin_fmaf(p, t, 0.10550796240568161f);
+    p = __builtin_fmaf(p, t, 0.11983288079500198f);
+    p = __builtin_fmaf(p, t, 0.13986186683177948f);
+    p = __builtin_fmaf(p, t, 0.13962140679359436f);
+    const float low = p * t * e;
+    cdf = z < 0.0f ? low : 1.0f - low;
+    pdf = 0.398942291736602783203125f * e;
+}
+
+// tanh z: its odd series' place is taken below |z| = 0.35 by z times a
+// polynomial in z^2 (least relative error 4e-10), above by (1 - e) / (1 + e)
+// with e = e^(-2 |z|), where 1 - e loses one bit at most.  NaN kept.
+__device__ __forceinline__ float tanh_f32(float z)
+{
+    const float a = __builtin_fabsf(z);
+    const float e = exp_f32(-2.0f * a);
+    const float big = (1.0f - e) * __builtin_amdgcn_rcpf(1.0f + e);
+    const float q = z * z;
+    float p = 0.019361333921551704f;
+    p = __builtin_fmaf(p, q, -0.053706347942352295f);
+    p = __builtin_fmaf(p, q, 0.13332201540470123f);
+    p = __builtin_fmaf(p, q, -0.33333316445350647f);
+    p = __builtin_fmaf(p * q, z, z);
+    return a >= 0.35f ? __builtin_copysignf(big, z) : p;
+}
 
 constexpr float kGeluC = 0.797884583473205566406f;   // sqrt(2 / pi)
 constexpr float kGeluA = 0.044715f;
@@ -109,13 +155,17 @@ __device__ __forceinline__ float act_value(float z)
     if constexpr (ACT == EMU_ACT_IDENTITY) return z;
     if constexpr (ACT == EMU_ACT_RELU) return z <= 0.0f ? 0.0f : z;   // (NaN kept)
     if constexpr (ACT == EMU_ACT_SILU) return z * sigmoid(z);
-    if constexpr (ACT == EMU_ACT_GELU) return z * normal_cdf(z);
+    if constexpr (ACT == EMU_ACT_GELU) {
+        float c, d;
+        normal(z, c, d);
+        return z * c;
+    }
     if constexpr (ACT == EMU_ACT_GELU_TANH) {
         // (1 + tanh q) / 2 = sigmoid(2 q)
         const float q2 = 2.0f * kGeluC * (z + kGeluA * z * z * z);
         return z * sigmoid(q2);
     }
-    if constexpr (ACT == EMU_ACT_TANH) return tanhf(z);
+    if constexpr (ACT == EMU_ACT_TANH) return tanh_f32(z);
     return z;
 }
 
@@ -127,16 +177,17 @@ __device__ __forceinline__ float act_slope(float z)
     if constexpr (ACT == EMU_ACT_IDENTITY) return D == 1 ? 1.0f : 0.0f;
     if constexpr (ACT == EMU_ACT_RELU) return D == 2 || z <= 0.0f ? 0.0f : 1.0f;
     if constexpr (ACT == EMU_ACT_SILU) {
-        z = limit_z(z, 88.0f);
-        const float s = sigmoid(z);
-        const float t = sigmoid(-z);   // 1 - s without its cancellation
+        float s, t;
+        sigmoid_pair(z, s, t);   // (s t is 0 where z t overflows)
         if constexpr (D == 1) return s * __builtin_fmaf(z, t, 1.0f);
         return s * t * __builtin_fmaf(z, t - s, 2.0f);
     }
     if constexpr (ACT == EMU_ACT_GELU) {
-        z = limit_z(z, 16.0f);
-        if constexpr (D == 1) return __builtin_fmaf(z, normal_pdf(z), normal_cdf(z));
-        return normal_pdf(z) * __builtin_fmaf(-z, z, 2.0f);
+        if constexpr (D == 2) z = limit_z(z, 16.0f);
+        float c, d;
+        normal(z, c, d);
+        if constexpr (D == 1) return __builtin_fmaf(z, d, c);
+        return d * __builtin_fmaf(-z, z, 2.0f);
     }
     if constexpr (ACT == EMU_ACT_GELU_TANH) {
         // f = z s, s = sigmoid(p), p = 2 c (z + a z^3): f' = s + z s t p',
@@ -144,7 +195,8 @@ __device__ __forceinline__ float act_slope(float z)
         z = limit_z(z, 16.0f);
         const float p = 2.0f * kGeluC * (z + kGeluA * z * z * z);
         const float p1 = 2.0f * kGeluC * __builtin_fmaf(3.0f * kGeluA * z, z, 1.0f);
-        const float s = sigmoid(p), t = sigmoid(-p);
+        float s, t;
+        sigmoid_pair(p, s, t);
         if constexpr (D == 1) return __builtin_fmaf(z * p1, s * t, s);
         const float p2 = 12.0f * kGeluC * kGeluA * z;
         return s * t * __builtin_fmaf(z, __builtin_fmaf((t - s) * p1, p1, p2), 2.0f * p1);
@@ -152,11 +204,41 @@ __device__ __forceinline__ float act_slope(float z)
     if constexpr (ACT == EMU_ACT_TANH) {
         // 1 - tanh^2 = 4 s t with s = sigmoid(2 z), without the cancellation
         z = limit_z(z, 44.0f);
-        const float u = 4.0f * sigmoid(2.0f * z) * sigmoid(-2.0f * z);
+        float s, t;
+        sigmoid_pair(2.0f * z, s, t);
+        const float u = 4.0f * s * t;
         if constexpr (D == 1) return z != z ? z : u;   // (the sigmoids drop a NaN)
-        return -2.0f * tanhf(z) * u;
+        return -2.0f * tanh_f32(z) * u;
     }
     return 0.0f;
+}
+
+// Value and first derivative together.
+template <int ACT>
+__device__ __forceinline__ void act_both(float z, float& v, float& d)
+{
+    if constexpr (ACT == EMU_ACT_SILU) {
+        float s, t;
+        sigmoid_pair(z, s, t);
+        v = z * s;
+        d = s * __builtin_fmaf(z, t, 1.0f);
+    } else if constexpr (ACT == EMU_ACT_GELU) {
+        float c, f;
+        normal(z, c, f);
+        v = z * c;
+        d = __builtin_fmaf(z, f, c);
+    } else if constexpr (ACT == EMU_ACT_GELU_TANH) {
+        const float l = limit_z(z, 16.0f);
+        const float p = 2.0f * kGeluC * (l + kGeluA * l * l * l);
+        const float p1 = 2.0f * kGeluC * __builtin_fmaf(3.0f * kGeluA * l, l, 1.0f);
+        float s, t;
+        sigmoid_pair(p, s, t);
+        v = z * s;
+        d = __builtin_fmaf(l * p1, s * t, s);
+    } else {
+        v = act_value<ACT>(z);
+        d = act_slope<ACT, 1>(z);
+    }
 }
 
 // f with the activation as a compile-time constant: f.operator()<ACT>().

@@ -82,8 +82,21 @@ hipError_t launch_rows_gemm(bool trans_b, int64_t M, int64_t N, int64_t K, const
 // Leading dimensions of the weight-gradient product: its 32-row slabs are
 // addressed with 32-bit byte offsets.
 constexpr int64_t kWgradMaxLd = ((int64_t)1 << 31) / (4 * 32) - 128;
-size_t wgrad_workspace(int64_t rows, int64_t M, int64_t N);
-hipError_t launch_wgrad(int64_t rows, int64_t M, int64_t N, const float* dZ, int64_t lddz, const float* X,
-                        int64_t ldx, float* dW, int64_t lddw, float* db, void* ws, hipStream_t s);
+// dZ of the weight-gradient product: an array (Z, with dY null), or made from
+// dY and the pre-activations Z and written to dZ (gated: Z and dZ hold 2 M
+// columns, dY M).
+struct WgradSource {
+    const float* Z;
+    int64_t ldz;
+    const float* dY = nullptr;
+    int64_t ldy = 0;
+    float* dZ = nullptr;
+    int64_t ldd = 0;
+    int act = 0;
+    bool gated = false;
+};
+size_t wgrad_workspace(int64_t rows, int64_t M, int64_t N, bool gated);
+hipError_t launch_wgrad(int64_t rows, int64_t M, int64_t N, const WgradSource& src, const float* X, int64_t ldx,
+                        float* dW, int64_t lddw, float* db, void* ws, hipStream_t s);
 
 }  // namespace emu

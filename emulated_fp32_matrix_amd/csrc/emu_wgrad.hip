@@ -35,11 +35,19 @@ namespace {
 
 constexpr int SLAB = BK * TILE;   // floats of one operand's slab
 
+// Where the rows of dZ come from: memory (WG_PLAIN), or an activation's
+// backward pass that runs on the way to LDS and also writes dZ for the
+// input-gradient product: dZ = dY act'(Z) (WG_ACT), or with Z = [g | u]
+// dZ = [dY u act'(g) | dY act(g)] (WG_GATED).
+enum { WG_PLAIN = 0, WG_ACT = 1, WG_GATED = 2 };
+
 struct WgradArgs {
-    const float* Z;
+    const float* Z;        // WG_PLAIN: dZ; else the pre-activations
     const float* X;
-    int64_t ldz, ldx, rows;
-    int M, N;
+    const float* Y;        // WG_ACT, WG_GATED: dY
+    float* dZ;             // and the result
+    int64_t ldz, ldx, ldy, ldd, rows;
+    int M, N;              // columns of dZ (WG_GATED: of each half) and of X
     int tiles_n, tiles;
     int segs, seg_steps;   // segments of seg_steps slabs
     float* out;            // dW, or the partial results: seg * pstride + m * ldo + n
@@ -48,8 +56,15 @@ struct WgradArgs {
     int64_t bstride;
 };
 
+template <int SRC, int ACT>
 __global__ __launch_bounds__(256, 2) void wgrad_kernel(WgradArgs p)
 {
+    // columns of dZ per tile and half, 16-byte groups of a row, and copies of
+    // a slab per thread
+    constexpr int TW = SRC == WG_GATED ? TILE / 2 : TILE;
+    constexpr int PER_ROW = TW / 4, ROWS = 256 / PER_ROW, COPIES = BK / ROWS;
+    constexpr int HALVES = SRC == WG_GATED ? 2 : 1;
+    constexpr int READS = SRC == WG_PLAIN ? 1 : SRC == WG_ACT ? 2 : 3;   // arrays behind dZ
     __shared__ __attribute__((aligned(16))) float smZ[2][SLAB];
     __shared__ __attribute__((aligned(16))) float smX[2][SLAB];
 
@@ -62,42 +77,90 @@ __global__ __launch_bounds__(256, 2) void wgrad_kernel(WgradArgs p)
     const int seg = item / p.tiles;
     const int tile = item - seg * p.tiles;
     const int tm = tile / p.tiles_n, tn = tile - tm * p.tiles_n;
-    const int m0 = tm * TILE, n0 = tn * TILE;
+    const int m0 = tm * TW, n0 = tn * TILE;
     const int64_t k0 = (int64_t)seg * p.seg_steps * BK;
     int64_t kend = k0 + (int64_t)p.seg_steps * BK;
     if (kend > p.rows) kend = p.rows;
     const int steps = (int)((kend - k0 + BK - 1) / BK);
 
-    // Thread t copies columns 4 (t % 32) .. +3 of rows t / 32 + 8 r of a slab.
-    // The buffer descriptors end with the segment's last row, so rows past
-    // it read as zeros; columns past M (N) read what follows in memory, or
-    // zeros, and only feed outputs that are not stored.
-    const int cr = t >> 5, cc = (t & 31) * 4;
+    // Thread t copies columns 4 (t % PER_ROW) .. +3 of rows t / PER_ROW + ROWS
+    // r of a slab of dZ (and of what it is made of), and likewise with 32
+    // groups per row of X.  The buffer descriptors end with the segment's
+    // last row, so rows past it read as zeros (and are not written); columns
+    // past M (N) read what follows in memory, or zeros, and only feed outputs
+    // that are not stored.
+    const int cr = t / PER_ROW, cc = (t % PER_ROW) * 4;
+    const int xr = t >> 5, xc = (t & 31) * 4;
     const int mleft = p.M - m0, nleft = p.N - n0;
-    const float* zbase = p.Z + k0 * p.ldz + m0;
-    const float* xbase = p.X + k0 * p.ldx + n0;
-    const uint32_t zoff = (uint32_t)(cr * p.ldz + cc) * 4, xoff = (uint32_t)(cr * p.ldx + cc) * 4;
-    const uint32_t zrow = (uint32_t)p.ldz * 32, xrow = (uint32_t)p.ldx * 32;   // bytes of 8 rows
-    u32x4_t rz[4], rx[4];
-    __amdgpu_buffer_rsrc_t zr, xr;   // the slab that is loaded next
-    auto aim = [&](int step) __attribute__((always_inline)) {
+    const int zcols = SRC == WG_GATED ? 2 * p.M - m0 : mleft;   // from m0 to the end of Z's row
+    u32x4_t rz[READS][COPIES], rx[4];
+    __amdgpu_buffer_rsrc_t bz, bx, by, bd;   // the slab that is loaded next; bd: that is written now
+    auto rows_from = [&](int step) __attribute__((always_inline)) {
         const int64_t left = kend - k0 - (int64_t)step * BK;
-        const int rows = left < BK ? (int)left : BK;   // (none left: an empty buffer, zeros)
-        zr = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(zbase + (int64_t)step * BK * p.ldz), (short)0,
-                                               rows > 0 ? (int)((rows - 1) * p.ldz + mleft) * 4 : 0, 0x00020000);
-        xr = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(xbase + (int64_t)step * BK * p.ldx), (short)0,
-                                               rows > 0 && nleft > 0 ? (int)((rows - 1) * p.ldx + nleft) * 4 : 0,
-                                               0x00020000);   // (N = 0: X may be null)
+        return left < BK ? (int)left : BK;   // (none left: an empty buffer, zeros)
     };
-    auto load = [&](int r) __attribute__((always_inline)) {
-        rz[r] = __builtin_amdgcn_raw_buffer_load_b128(zr, zoff + r * zrow, 0, 0);
-        rx[r] = __builtin_amdgcn_raw_buffer_load_b128(xr, xoff + r * xrow, 0, 0);
+    auto buffer = [&](const float* base, int64_t ld, int step, int cols) __attribute__((always_inline)) {
+        const int rows = rows_from(step);
+        // (cols 0: N = 0, X may be null)
+        return __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(base + (k0 + (int64_t)step * BK) * ld), (short)0,
+                                                 rows > 0 && cols > 0 ? (int)((rows - 1) * ld + cols) * 4 : 0,
+                                                 0x00020000);
     };
-    const bool sums = p.db != nullptr && tn == 0;
-    f32x4_t bsum = {};   // column sums of the rows this thread copies
-    auto store = [&](int b, int r) __attribute__((always_inline)) {
-        *reinterpret_cast<u32x4_t*>(&smZ[b][(cr + 8 * r) * TILE + cc]) = rz[r];
-        *reinterpret_cast<u32x4_t*>(&smX[b][(cr + 8 * r) * TILE + cc]) = rx[r];
+    auto aim = [&](int step) __attribute__((always_inline)) {
+        bz = buffer(p.Z + m0, p.ldz, step, zcols);
+        bx = buffer(p.X + n0, p.ldx, step, nleft);
+        if (SRC != WG_PLAIN) by = buffer(p.Y + m0, p.ldy, step, mleft);
+    };
+    auto offset = [&](int64_t ld, int r) __attribute__((always_inline)) {
+        return (uint32_t)((cr + ROWS * r) * ld + cc) * 4;
+    };
+    auto load_z = [&](int r) __attribute__((always_inline)) {
+        rz[0][r] = __builtin_amdgcn_raw_buffer_load_b128(bz, offset(p.ldz, r), 0, 0);
+        if constexpr (SRC != WG_PLAIN) rz[1][r] = __builtin_amdgcn_raw_buffer_load_b128(by, offset(p.ldy, r), 0, 0);
+        if constexpr (SRC == WG_GATED)
+            rz[2][r] = __builtin_amdgcn_raw_buffer_load_b128(bz, offset(p.ldz, r) + (uint32_t)p.M * 4, 0, 0);
+    };
+    auto load_x = [&](int r) __attribute__((always_inline)) {
+        rx[r] = __builtin_amdgcn_raw_buffer_load_b128(bx, (uint32_t)((xr + 8 * r) * p.ldx + xc) * 4, 0, 0);
+    };
+    const bool first_n = tn == 0;
+    const bool sums = p.db != nullptr && first_n;
+    f32x4_t bsum[HALVES] = {};   // column sums of the rows this thread copies
+    f32x4_t dz[HALVES];          // the copy being made
+    auto value = [&](const u32x4_t& v, int e) __attribute__((always_inline)) { return __uint_as_float(v[e]); };
+    auto make = [&](int r, int e) __attribute__((always_inline)) {
+        if constexpr (SRC == WG_PLAIN) {
+            dz[0][e] = value(rz[0][r], e);
+        } else if constexpr (SRC == WG_ACT) {
+            dz[0][e] = value(rz[1][r], e) * act_slope<ACT, 1>(value(rz[0][r], e));
+        } else {
+            float a, d;
+            act_both<ACT>(value(rz[0][r], e), a, d);
+            const float dy = value(rz[1][r], e);
+            dz[0][e] = dy * value(rz[2][r], e) * d;
+            dz[HALVES - 1][e] = dy * a;
+        }
+    };
+    auto put = [&](int b, int r) __attribute__((always_inline)) {
+#pragma unroll
+        for (int h = 0; h < HALVES; ++h) {
+            *reinterpret_cast<f32x4_t*>(&smZ[b][(cr + ROWS * r) * TILE + h * TW + cc]) = dz[h];
+            if (sums) bsum[h] = bsum[h] + dz[h];
+            if (SRC != WG_PLAIN && first_n) {
+                const uint32_t off = offset(p.ldd, r) + (uint32_t)(h * p.M) * 4;
+                if (cc + 4 <= mleft) {
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, dz[h]), bd, off, 0, 0);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (cc + e < mleft)
+                            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(dz[h][e]), bd, off + 4 * e, 0, 0);
+                }
+            }
+        }
+    };
+    auto put_x = [&](int b, int r) __attribute__((always_inline)) {
+        *reinterpret_cast<u32x4_t*>(&smX[b][(xr + 8 * r) * TILE + xc]) = rx[r];
     };
 
     f32x16_t acc[2][2];
@@ -114,21 +177,29 @@ __global__ __launch_bounds__(256, 2) void wgrad_kernel(WgradArgs p)
         return *reinterpret_cast<const f32x2_t*>(&sm[k * TILE + f]);
     };
     // Slab s is in LDS buffer s % 2.  During its step slab s + 1 goes to the
-    // other buffer from the registers it was read to during step s - 1, and
-    // slab s + 2 is requested into them, a quarter at a time between the
-    // products, so that the matrix unit never waits for a wave's copies.
+    // other buffer from the registers it was read to during step s - 1 (with
+    // the activation's backward pass on the way, one element of a copy per k
+    // pair), and slab s + 2 is requested into them, a copy at a time between
+    // the products, so that the matrix unit never waits for a wave's copies.
     aim(0);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) load(r);
+    for (int r = 0; r < COPIES; ++r) load_z(r);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) load_x(r);
     aim(1);
-    f32x4_t part[2] = {};
+    if (SRC != WG_PLAIN) bd = buffer(p.dZ + m0, p.ldd, 0, zcols);
+#pragma unroll
+    for (int r = 0; r < COPIES; ++r) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) make(r, e);
+        put(0, r);
+        load_z(r);
+    }
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-        store(0, r);
-        part[r & 1] = part[r & 1] + __builtin_bit_cast(f32x4_t, rz[r]);
-        load(r);
+        put_x(0, r);
+        load_x(r);
     }
-    bsum = part[0] + part[1];
     wait_lgkmcnt0();
     __builtin_amdgcn_s_barrier();
     for (int s = 0; s < steps; ++s) {
@@ -140,21 +211,23 @@ __global__ __launch_bounds__(256, 2) void wgrad_kernel(WgradArgs p)
         a[0] = read(sz, fz, 0);
         c[0] = read(sx, fx, 0);
         aim(s + 2);
-        part[0] = part[1] = f32x4_t{};
+        if (SRC != WG_PLAIN) bd = buffer(p.dZ + m0, p.ldd, s + 1, zcols);
 #pragma unroll
         for (int k = 0; k < BK / 2; ++k) {
             if (k + 1 < BK / 2) {
                 a[(k + 1) & 1] = read(sz, fz, 2 * k + 2);
                 c[(k + 1) & 1] = read(sx, fx, 2 * k + 2);
             }
-            if (k % 3 == 2 && k / 3 < 4) {
-                const int r = k / 3;
-                store(b ^ 1, r);
-                if (sums) part[r & 1] = part[r & 1] + __builtin_bit_cast(f32x4_t, rz[r]);
-                load(r);
+            if (k % 4 == 2) {
+                put_x(b ^ 1, k / 4);
+                load_x(k / 4);
             }
-            if (k == BK / 2 - 1) bsum = bsum + (part[0] + part[1]);
+            if (k % 4 == 0 && k > 0 && k / 4 <= COPIES) {
+                put(b ^ 1, k / 4 - 1);
+                load_z(k / 4 - 1);
+            }
             __builtin_amdgcn_sched_barrier(0);
+            if (k / 4 < COPIES) make(k / 4, k % 4);
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -162,7 +235,19 @@ __global__ __launch_bounds__(256, 2) void wgrad_kernel(WgradArgs p)
                     // X first: lane l then holds one row of dW and four
                     // columns per register group
                     acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(c[k & 1][j], a[k & 1][i], acc[i][j], 0, 0, 0);
+            if (SRC != WG_PLAIN && k / 4 < COPIES) {
+                // the activation's vector work between the products
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x402, 8, 0);
+                }
+            }
             __builtin_amdgcn_sched_barrier(0);
+        }
+        if (COPIES == 4) {
+            put(b ^ 1, 3);
+            load_z(3);
         }
         wait_lgkmcnt0();   // this step's writes and reads
         __builtin_amdgcn_sched_barrier(0);
@@ -170,33 +255,39 @@ __global__ __launch_bounds__(256, 2) void wgrad_kernel(WgradArgs p)
         __builtin_amdgcn_sched_barrier(0);
     }
 
+    // dZ column m of the tile is row (of dW) row_of(m), if valid
+    auto row_of = [&](int m) __attribute__((always_inline)) {
+        return SRC == WG_GATED && m >= TW ? p.M + m0 + m - TW : m0 + m;
+    };
+    auto valid = [&](int m) __attribute__((always_inline)) { return (m % TW) < mleft; };
     float* out = p.out + seg * p.pstride;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const int m = m0 + wm * 64 + 2 * (lane & 31) + i;
-        if (m < p.M) {
+        const int m = wm * 64 + 2 * (lane & 31) + i;
+        if (valid(m)) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 // columns 2 p + j for p = 8 q + 4 (l / 32) .. +3
                 const int n = n0 + wn * 64 + 16 * q + 8 * (lane >> 5);
                 const f32x4_t u = {acc[i][0][4 * q], acc[i][1][4 * q], acc[i][0][4 * q + 1], acc[i][1][4 * q + 1]};
                 const f32x4_t v = {acc[i][0][4 * q + 2], acc[i][1][4 * q + 2], acc[i][0][4 * q + 3], acc[i][1][4 * q + 3]};
-                store4(out + (int64_t)m * p.ldo, n, p.N, u);
-                store4(out + (int64_t)m * p.ldo, n + 4, p.N, v);
+                store4(out + (int64_t)row_of(m) * p.ldo, n, p.N, u);
+                store4(out + (int64_t)row_of(m) * p.ldo, n + 4, p.N, v);
             }
         }
     }
     if (sums) {
         // (every wave has passed the last step's barrier: the slabs are free)
         float* sum = smZ[0];
-        *reinterpret_cast<f32x4_t*>(&sum[cr * TILE + cc]) = bsum;
+#pragma unroll
+        for (int h = 0; h < HALVES; ++h) *reinterpret_cast<f32x4_t*>(&sum[cr * TILE + h * TW + cc]) = bsum[h];
         wait_lgkmcnt0();
         __builtin_amdgcn_s_barrier();
-        if (t < TILE && t < mleft) {
+        if (t < TILE && valid(t)) {
             float v = sum[t];
 #pragma unroll
-            for (int r = 1; r < 8; ++r) v = v + sum[r * TILE + t];
-            p.db[seg * p.bstride + m0 + t] = v;
+            for (int r = 1; r < ROWS; ++r) v = v + sum[r * TILE + t];
+            p.db[seg * p.bstride + row_of(t)] = v;
         }
     }
 }
@@ -245,15 +336,18 @@ struct WgradPlan {
     int64_t tiles_m, tiles_n, tiles;
     int segs, seg_steps;
     int64_t ldp;      // row of a partial result
+    int64_t rows_out; // rows of dW
 };
 
 // Segments: the load of the busiest CU is ceil(tiles * segs / 256) segment
 // tiles of ceil(steps / segs) slabs; the fewest segments within 5 % of the
-// least load, 64 at most and 4 slabs each at least.
-WgradPlan plan_wgrad(int64_t rows, int64_t M, int64_t N)
+// least load, 128 at most and 4 slabs each at least.
+WgradPlan plan_wgrad(int64_t rows, int64_t M, int64_t N, bool gated)
 {
     WgradPlan p;
-    p.tiles_m = (M + TILE - 1) / TILE;
+    const int64_t tw = gated ? TILE / 2 : TILE;
+    p.rows_out = gated ? 2 * M : M;
+    p.tiles_m = (M + tw - 1) / tw;
     p.tiles_n = N > 0 ? (N + TILE - 1) / TILE : 1;
     p.tiles = p.tiles_m * p.tiles_n;
     const int64_t steps = (rows + BK - 1) / BK;
@@ -279,25 +373,48 @@ WgradPlan plan_wgrad(int64_t rows, int64_t M, int64_t N)
     return p;
 }
 
-}  // namespace
-
-size_t wgrad_workspace(int64_t rows, int64_t M, int64_t N)
+template <int SRC>
+void launch_src(int act, int grid, const WgradArgs& a, hipStream_t s)
 {
-    const WgradPlan p = plan_wgrad(rows, M, N);
-    return p.segs > 1 ? (size_t)p.segs * (size_t)(M * p.ldp + ((M + 3) & ~(int64_t)3)) * sizeof(float) : 0;
+    auto go = [&]<int ACT>() { hipLaunchKernelGGL((wgrad_kernel<SRC, ACT>), dim3(grid), dim3(256), 0, s, a); };
+    if constexpr (SRC == WG_PLAIN) {
+        go.template operator()<EMU_ACT_IDENTITY>();
+    } else {
+        switch (act) {
+        case EMU_ACT_RELU: go.template operator()<EMU_ACT_RELU>(); break;
+        case EMU_ACT_SILU: go.template operator()<EMU_ACT_SILU>(); break;
+        case EMU_ACT_GELU: go.template operator()<EMU_ACT_GELU>(); break;
+        case EMU_ACT_GELU_TANH: go.template operator()<EMU_ACT_GELU_TANH>(); break;
+        case EMU_ACT_TANH: go.template operator()<EMU_ACT_TANH>(); break;
+        default: go.template operator()<EMU_ACT_IDENTITY>(); break;
+        }
+    }
 }
 
-hipError_t launch_wgrad(int64_t rows, int64_t M, int64_t N, const float* dZ, int64_t lddz, const float* X,
-                        int64_t ldx, float* dW, int64_t lddw, float* db, void* ws, hipStream_t s)
+}  // namespace
+
+size_t wgrad_workspace(int64_t rows, int64_t M, int64_t N, bool gated)
 {
-    const WgradPlan pl = plan_wgrad(rows, M, N);
-    if (pl.tiles * pl.segs >= ((int64_t)1 << 31) || lddz > kWgradMaxLd || ldx > kWgradMaxLd || M >= ((int64_t)1 << 31) - TILE ||
+    const WgradPlan p = plan_wgrad(rows, M, N, gated);
+    return p.segs > 1 ? (size_t)p.segs * (size_t)(p.rows_out * p.ldp + ((p.rows_out + 3) & ~(int64_t)3)) * sizeof(float) : 0;
+}
+
+hipError_t launch_wgrad(int64_t rows, int64_t M, int64_t N, const WgradSource& src, const float* X, int64_t ldx,
+                        float* dW, int64_t lddw, float* db, void* ws, hipStream_t s)
+{
+    const WgradPlan pl = plan_wgrad(rows, M, N, src.gated);
+    if (pl.tiles * pl.segs >= ((int64_t)1 << 31) || src.ldz > kWgradMaxLd || ldx > kWgradMaxLd ||
+        src.ldy > kWgradMaxLd || src.ldd > kWgradMaxLd || pl.rows_out >= ((int64_t)1 << 31) - TILE ||
         N >= ((int64_t)1 << 31) - TILE)
         return hipErrorInvalidValue;
     WgradArgs a{};
-    a.Z = dZ;
+    a.Z = src.Z;
+    a.ldz = src.ldz;
+    a.Y = src.dY;
+    a.ldy = src.ldy;
+    a.dZ = src.dZ;
+    a.ldd = src.ldd;
     a.X = X;
-    a.ldz = lddz;
     a.ldx = ldx;
     a.rows = rows;
     a.M = (int)M;
@@ -307,9 +424,9 @@ hipError_t launch_wgrad(int64_t rows, int64_t M, int64_t N, const float* dZ, int
     a.segs = pl.segs;
     a.seg_steps = pl.seg_steps;
     float* part = static_cast<float*>(ws);
-    const int64_t pstride = M * pl.ldp;
+    const int64_t pstride = pl.rows_out * pl.ldp;
+    const int64_t bstride = (pl.rows_out + 3) & ~(int64_t)3;
     float* bpart = part + pl.segs * pstride;
-    const int64_t bstride = (M + 3) & ~(int64_t)3;
     if (pl.segs > 1) {
         a.out = part;
         a.ldo = pl.ldp;
@@ -321,13 +438,19 @@ hipError_t launch_wgrad(int64_t rows, int64_t M, int64_t N, const float* dZ, int
         a.ldo = lddw;
         a.db = db;
     }
-    hipLaunchKernelGGL(wgrad_kernel, dim3((int)(pl.tiles * pl.segs)), dim3(256), 0, s, a);
+    const int grid = (int)(pl.tiles * pl.segs);
+    if (src.gated)
+        launch_src<WG_GATED>(src.act, grid, a, s);
+    else if (src.dY != nullptr)
+        launch_src<WG_ACT>(src.act, grid, a, s);
+    else
+        launch_src<WG_PLAIN>(0, grid, a, s);
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && pl.segs > 1) {
-        const int64_t work = M * (pl.ldp / 4) + (db != nullptr ? bstride / 4 : 0);
+        const int64_t work = pl.rows_out * (pl.ldp / 4) + (db != nullptr ? bstride / 4 : 0);
         if ((work + 63) / 64 >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
         hipLaunchKernelGGL(wgrad_join_kernel, dim3((int)((work + 63) / 64)), dim3(256), 0, s, part, pl.segs, pstride,
-                           pl.ldp, (int)M, (int)N, dW, lddw, bpart, bstride, db);
+                           pl.ldp, (int)pl.rows_out, (int)N, dW, lddw, bpart, bstride, db);
         e = hipGetLastError();
     }
     return e;

@@ -191,6 +191,24 @@ emu_status_t emu_wgrad(int64_t rows, int64_t M, int64_t N, const float* dZ, int6
                        const float* X, int64_t ldx, float* dW, int64_t lddw, float* db,
                        void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * The same with the activation's backward pass on the way: dZ, which the
+ * input-gradient product needs too, is made from dY and Z as by
+ * emu_act_backward (emu_gated_backward: dH, Z = [g | u], dZ = [dg | du], dW
+ * 2F x N, db 2F), written once and multiplied in the same pass.  dZ may not
+ * overlap dY or Z.  Workspaces: emu_wgrad_workspace(rows, M, N),
+ * emu_wgrad_gated_workspace(rows, F, N).
+ */
+emu_status_t emu_wgrad_act(int64_t rows, int64_t M, int64_t N, const float* dY, int64_t lddy,
+                           const float* Z, int64_t ldz, emu_act_t act, float* dZ, int64_t lddz,
+                           const float* X, int64_t ldx, float* dW, int64_t lddw, float* db,
+                           void* workspace, size_t workspace_bytes, void* stream);
+emu_status_t emu_wgrad_gated_workspace(int64_t rows, int64_t F, int64_t N, size_t* bytes);
+emu_status_t emu_wgrad_gated(int64_t rows, int64_t F, int64_t N, const float* dH, int64_t lddh,
+                             const float* Z, int64_t ldz, emu_act_t act, float* dZ, int64_t lddz,
+                             const float* X, int64_t ldx, float* dW, int64_t lddw, float* db,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -73,6 +73,12 @@ CALLS = {
                             [(0, -1), (2, None), (3, 11), (4, None), (5, 5), (6, None), (7, 11), (8, 6), (10, 5), (12, 11)]),
     "emu_wgrad": ([64, 6, 8, FAKE, 6, FAKE, 8, FAKE, 8, None, None, 0, None],
                   [(0, -1), (1, -1), (2, -1), (3, None), (4, 5), (5, None), (6, 7), (7, None), (8, 7)]),
+    "emu_wgrad_act": ([64, 6, 8, FAKE, 6, FAKE, 6, 2, FAKE, 6, FAKE, 8, FAKE, 8, None, None, 0, None],
+                      [(0, -1), (1, -1), (2, -1), (3, None), (4, 5), (5, None), (6, 5), (7, 6), (8, None), (9, 5),
+                       (10, None), (11, 7), (12, None), (13, 7)]),
+    "emu_wgrad_gated": ([64, 6, 8, FAKE, 6, FAKE, 12, 2, FAKE, 12, FAKE, 8, FAKE, 8, None, None, 0, None],
+                        [(0, -1), (1, -1), (2, -1), (3, None), (4, 5), (5, None), (6, 11), (7, -1), (8, None), (9, 11),
+                         (10, None), (11, 7), (12, None), (13, 7)]),
     "emu_presplit_gated": ([6, 8, FAKE, 8, 1, FAKE, None], [(0, -1), (1, -1), (2, None), (3, 7), (4, 0), (5, None), (5, FAKE + 8)]),
 }
 
