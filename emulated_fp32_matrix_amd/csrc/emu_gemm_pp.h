@@ -45,6 +45,24 @@ __host__ __device__ constexpr int64_t chunk_elems(int np) { return (int64_t)np *
 
 namespace {
 
+// The kernel's BlockEpilogue argument, read from its argument segment where
+// the epilogue begins: held in scalar registers through the main loop
+// instead, its 18 words spilled 40 of them, and those into vector registers.
+template <class E>
+__device__ __forceinline__ E reload_epilogue(const E& e)
+{
+#ifndef __HIP_DEVICE_COMPILE__
+    return e;   // (the host pass only parses this)
+#else
+    typedef const __attribute__((address_space(4))) char* kernarg_t;
+    constexpr int at = (sizeof(Params) + 7) / 8 * 8 + sizeof(void*);   // (Params, Wb, epilogue)
+    static_assert(alignof(E) == 8, "arguments of 8-byte alignment");
+    kernarg_t k = (kernarg_t)__builtin_amdgcn_kernarg_segment_ptr() + at;
+    asm volatile("" : "+s"(k));   // (not hoisted out of the loop)
+    return *reinterpret_cast<const __attribute__((address_space(4))) E*>(k);
+#endif
+}
+
 // ---------------------------------------------------------------------------
 // Ping-pong form of the GEMM kernel for a k-contiguous FP32 op(A) (split in
 // the kernel).  The 8 waves form two groups of four, one wave of each group
@@ -377,6 +395,28 @@ __global__ __launch_bounds__(512, 1) void gemm_bf16_pp_kernel(Params p, const ui
             return __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(q), (short)0, 0x7FFFFFFF, 0x00020000);
         };
         const int half4 = 4 * (lane >> 5);
+        // every residual of the wave's rows is requested here: one memory
+        // latency per tile
+        f32x4_t res[EPI == EPI_ACT ? TM : 1][4];
+        if constexpr (EPI == EPI_ACT) {
+            if (has_r) {
+#pragma unroll
+                for (int i = 0; i < TM; ++i) {
+                    const int row = grp * GROWS + i * 32 + (lane & 31);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int col = gw * 32 + 8 * q + half4;
+                        if (full)
+                            res[i][q] = __builtin_bit_cast(
+                                f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                                             rsrc(rbase), row < w.rows ? (row * (int)be.ldr + col) * 4 : (int)0x80000000, 0, 0));
+                        else
+                            res[i][q] = row < w.rows ? load4(rbase + row * be.ldr, col, cols_left) : f32x4_t{};
+                    }
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
             const int row = grp * GROWS + i * 32 + (lane & 31);
@@ -394,17 +434,6 @@ __global__ __launch_bounds__(512, 1) void gemm_bf16_pp_kernel(Params p, const ui
                 else if (row_ok)
                     store4(base + row * ld, col, cols_left, v);
             };
-            f32x4_t res[4];
-            if (has_r) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int col = col_of(q);
-                    if (full)
-                        res[q] = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rsrc(rbase), offset(be.ldr, col), 0, 0));
-                    else
-                        res[q] = row_ok ? load4(rbase + row * be.ldr, col, cols_left) : f32x4_t{};
-                }
-            }
             f32x4_t z[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q)
@@ -458,7 +487,8 @@ __global__ __launch_bounds__(512, 1) void gemm_bf16_pp_kernel(Params p, const ui
             for (int q = 0; q < NOUT; ++q) {
                 f32x4_t o = z[q];
                 if constexpr (EPI == EPI_GATED) o = o * z[q + 2];
-                if (has_r) o = o + res[q];
+                if constexpr (EPI == EPI_ACT)
+                    if (has_r) o = o + res[i][q];
                 put(cbase, ldc, col_of(q), o);
             }
         }
@@ -466,7 +496,7 @@ __global__ __launch_bounds__(512, 1) void gemm_bf16_pp_kernel(Params p, const ui
     const bool unit_alpha = p.alpha == 1.0f;
     auto epilogue_any = [&](const TilePos& w) __attribute__((always_inline)) {
         if constexpr (EPI != EPI_PLAIN)
-            block_epilogue(w, finish...);
+            block_epilogue(w, reload_epilogue(finish...));
         else if constexpr (SPLIT)
             epilogue.template operator()<true>(w);
         else if (unit_alpha)
