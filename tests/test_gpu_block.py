@@ -144,7 +144,7 @@ def test_layer_norm_in_place_and_untouched_surroundings():
     """Raw calls: y over x, dx over dy, leading dimensions wider than the row;
     what lies between the rows stays as it was."""
     block = _block()
-    lib, s = block._lib, torch.cuda.current_stream().cuda_stream
+    lib, s = block._lib, torch.cuda.current_stream().cuda_stream or None
     for rows, cols, ld in ((37, 61, 70), (20, 256, 260), (5, 2500, 2501)):
         buf = _randn(rows, rows, ld)
         x = buf.clone()
@@ -187,11 +187,11 @@ def test_activation_values_and_slopes(name):
     d1, d2, s1, s2 = ref.slopes(name, zz.double())
     dy, v = _randn(1, n, 1), _randn(2, n, 1)
     tiny = 2.0**-110   # where exponentials and reciprocals fall below 2^-126
-    got = block._ActBackward.apply(dy, zz, block.ACTIVATIONS[name])
+    got = block.act_grad(dy, zz, name)
     _within(f"{name}'", got, (dy.double() * d1, dy.double().abs() * (24 * U * s1.nan_to_num(0, 0, 0) + tiny)))
     dyg, zg = dy.clone().requires_grad_(True), small.clone().requires_grad_(True)
     m = small.shape[0]
-    out = block._ActBackward.apply(dyg[:m], zg, block.ACTIVATIONS[name])
+    out = block.act_grad(dyg[:m], zg, name)
     gdy, gz = torch.autograd.grad(out, (dyg, zg), v[:m])
     d1, d2, s1, s2 = ref.slopes(name, small.double())
     _within(f"{name}' again", gdy[:m], (v[:m].double() * d1, v[:m].double().abs() * (24 * U * s1 + tiny)))
@@ -208,7 +208,7 @@ def test_activation_keeps_nan(name):
                          activation=name)
     assert bool(torch.isnan(y).all())
     if name not in ("identity", "relu"):
-        d = block._ActBackward.apply(dy, z, block.ACTIVATIONS[name])
+        d = block.act_grad(dy, z, name)
         assert torch.isnan(d).tolist() == [[True, False, True, False]]
 
 
@@ -289,16 +289,67 @@ def test_linear_act_matches_sgemm_in_the_explicit_modes():
             y = block.linear_act(x, w, b, activation="silu", mode=mode)
             x2 = x.clone().requires_grad_(True)
             assert torch.equal(block.linear_act(x2, w, b, activation="silu", mode=mode), y)
-            assert torch.equal(block._product(x, w.t().contiguous(), False, b, 2, None, None, emu.MODES[mode]),
-                               emu_act_of(block, x, w.t().contiguous(), b, mode))
 
 
-def emu_act_of(block, x, wt, b, mode):
+def _raw_linear(x, w, trans_b, bias, act, mode, z=None):
+    """emu_sgemm_act with op(B) = w or w^T and wider leading dimensions than
+    the rows; what lies between the rows of C and Z stays."""
     import emulated_fp32_matrix_amd as emu
 
-    z = emu.sgemm(x, wt, mode=mode) + b
-    one = torch.eye(z.shape[1], device="cuda:0")
-    return block.linear_act(z, one, activation="silu", mode="BF16X9")   # z I = z exactly
+    block = _block()
+    lib, (M, K) = block._lib, x.shape
+    N = w.shape[0] if trans_b else w.shape[1]
+    c = torch.full((M, N + 3), 7.0, device="cuda:0")
+    zz = torch.full((M, N + 5), 7.0, device="cuda:0")
+    need = ctypes.c_size_t(0)
+    args = (int(trans_b), M, N, K, x.data_ptr(), x.stride(0))
+    assert lib.emu_sgemm_act_workspace(*args, 0, emu.MODES[mode], ctypes.byref(need)) == 0
+    ws = torch.empty(max(need.value, 1), dtype=torch.uint8, device="cuda:0")
+    assert lib.emu_sgemm_act(*args, w.data_ptr(), w.stride(0), None, bias.data_ptr(), act, zz.data_ptr(), N + 5, None, N,
+                             c.data_ptr(), N + 3, emu.MODES[mode], ws.data_ptr(), need.value,
+                             torch.cuda.current_stream().cuda_stream) == 0
+    assert bool((c[:, N:] == 7.0).all()) and bool((zz[:, N:] == 7.0).all())
+    return c[:, :N], zz[:, :N]
+
+
+@pytest.mark.parametrize("mode", ["AUTO", "BF16X9", "BF16X6", "NATIVE_F32"])
+def test_sgemm_act_both_layouts_of_b(mode):
+    """B stored K x N and N x K give the same bits; Z is the product plus the
+    bias, C its activation."""
+    block = _block()
+    for M, N, K in ((1, 70, 33), (40, 64, 128), (300, 260, 100), (150, 131, 387)):
+        x, w, b, _ = _linear_case(M, N, K, False)
+        c1, z1 = _raw_linear(x, w, True, b, 2, mode)
+        c2, z2 = _raw_linear(x, w.t().contiguous(), False, b, 2, mode)
+        assert torch.equal(c1, c2) and torch.equal(z1, z2), (M, N, K)
+        assert torch.equal(z1, block.linear_act(x, w, b, mode=mode))
+        assert torch.equal(c1, block.linear_act(x, w, b, activation="silu", mode=mode))
+
+
+@pytest.mark.parametrize("mode", ["AUTO", "BF16X9", "BF16X6"])
+def test_planes_bitwise(mode):
+    """Weights split once beforehand: the results of the calls that split."""
+    import emulated_fp32_matrix_amd as emu
+
+    block = _block()
+    split = "BF16X9" if mode == "AUTO" else mode
+    for M in (100, 300, 6144):
+        x, w, b, r = _linear_case(M, 200, 96, True)
+        pb = emu.presplit_b(w, mode=split, trans_b=True)
+        pg = block.presplit_gated(w, split)
+        assert torch.equal(block.linear_act(x, w, b, "gelu", r, mode=mode, planes=pb),
+                           block.linear_act(x, w, b, "gelu", r, mode=mode)), M
+        assert torch.equal(block.gated_linear(x, w, b, mode=mode, planes=pg), block.gated_linear(x, w, b, mode=mode)), M
+    x1 = x[:3]   # few rows: AUTO without planes runs FP32, with them the emulation
+    got = block.linear_act(x1, w, b, mode=mode, planes=pb)
+    z, zb = ref.product(x1.double(), w.double(), b, mode)
+    _within("few rows with planes", got, (z, zb))
+    with pytest.raises(ValueError):
+        block.linear_act(x, w, b, mode="BF16X3", planes=pb)
+    with pytest.raises(ValueError):
+        block.linear_act(x, w[:100], None, mode=mode, planes=pb)
+    with pytest.raises(TypeError):
+        block.gated_linear(x, w, b, mode=mode, planes=pb)
 
 
 def test_linear_act_strides_batches_and_empty():
@@ -437,7 +488,8 @@ def test_wgrad_refusals_and_empty():
     with pytest.raises(ValueError):
         block.wgrad(dz, x)
     with pytest.raises(ValueError):
-        block.wgrad(dz.t(), x[:8])
+        block.wgrad(dz[0], x)
+    assert torch.equal(block.wgrad(dz.t(), x[:8])[0], block.wgrad(dz.t().contiguous(), x[:8])[0])   # strided: copied
     dw, db = block.wgrad(dz[:0], x[:0], want_db=True)
     assert dw.shape == (8, 4) and bool((dw == 0).all()) and bool((db == 0).all())
     dw, db = block.wgrad(dz, x[:10, :0], want_db=True)
@@ -461,8 +513,7 @@ def _ffn64(ffn, x):
 
 @pytest.mark.parametrize("mode,activation,rows", [("AUTO", "silu", 40), ("AUTO", "gelu", 400), ("BF16X6", "gelu_tanh", 400),
                                                   ("NATIVE_F32", "tanh", 130)])
-@pytest.mark.parametrize("cache_weights", [False, True])
-def test_feed_forward_block_energy_and_force_loss(mode, activation, rows, cache_weights):
+def test_feed_forward_block_energy_and_force_loss(mode, activation, rows):
     """LayerNorm, gated projection and output layer with its residual as one
     block: y, the forces -dE/dx and the gradients of an energy + force loss
     against torch float64.  The relative errors of FP32 products of a few
@@ -470,7 +521,7 @@ def test_feed_forward_block_energy_and_force_loss(mode, activation, rows, cache_
     twenty such operations one after the other: 1e-5 leaves a factor of five."""
     block = _block()
     torch.manual_seed(3)
-    ffn = block.EmuGatedFFN(64, 96, activation=activation, mode=mode, device="cuda:0", cache_weights=cache_weights)
+    ffn = block.EmuGatedFFN(64, 96, activation=activation, mode=mode, device="cuda:0")
     with torch.no_grad():
         ffn.norm.weight.add_(0.1 * torch.randn_like(ffn.norm.weight))
         ffn.norm.bias.add_(0.1 * torch.randn_like(ffn.norm.bias))
@@ -493,7 +544,7 @@ def test_feed_forward_block_energy_and_force_loss(mode, activation, rows, cache_
     rel = lambda a, b: float((a.detach().double() - b.detach()).norm() / b.detach().norm())
     for name, a, b in [("y", y, y64), ("force", f, f64)] + list(zip(list(params) + ["x"], got, want)):
         e = rel(a, b)
-        say(f"block {mode} {activation} {rows} rows cache={cache_weights} {name}: {e:.2e}")
+        say(f"block {mode} {activation} {rows} rows {name}: {e:.2e}")
         assert e <= 1e-5, (name, e)
 
 
@@ -505,29 +556,6 @@ def test_third_derivative_is_refused():
     (h,) = torch.autograd.grad(g.pow(2).sum(), x, create_graph=True)
     with pytest.raises(RuntimeError):
         torch.autograd.grad(h.sum(), x)
-
-
-@pytest.mark.parametrize("mode", ["AUTO", "BF16X9", "BF16X6"])
-def test_cached_weights_bitwise(mode):
-    """cache_weights splits the weights once: bit-identical results, and an
-    in-place update of the weights is seen."""
-    block = _block()
-    torch.manual_seed(0)
-    plain = block.EmuGatedFFN(64, 160, mode=mode, device="cuda:0")
-    cached = block.EmuGatedFFN(64, 160, mode=mode, device="cuda:0", cache_weights=True)
-    cached.load_state_dict(plain.state_dict())
-    for step in range(2):
-        for rows in (300, 20, 1000):
-            x = _randn(rows, rows, 64).requires_grad_(True)
-            ya, yb = plain(x), cached(x)
-            assert torch.equal(ya, yb), (step, rows)
-            ga = torch.autograd.grad(ya.sum(), [x, plain.w_in])
-            gb = torch.autograd.grad(yb.sum(), [x, cached.w_in])
-            assert all(torch.equal(a, b) for a, b in zip(ga, gb)), (step, rows)
-        with torch.no_grad():
-            for m in (plain, cached):
-                m.w_in.mul_(1.5)
-                m.out.weight.mul_(0.5)
 
 
 def test_streams_and_interleaved_calls():
@@ -645,7 +673,7 @@ def test_shape_and_device_refusals():
                  lambda: block.layer_norm(x.half()), lambda: block.linear_act(x, w.cpu())):
         with pytest.raises(TypeError):
             call()
-    with pytest.raises(Exception):
+    with pytest.raises(ValueError):
         block.layer_norm(x, eps=-1.0)
 
 
