@@ -469,6 +469,13 @@ namespace emu {
 
 bool api_current_device(DeviceInfo& info) { return current_device(info); }
 
+double api_predict_us(int64_t M, int64_t N, int64_t K)
+{
+    double f32, x9;
+    predict_us(M, N, K, f32, x9);
+    return x9 < f32 ? x9 : f32;
+}
+
 int api_select_mode(int64_t M, int64_t N, int64_t K) { return (int)select_mode(M, N, K); }
 
 GemmPlan api_plan(int64_t M, int64_t N, int64_t K, bool split, int num_cu)

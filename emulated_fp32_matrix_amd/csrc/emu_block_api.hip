@@ -49,12 +49,24 @@ int bands_of(emu_mode_t mode)
     }
 }
 
-// Where EMU_MODE_AUTO takes the one-launch FP32 kernel.
+// Where EMU_MODE_AUTO takes the one-launch FP32 kernel: where it is predicted
+// faster than what emu_sgemm's AUTO runs with the epilogue.  Its time is a
+// launch and, per workgroup of a CU (64 rows x 16 columns), a latency and K;
+// measured over ten (K, N) and M = 1 .. 6,144 (us, this kernel / the emulated
+// one): 6,144 x 64 x 64 5.2 / 11.8, 1 x 512 x 256 3.6 / 12.1, 2,048 x 512 x 256
+// 14.4 / 17.7, 4,096 x 512 x 256 27.4 / 19.2, 512 x 1024 x 1024 23.6 / 30.8,
+// 1,024 x 1024 x 1024 44.4 / 40.1, 16 x 1024 x 4096 16.6 / 47.2, 64 x 1024 x
+// 4096 41.1 / 46.3.  The model picks the faster one but where the two are
+// within a tenth of each other.
 bool few_rows(int64_t M, int64_t N, int64_t K)
 {
-    (void)N;
-    (void)K;
-    return M <= 64;
+    if (M == 0 || N == 0 || K == 0 || M > ((int64_t)1 << 20)) return false;
+    const double groups = (double)((M + 63) / 64) * (double)((N + 15) / 16) / 256.0;
+    const double per_k = M <= 16 ? 0.0034 : M <= 32 ? 0.0057 : 0.0094;
+    const double us = 2.4 + (groups < 1.0 ? 1.0 : groups) * (0.75 + per_k * (double)K);
+    // (the library's model leaves out the traffic of the weights' split: 10
+    // bytes per element)
+    return us < emu::api_predict_us(M, N, K) + 10.0 * (double)N * (double)K / 4.0e6;
 }
 
 size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }

@@ -8,11 +8,12 @@
 namespace emu {
 
 // From emu_api.hip: the current device (false unless gfx950), the mode
-// EMU_MODE_AUTO runs for a shape, and a launch plan of the emulated kernel:
+// EMU_MODE_AUTO runs for a shape and its predicted time, and a launch plan of the emulated kernel:
 // AUTO's (K split included) or, without `split`, one that only picks the
 // tile height.
 bool api_current_device(DeviceInfo& info);
 int api_select_mode(int64_t M, int64_t N, int64_t K);
+double api_predict_us(int64_t M, int64_t N, int64_t K);
 struct GemmPlan {
     int split, tile_m;
     int64_t split_from;

@@ -127,9 +127,10 @@ emu_status_t emu_act_backward2(int64_t rows, int64_t cols, const float* v, int64
  *
  * mode: as emu_sgemm's, and the product is emu_sgemm's in the explicit modes,
  * bit for bit.  EMU_MODE_AUTO: for few
- * rows (emu_sgemm_act_route) an FP32 matrix-instruction kernel that reads the
- * operands as they are and runs as one launch, otherwise what emu_sgemm's
- * AUTO runs, its K split plan included.
+ * rows (where a cost model predicts it faster: emu_sgemm_act_route) an FP32
+ * matrix-instruction kernel that reads the operands as they are and runs as
+ * one launch, otherwise what emu_sgemm's AUTO runs, its K split plan
+ * included.
  * planes: op(B) split by emu_presplit_b in `mode` (an emulated one), or in
  * BF16X9 for EMU_MODE_AUTO, which then runs BF16X9 whatever the shape; B and
  * ldb are not read.  NULL: the call splits op(B) into the workspace.

@@ -333,7 +333,7 @@ def test_planes_bitwise(mode):
 
     block = _block()
     split = "BF16X9" if mode == "AUTO" else mode
-    for M in (100, 300, 6144):
+    for M in (30000,) if mode == "AUTO" else (100, 300, 6144):   # (AUTO takes the FP32 kernel for fewer rows)
         x, w, b, r = _linear_case(M, 200, 96, True)
         pb = emu.presplit_b(w, mode=split, trans_b=True)
         pg = block.presplit_gated(w, split)
@@ -350,6 +350,40 @@ def test_planes_bitwise(mode):
         block.linear_act(x, w[:100], None, mode=mode, planes=pb)
     with pytest.raises(TypeError):
         block.gated_linear(x, w, b, mode=mode, planes=pb)
+
+
+# (M, N, K): every tile split, the last round split, 64- and 128-row tiles, none
+@pytest.mark.parametrize("M,N,K", [(6144, 1024, 1024), (768, 512, 4096), (700, 640, 2048), (3300, 1200, 512), (9000, 260, 96)])
+def test_auto_plans(M, N, K):
+    """The K split plans of AUTO with the fused epilogues: bit for bit
+    emu_sgemm's product where the epilogue adds one rounding, and the gated
+    projection against the linear one with its rows reordered."""
+    import emulated_fp32_matrix_amd as emu
+
+    block = _block()
+    few = ctypes.c_int(-1)
+    assert block._lib.emu_sgemm_act_route(1, M, N, K, ctypes.byref(few)) == 0
+    say(f"{M}x{N}x{K}: plan {emu.select_plan(M, N, K)}, few rows {few.value}")
+    assert few.value == 0 and emu.select_mode(M, N, K) == "BF16X9"
+    x, w, b, r = _linear_case(M, N, K, True)
+    t = emu.sgemm(x, w, mode="AUTO", trans_b=True)
+    assert torch.equal(block.linear_act(x, w, b, residual=r), (t + b) + r)
+    z, zb = ref.product(x.double(), w.double(), b, "AUTO")
+    y = block.linear_act(x, w, b, "gelu", r)
+    want = ref.act("gelu", z) + r.double()
+    _within("gelu", y, (want, 1.01 * (ref.act_bound("gelu", z) + 1.2 * zb + U * want.abs())))
+    # [g | u] = t + b: the gated product of the same weight, bit for bit where
+    # the plan splits whole rows of tiles (its tiles hold other columns)
+    F = N // 2
+    zz = t + b
+    h = block.gated_linear(x, w, b, "relu")
+    if emu.select_plan(M, N, K)[2] % -(-N // 128) == 0:
+        assert torch.equal(h, torch.relu(zz[:, :F]) * zz[:, F:])
+    a, u, ab, ub = torch.relu(z[:, :F]), z[:, F:], zb[:, :F], zb[:, F:]
+    _within("gated", h, (a * u, 1.01 * (ab * (u.abs() + ub) + a * ub) + U * (a * u).abs() + 1e-30))
+    xg = x.clone().requires_grad_(True)
+    h2 = block.gated_linear(xg, w, b, "relu")   # keeps Z
+    assert torch.equal(h2, h)
 
 
 def test_linear_act_strides_batches_and_empty():
