@@ -126,7 +126,7 @@ emu_status_t emu_act_backward2(int64_t rows, int64_t cols, const float* v, int64
  * One rounding per operation, in the order written; act in FP32.
  *
  * mode: as emu_sgemm's, and the product is emu_sgemm's in the explicit modes,
- * bit for bit.  EMU_MODE_AUTO: for few
+ * bit for bit (a row of C never depends on the other rows).  EMU_MODE_AUTO: for few
  * rows (where a cost model predicts it faster: emu_sgemm_act_route) an FP32
  * matrix-instruction kernel that reads the operands as they are and runs as
  * one launch, otherwise what emu_sgemm's AUTO runs, its K split plan
