@@ -451,24 +451,31 @@ __global__ __launch_bounds__(512, 1) void gemm_bf16_pp_kernel(Params p, const ui
                 continue;
             }
             if (be.bias != nullptr) {
+                if (full) {
+                    // the bias of the wave's 32 columns (gated: 16 gates, 16
+                    // ups) by scalar loads under one wait, which never waits
+                    // for the direct loads in flight (a wait per 8 columns:
+                    // 2,325 us instead of 2,258 on the gated 552,960 x 256 ->
+                    // 2 x 512)
+                    const float* b = be.bias + n0 + gw * (EPI == EPI_GATED ? 16 : 32);
+                    i32x16_t bw[2];
+                    scalar_load16x2(b, EPI == EPI_GATED ? b + p.N : b + 16, bw[0], bw[1]);
+                    const bool upper = (lane >> 5) != 0;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const float* b = be.bias + n0 + (EPI == EPI_GATED && q >= 2 ? p.N : 0);
-                    if (full) {
-                        // (scalar loads: waiting for them never waits for the
-                        // direct loads in flight)
-                        const i32x8_t bv = scalar_load8(b + (EPI == EPI_GATED ? gw * 16 + 8 * (q & 1) : gw * 32 + 8 * q));
-                        const bool upper = (lane >> 5) != 0;
+                    for (int q = 0; q < 4; ++q)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            int lo = bv[e], hi = bv[4 + e];
+                            // (opaque copies: otherwise the two selects fold
+                            // into an index and a chain of compares)
+                            int lo = bw[q >> 1][8 * (q & 1) + e], hi = bw[q >> 1][8 * (q & 1) + 4 + e];
                             asm("" : "+s"(lo));
                             asm("" : "+s"(hi));
                             z[q][e] = z[q][e] + __int_as_float(upper ? hi : lo);
                         }
-                    } else {
-                        z[q] = z[q] + load4(b, col_of(q), cols_left);
-                    }
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        z[q] = z[q] + load4(be.bias + n0 + (EPI == EPI_GATED && q >= 2 ? p.N : 0), col_of(q), cols_left);
                 }
             }
             if (has_z) {

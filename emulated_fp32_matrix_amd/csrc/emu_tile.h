@@ -143,6 +143,20 @@ __device__ __forceinline__ i32x8_t scalar_load8(const void* p)
     return v;
 }
 
+typedef int i32x16_t __attribute__((ext_vector_type(16)));
+
+// Two runs of sixteen words, as scalar_load8, under one wait.
+__device__ __forceinline__ void scalar_load16x2(const void* p, const void* q, i32x16_t& a, i32x16_t& b)
+{
+    i32x16_t u, v;
+    asm volatile("s_load_dwordx16 %0, %2, 0x0\n\ts_load_dwordx16 %1, %3, 0x0\n\ts_waitcnt lgkmcnt(0)"
+                 : "=&s"(u), "=&s"(v)
+                 : "s"(uniform_ptr(p)), "s"(uniform_ptr(q))
+                 : "memory");
+    a = u;
+    b = v;
+}
+
 // Direct global->LDS copy of 16 bytes per lane: lane l reads gbase + voff
 // and its bytes land at LDS offset lds_base + 16 l (gbase and lds_base
 // wave-uniform).  Inline assembly keeps the compiler from guarding later LDS
