@@ -247,9 +247,9 @@ WeightGrads weight_grad_from(const Rows& dy, const Rows& z, int act, const Rows&
 }
 
 // Whether the activation's backward pass runs inside the weight gradient:
-// every 128 columns of x repeat it, which pays for up to two such tiles
-// (552,960 x 256 -> 2 x 512, silu: 8,123 us apart, 7,435 inside; 6,144 x 1024
-// -> 4096, gelu: 1,277 apart, 1,719 inside).
+// every 256 columns of x repeat it, which pays where there is one such tile
+// (552,960 x 256 -> 2 x 512, silu: 3,230 us apart, 2,530 inside; 6,144 x 1024
+// -> 4096, gelu, training step: 1,277 apart, 1,719 inside).
 bool fuse_act(int64_t in_features) { return in_features <= 256; }
 
 Tensor act_backward(const Rows& dy, const Rows& z, int act, bool is_gated)

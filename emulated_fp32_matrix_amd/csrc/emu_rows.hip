@@ -19,33 +19,40 @@ namespace emu {
 namespace {
 
 constexpr int WAVES = 8;
+constexpr int64_t kWide = 256;   // workgroups of 32 columns from which on they are used
 
-template <bool TB, bool GATED, int MT>
+template <bool TB, bool GATED, int MT, int NT>
 __global__ __launch_bounds__(64 * WAVES) void rows_gemm_kernel(int64_t M, int N, int K, const float* __restrict__ A,
                                                                int64_t lda, const float* __restrict__ B,
                                                                int64_t ldb, BlockEpilogue ep)
 {
     static_assert(TB || !GATED, "the gated projection's weights are stored N x K");
-    constexpr int G = GATED ? 2 : 1;
+    static_assert(NT == 1 || !GATED, "a gated workgroup's second 16 columns are the up projection's");
+    constexpr int G = GATED ? 2 : NT;    // 16-column fragments of the weights
     constexpr int U = MT == 4 ? 2 : 4;   // slices of k in flight per wave
     __shared__ __attribute__((aligned(16))) f32x4_t part[WAVES][MT * G][64];
 
     const int lane = threadIdx.x & 63;
     const int wave = threadIdx.x >> 6;
     const int64_t m0 = (int64_t)blockIdx.y * (16 * MT);
-    const int n0 = blockIdx.x * 16;
+    const int n0 = blockIdx.x * (16 * NT);
     const int kq = (lane >> 4) * 4;
     // rows and columns past the end repeat the last one; they are not stored
-    const int n = n0 + (lane & 15) < N ? n0 + (lane & 15) : N - 1;
+    int64_t bcol[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        const int n = n0 + (GATED ? 0 : 16 * g) + (lane & 15);
+        bcol[g] = (n < N ? n : N - 1) + (GATED ? (int64_t)g * N : 0);
+    }
     const float* arow[MT];
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
         const int64_t m = m0 + 16 * i + (lane & 15);
         arow[i] = A + (m < M ? m : M - 1) * lda;
     }
-    auto load_b = [&](int k, int col) __attribute__((always_inline)) {
+    auto load_b = [&](int k, int64_t col) __attribute__((always_inline)) {
         if constexpr (TB) {
-            return load4(B + (int64_t)col * ldb, k, K);
+            return load4(B + col * ldb, k, K);
         } else {
             f32x4_t v;
 #pragma unroll
@@ -67,7 +74,7 @@ __global__ __launch_bounds__(64 * WAVES) void rows_gemm_kernel(int64_t M, int N,
         for (int u = 0; u < U; ++u) {
             const int k = (c0 + u * WAVES) * 16 + kq;   // past the end: zeros
 #pragma unroll
-            for (int g = 0; g < G; ++g) b[u][g] = load_b(k, n + g * N);
+            for (int g = 0; g < G; ++g) b[u][g] = load_b(k, bcol[g]);
 #pragma unroll
             for (int i = 0; i < MT; ++i) a[u][i] = load4(arow[i], k, K);
         }
@@ -89,18 +96,20 @@ __global__ __launch_bounds__(64 * WAVES) void rows_gemm_kernel(int64_t M, int N,
         for (int g = 0; g < G; ++g) part[wave][i * G + g][lane] = acc[i][g];
     __syncthreads();
 
-    if (threadIdx.x >= 64 * MT) return;
-    const int i = threadIdx.x >> 6;
+    if (threadIdx.x >= 64 * MT * NT) return;
+    const int i = (threadIdx.x >> 6) % MT, h = (threadIdx.x >> 6) / MT;
     const int64_t m = m0 + 16 * i + (lane & 15);
     if (m >= M) return;
-    const int c = n0 + 4 * (lane >> 4);
+    const int c = n0 + 16 * h + 4 * (lane >> 4);
     if (c >= N) return;
-    f32x4_t z[G];
+    constexpr int Z = GATED ? 2 : 1;
+    f32x4_t z[Z];
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-        z[g] = part[0][i * G + g][lane];
+    for (int g = 0; g < Z; ++g) {
+        const int f = i * G + (GATED ? g : h);
+        z[g] = part[0][f][lane];
 #pragma unroll
-        for (int w = 1; w < WAVES; ++w) z[g] = z[g] + part[w][i * G + g][lane];
+        for (int w = 1; w < WAVES; ++w) z[g] = z[g] + part[w][f][lane];
         if (ep.bias != nullptr) z[g] = z[g] + load4(ep.bias + (int64_t)g * N, c, N);
         if (ep.Z != nullptr) store4(ep.Z + m * ep.ldz + (int64_t)g * N, c, N, z[g]);
     }
@@ -110,7 +119,7 @@ __global__ __launch_bounds__(64 * WAVES) void rows_gemm_kernel(int64_t M, int N,
         for (int e = 0; e < 4; ++e) o[e] = act_value<ACT>(z[0][e]);
     });
     if constexpr (GATED)
-        o = o * z[G - 1];
+        o = o * z[Z - 1];
     else if (ep.R != nullptr)
         o = o + load4(ep.R + m * ep.ldr, c, N);
     store4(ep.C + m * ep.ldc, c, N, o);
@@ -120,17 +129,22 @@ template <bool TB, bool GATED>
 void launch(int64_t M, int64_t N, int64_t K, const float* A, int64_t lda, const float* B, int64_t ldb,
             const BlockEpilogue& ep, hipStream_t s)
 {
-    const int gx = (int)((N + 15) / 16);
-    auto go = [&]<int MT>() {
-        hipLaunchKernelGGL((rows_gemm_kernel<TB, GATED, MT>), dim3(gx, (int)((M + 16 * MT - 1) / (16 * MT))),
+    auto go = [&]<int MT, int NT>() {
+        const int gx = (int)((N + 16 * NT - 1) / (16 * NT));
+        hipLaunchKernelGGL((rows_gemm_kernel<TB, GATED, MT, NT>), dim3(gx, (int)((M + 16 * MT - 1) / (16 * MT))),
                            dim3(64 * WAVES), 0, s, M, (int)N, (int)K, A, lda, B, ldb, ep);
     };
-    if (M <= 16)
-        go.template operator()<1>();
-    else if (M <= 32)
-        go.template operator()<2>();
-    else
-        go.template operator()<4>();
+    if (M <= 16) {
+        go.template operator()<1, 1>();
+    } else if (M <= 32) {
+        go.template operator()<2, 1>();
+    } else {
+        // two fragments of columns per workgroup where that leaves every CU one
+        if constexpr (!GATED) {
+            if (((M + 63) / 64) * ((N + 31) / 32) >= kWide) return go.template operator()<4, 2>();
+        }
+        go.template operator()<4, 1>();
+    }
 }
 
 }  // namespace

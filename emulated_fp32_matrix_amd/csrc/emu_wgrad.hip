@@ -11,21 +11,23 @@
 // the chip's power as the BF16 stream is, so the product runs near their
 // peak.
 //
-// One 256-thread workgroup owns a 128 x 128 tile of dW over one segment of
-// the rows; 4 waves, 64 x 64 each (2 x 2 instructions' tiles, 64 accumulator
-// registers); two workgroups share a CU, so one computes while the other
-// waits at its barrier.  The next slab goes from registers to the other LDS
-// buffer, and the one after it is requested, in quarters between the
-// products: with the copies at the start of a step instead, the wave that
-// the scheduler favours left its neighbour to finish alone, at 0.83 of the
-// matrix unit's cycles (now 0.89; 552,960 x 1024 x 256 in 2,240 us, 129
-// TFLOP/s at the 2.1-2.2 GHz that the chip holds under it).  Reading the two
-// blocks of a wave as neighbouring columns takes one 8-byte LDS read per
-// operand and k instead of two.  The tiles of one segment run on one XCD,
-// whose L2 then serves the segment's rows to all of them.  The workgroups of
-// the first tile column also add up the columns of the dZ rows they copy
-// (no measurable cost).  Segments are written as partial tiles and joined in
-// order by a second launch.
+// A workgroup owns 128 rows x 256 (or 128) columns of dW over one segment of
+// the rows of dZ and X; its 8 (4) waves take 64 x 64 each (2 x 2 instructions'
+// tiles, 64 accumulator registers), two per SIMD (of one workgroup, or of two
+// that share a CU).  The next slab goes from registers to the other LDS
+// buffer, and the one after it is requested, a copy at a time between the
+// products: with the copies at the start of a step instead, the wave that the
+// scheduler favours left its neighbour to finish alone, at 0.83 of the matrix
+// unit's cycles (0.89 spread out).  Reading the two blocks of a wave as
+// neighbouring columns takes one 8-byte LDS read per operand and k instead of
+// two.  256 columns halve the copies of dZ per product and, where dZ is made
+// on the way, its making: 552,960 x 1024 x 256 in 2,090 us against 2,165 with
+// 128 (139 TFLOP/s of 157; the chip holds 2.1-2.2 GHz under it), with the
+// gated product's backward pass 2,530 against 2,920.  The tiles of one
+// segment run on one XCD, whose L2 then serves the segment's rows to all of
+// them.  The workgroups of the first tile column also add up the columns of
+// the dZ rows they copy (no measurable cost).  Segments are written as
+// partial tiles and joined in order by a second launch.
 #include "emu_block_device.h"
 #include "emu_block_launch.h"
 #include "emu_tile.h"
@@ -33,7 +35,6 @@
 namespace emu {
 namespace {
 
-constexpr int SLAB = BK * TILE;   // floats of one operand's slab
 
 // Where the rows of dZ come from: memory (WG_PLAIN), or an activation's
 // backward pass that runs on the way to LDS and also writes dZ for the
@@ -56,41 +57,44 @@ struct WgradArgs {
     int64_t bstride;
 };
 
-template <int SRC, int ACT>
-__global__ __launch_bounds__(256, 2) void wgrad_kernel(WgradArgs p)
+// WN: waves along N (2 or 4), 64 columns of dW each.
+template <int SRC, int ACT, int WN>
+__global__ __launch_bounds__(128 * WN, 2) void wgrad_kernel(WgradArgs p)
 {
+    constexpr int NT = 128 * WN, TN = 64 * WN;
     // columns of dZ per tile and half, 16-byte groups of a row, and copies of
     // a slab per thread
     constexpr int TW = SRC == WG_GATED ? TILE / 2 : TILE;
-    constexpr int PER_ROW = TW / 4, ROWS = 256 / PER_ROW, COPIES = BK / ROWS;
+    constexpr int PER_ROW = TW / 4, ROWS = NT / PER_ROW, COPIES = BK / ROWS;
+    constexpr int X_ROWS = NT / (TN / 4);
+    static_assert(X_ROWS * 4 == BK && ROWS * COPIES == BK, "four copies of X per thread and slab");
     constexpr int HALVES = SRC == WG_GATED ? 2 : 1;
     constexpr int READS = SRC == WG_PLAIN ? 1 : SRC == WG_ACT ? 2 : 3;   // arrays behind dZ
-    __shared__ __attribute__((aligned(16))) float smZ[2][SLAB];
-    __shared__ __attribute__((aligned(16))) float smX[2][SLAB];
+    __shared__ __attribute__((aligned(16))) float smZ[2][BK * TILE];
+    __shared__ __attribute__((aligned(16))) float smX[2][BK * TN];
 
     const int t = threadIdx.x;
     const int lane = t & 63;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
-    const int wm = wave >> 1, wn = wave & 1;
+    const int wm = wave / WN, wn = wave % WN;
 
     const int item = xcd_position(blockIdx.x, gridDim.x);
     const int seg = item / p.tiles;
     const int tile = item - seg * p.tiles;
     const int tm = tile / p.tiles_n, tn = tile - tm * p.tiles_n;
-    const int m0 = tm * TW, n0 = tn * TILE;
+    const int m0 = tm * TW, n0 = tn * TN;
     const int64_t k0 = (int64_t)seg * p.seg_steps * BK;
     int64_t kend = k0 + (int64_t)p.seg_steps * BK;
     if (kend > p.rows) kend = p.rows;
     const int steps = (int)((kend - k0 + BK - 1) / BK);
 
     // Thread t copies columns 4 (t % PER_ROW) .. +3 of rows t / PER_ROW + ROWS
-    // r of a slab of dZ (and of what it is made of), and likewise with 32
-    // groups per row of X.  The buffer descriptors end with the segment's
+    // r of a slab of dZ (and of what it is made of), and likewise of X.  The buffer descriptors end with the segment's
     // last row, so rows past it read as zeros (and are not written); columns
     // past M (N) read what follows in memory, or zeros, and only feed outputs
     // that are not stored.
     const int cr = t / PER_ROW, cc = (t % PER_ROW) * 4;
-    const int xr = t >> 5, xc = (t & 31) * 4;
+    const int xr = t / (TN / 4), xc = (t % (TN / 4)) * 4;
     const int mleft = p.M - m0, nleft = p.N - n0;
     const int zcols = SRC == WG_GATED ? 2 * p.M - m0 : mleft;   // from m0 to the end of Z's row
     u32x4_t rz[READS][COPIES], rx[4];
@@ -121,7 +125,7 @@ __global__ __launch_bounds__(256, 2) void wgrad_kernel(WgradArgs p)
             rz[2][r] = __builtin_amdgcn_raw_buffer_load_b128(bz, offset(p.ldz, r) + (uint32_t)p.M * 4, 0, 0);
     };
     auto load_x = [&](int r) __attribute__((always_inline)) {
-        rx[r] = __builtin_amdgcn_raw_buffer_load_b128(bx, (uint32_t)((xr + 8 * r) * p.ldx + xc) * 4, 0, 0);
+        rx[r] = __builtin_amdgcn_raw_buffer_load_b128(bx, (uint32_t)((xr + X_ROWS * r) * p.ldx + xc) * 4, 0, 0);
     };
     const bool first_n = tn == 0;
     const bool sums = p.db != nullptr && first_n;
@@ -160,7 +164,7 @@ __global__ __launch_bounds__(256, 2) void wgrad_kernel(WgradArgs p)
         }
     };
     auto put_x = [&](int b, int r) __attribute__((always_inline)) {
-        *reinterpret_cast<u32x4_t*>(&smX[b][(xr + 8 * r) * TILE + xc]) = rx[r];
+        *reinterpret_cast<u32x4_t*>(&smX[b][(xr + X_ROWS * r) * TN + xc]) = rx[r];
     };
 
     f32x16_t acc[2][2];
@@ -172,9 +176,12 @@ __global__ __launch_bounds__(256, 2) void wgrad_kernel(WgradArgs p)
     // Block i (j) of a wave's 64 rows (columns) of dW holds the rows 2 l + i
     // of lanes l = 0..31: one 8-byte LDS read then gives both blocks' element.
     const int fz = (lane >> 5) * TILE + wm * 64 + 2 * (lane & 31);
-    const int fx = (lane >> 5) * TILE + wn * 64 + 2 * (lane & 31);
-    auto read = [&](const float* sm, int f, int k) __attribute__((always_inline)) {
-        return *reinterpret_cast<const f32x2_t*>(&sm[k * TILE + f]);
+    const int fx = (lane >> 5) * TN + wn * 64 + 2 * (lane & 31);
+    auto read_z = [&](const float* sm, int k) __attribute__((always_inline)) {
+        return *reinterpret_cast<const f32x2_t*>(&sm[k * TILE + fz]);
+    };
+    auto read_x = [&](const float* sm, int k) __attribute__((always_inline)) {
+        return *reinterpret_cast<const f32x2_t*>(&sm[k * TN + fx]);
     };
     // Slab s is in LDS buffer s % 2.  During its step slab s + 1 goes to the
     // other buffer from the registers it was read to during step s - 1 (with
@@ -208,15 +215,15 @@ __global__ __launch_bounds__(256, 2) void wgrad_kernel(WgradArgs p)
         // the operands of each k pair are read while the one before is
         // multiplied
         f32x2_t a[2], c[2];
-        a[0] = read(sz, fz, 0);
-        c[0] = read(sx, fx, 0);
+        a[0] = read_z(sz, 0);
+        c[0] = read_x(sx, 0);
         aim(s + 2);
         if (SRC != WG_PLAIN) bd = buffer(p.dZ + m0, p.ldd, s + 1, zcols);
 #pragma unroll
         for (int k = 0; k < BK / 2; ++k) {
             if (k + 1 < BK / 2) {
-                a[(k + 1) & 1] = read(sz, fz, 2 * k + 2);
-                c[(k + 1) & 1] = read(sx, fx, 2 * k + 2);
+                a[(k + 1) & 1] = read_z(sz, 2 * k + 2);
+                c[(k + 1) & 1] = read_x(sx, 2 * k + 2);
             }
             if (k % 4 == 2) {
                 put_x(b ^ 1, k / 4);
@@ -333,22 +340,25 @@ __global__ __launch_bounds__(256) void wgrad_join_kernel(const float* __restrict
 }
 
 struct WgradPlan {
+    int wn;           // waves along N
     int64_t tiles_m, tiles_n, tiles;
     int segs, seg_steps;
     int64_t ldp;      // row of a partial result
     int64_t rows_out; // rows of dW
+    double load;      // of the busiest CU, in products of a 128-column tile and slab
 };
 
-// Segments: the load of the busiest CU is ceil(tiles * segs / 256) segment
-// tiles of ceil(steps / segs) slabs; the fewest segments within 5 % of the
-// least load, 128 at most and 4 slabs each at least.
-WgradPlan plan_wgrad(int64_t rows, int64_t M, int64_t N, bool gated)
+// Segments for tiles of 64 wn columns: the load of the busiest CU is ceil(tiles
+// * segs / 256) segment tiles of ceil(steps / segs) slabs; the fewest segments
+// within 5 % of the least load, 128 at most and 4 slabs each at least.
+WgradPlan plan_wgrad(int64_t rows, int64_t M, int64_t N, bool gated, int wn)
 {
     WgradPlan p;
-    const int64_t tw = gated ? TILE / 2 : TILE;
+    p.wn = wn;
+    const int64_t tw = gated ? TILE / 2 : TILE, tn = 64 * wn;
     p.rows_out = gated ? 2 * M : M;
     p.tiles_m = (M + tw - 1) / tw;
-    p.tiles_n = N > 0 ? (N + TILE - 1) / TILE : 1;
+    p.tiles_n = N > 0 ? (N + tn - 1) / tn : 1;
     p.tiles = p.tiles_m * p.tiles_n;
     const int64_t steps = (rows + BK - 1) / BK;
     int64_t most = steps / 4;
@@ -356,15 +366,17 @@ WgradPlan plan_wgrad(int64_t rows, int64_t M, int64_t N, bool gated)
     if (most < 1) most = 1;
     auto load = [&](int64_t s) {
         const int64_t items = p.tiles * s, per = (steps + s - 1) / s;
-        // (two workgroups per CU hide each other's waits: one alone takes
-        // about a quarter longer per slab)
-        return (double)((items + 255) / 256) * (double)per * (items <= 256 ? 1.25 : 1.0) + 0.25 * (double)s;
+        // (two workgroups of 128 columns share a CU and hide each other's
+        // waits: one alone takes about a quarter longer per slab)
+        const double slab = wn == 4 ? 2.0 : items <= 256 ? 1.25 : 1.0;
+        return (double)((items + 255) / 256) * (double)per * slab + 0.25 * (double)s;
     };
     double best = load(1);
     for (int64_t s = 2; s <= most; ++s)
         if (load(s) < best) best = load(s);
     int64_t segs = 1;
     while (segs < most && load(segs) > 1.05 * best) ++segs;
+    p.load = load(segs);
     p.seg_steps = (int)((steps + segs - 1) / segs);
     if (p.seg_steps < 1) p.seg_steps = 1;
     p.segs = (int)((steps + p.seg_steps - 1) / p.seg_steps);
@@ -373,10 +385,20 @@ WgradPlan plan_wgrad(int64_t rows, int64_t M, int64_t N, bool gated)
     return p;
 }
 
-template <int SRC>
+WgradPlan plan_wgrad(int64_t rows, int64_t M, int64_t N, bool gated)
+{
+    const WgradPlan narrow = plan_wgrad(rows, M, N, gated, 2);
+    if (N <= 128) return narrow;
+    const WgradPlan wide = plan_wgrad(rows, M, N, gated, 4);
+    return wide.load <= narrow.load ? wide : narrow;
+}
+
+template <int SRC, int WN>
 void launch_src(int act, int grid, const WgradArgs& a, hipStream_t s)
 {
-    auto go = [&]<int ACT>() { hipLaunchKernelGGL((wgrad_kernel<SRC, ACT>), dim3(grid), dim3(256), 0, s, a); };
+    auto go = [&]<int ACT>() {
+        hipLaunchKernelGGL((wgrad_kernel<SRC, ACT, WN>), dim3(grid), dim3(128 * WN), 0, s, a);
+    };
     if constexpr (SRC == WG_PLAIN) {
         go.template operator()<EMU_ACT_IDENTITY>();
     } else {
@@ -439,12 +461,18 @@ hipError_t launch_wgrad(int64_t rows, int64_t M, int64_t N, const WgradSource& s
         a.db = db;
     }
     const int grid = (int)(pl.tiles * pl.segs);
-    if (src.gated)
-        launch_src<WG_GATED>(src.act, grid, a, s);
-    else if (src.dY != nullptr)
-        launch_src<WG_ACT>(src.act, grid, a, s);
+    auto launch = [&]<int WN>() {
+        if (src.gated)
+            launch_src<WG_GATED, WN>(src.act, grid, a, s);
+        else if (src.dY != nullptr)
+            launch_src<WG_ACT, WN>(src.act, grid, a, s);
+        else
+            launch_src<WG_PLAIN, WN>(0, grid, a, s);
+    };
+    if (pl.wn == 4)
+        launch.template operator()<4>();
     else
-        launch_src<WG_PLAIN>(0, grid, a, s);
+        launch.template operator()<2>();
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && pl.segs > 1) {
         const int64_t work = pl.rows_out * (pl.ldp / 4) + (db != nullptr ? bstride / 4 : 0);
