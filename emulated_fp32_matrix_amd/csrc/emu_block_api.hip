@@ -4,6 +4,8 @@
 // the caller.
 #include <hip/hip_runtime.h>
 
+#include <cmath>
+
 #include "emu_block.h"
 #include "emu_block_launch.h"
 
@@ -51,19 +53,28 @@ int bands_of(emu_mode_t mode)
 
 // Where EMU_MODE_AUTO takes the one-launch FP32 kernel: where it is predicted
 // faster than what emu_sgemm's AUTO runs with the epilogue.  Its time is a
-// launch and, per workgroup of a CU (64 rows x 16 columns), a latency and K;
-// measured over ten (K, N) and M = 1 .. 6,144 (us, this kernel / the emulated
-// one): 6,144 x 64 x 64 5.2 / 11.8, 1 x 512 x 256 3.6 / 12.1, 2,048 x 512 x 256
-// 14.4 / 17.7, 4,096 x 512 x 256 27.4 / 19.2, 512 x 1024 x 1024 23.6 / 30.8,
-// 1,024 x 1024 x 1024 44.4 / 40.1, 16 x 1024 x 4096 16.6 / 47.2, 64 x 1024 x
-// 4096 41.1 / 46.3.  The model picks the faster one but where the two are
-// within a tenth of each other.
-bool few_rows(int64_t M, int64_t N, int64_t K)
+// launch and, per workgroup of a CU, a latency and K; a workgroup has 64 rows
+// (or 32, 16) and 16 columns, or 32 where that still leaves every CU one and
+// in a gated projection (launch_rows_gemm).  Fitted to ten (K, N) and M = 1
+// .. 6,144, within a tenth of the measured times; the slower of the two was
+// taken only where they are as near.  Measured (us, this kernel / the emulated
+// one with AUTO's plan): 1 x 512 x 256 3.6 / 12.1, 6,144 x 64 x 64 5.2 / 11.8,
+// 2,048 x 512 x 256 12.1 / 17.7, 4,096 x 512 x 256 27.4 / 19.2, 512 x 1024 x
+// 1024 19.8 / 30.8, 1,024 x 1024 x 1024 44.4 / 40.1, 16 x 1024 x 4096 16.6 /
+// 47.2, 64 x 1024 x 4096 41.1 / 46.3.
+bool few_rows(int64_t M, int64_t N, int64_t K, bool is_gated)
 {
     if (M == 0 || N == 0 || K == 0 || M > ((int64_t)1 << 20)) return false;
-    const double groups = (double)((M + 63) / 64) * (double)((N + 15) / 16) / 256.0;
-    const double per_k = M <= 16 ? 0.0034 : M <= 32 ? 0.0057 : 0.0094;
-    const double us = 2.4 + (groups < 1.0 ? 1.0 : groups) * (0.75 + per_k * (double)K);
+    const double m64 = (double)((M + 63) / 64), n32 = (double)((N + 31) / 32), n16 = (double)((N + 15) / 16);
+    double us;
+    if (M > 32 && (is_gated || m64 * n32 >= 256.0)) {
+        const double rounds = std::ceil(m64 * n32 / 256.0);
+        us = 2.3 + rounds * (0.9 + 0.0162 * (double)K);
+    } else {
+        const double groups = m64 * n16 / 256.0;
+        const double per_k = M <= 16 ? 0.0034 : M <= 32 ? 0.0057 : 0.0094;
+        us = 2.4 + (groups < 1.0 ? 1.0 : groups) * (0.75 + per_k * (double)K);
+    }
     // (the library's model leaves out the traffic of the weights' split: 10
     // bytes per element)
     return us < emu::api_predict_us(M, N, K) + 10.0 * (double)N * (double)K / 4.0e6;
@@ -97,11 +108,11 @@ emu::GemmArgs with_copy(emu::GemmArgs g, const float* copy, int64_t ld)
 const float* const kSomeRows = reinterpret_cast<const float*>((uintptr_t)256);
 
 // N: columns of the product (gated: 2 F).
-Route route_of(const emu::GemmArgs& g, emu_mode_t mode, bool have_planes, int num_cu)
+Route route_of(const emu::GemmArgs& g, bool is_gated, emu_mode_t mode, bool have_planes, int num_cu)
 {
     Route r{};
     const bool automatic = mode == EMU_MODE_AUTO;
-    r.rows = g.K == 0 || (automatic && !have_planes && few_rows(g.M, g.N, g.K));
+    r.rows = g.K == 0 || (automatic && !have_planes && few_rows(g.M, g.N, g.K, is_gated));
     if (r.rows) return r;
     r.mode = !automatic ? mode : have_planes ? EMU_MODE_BF16X9 : (emu_mode_t)emu::api_select_mode(g.M, g.N, g.K);
     if (r.mode == EMU_MODE_NATIVE_F32) {
@@ -156,7 +167,7 @@ emu_status_t product(emu::GemmArgs g, int64_t n_out, const BlockEpilogue& ep, em
 {
     emu::DeviceInfo dev;
     if (!emu::api_current_device(dev)) return EMU_STATUS_NOT_SUPPORTED;
-    const Route r = route_of(g, mode, g.Bplanes != nullptr, dev.num_cu);
+    const Route r = route_of(g, ep.gated != 0, mode, g.Bplanes != nullptr, dev.num_cu);
     if (r.rows)
         return from_hip(emu::launch_rows_gemm(g.trans_b, g.M, n_out, g.K, g.A, g.lda, g.B, g.ldb, ep, s));
     if (bad_workspace(ws, ws_bytes, r.gemm_bytes + r.more_bytes)) return EMU_STATUS_INVALID_VALUE;
@@ -179,11 +190,12 @@ emu_status_t product(emu::GemmArgs g, int64_t n_out, const BlockEpilogue& ep, em
     return from_hip(e);
 }
 
-emu_status_t product_workspace(const emu::GemmArgs& g, emu_mode_t mode, bool have_planes, size_t* bytes)
+emu_status_t product_workspace(const emu::GemmArgs& g, bool is_gated, emu_mode_t mode, bool have_planes,
+                               size_t* bytes)
 {
     *bytes = 0;
     if (g.M == 0 || g.N == 0) return EMU_STATUS_SUCCESS;
-    const Route r = route_of(g, mode, have_planes, query_cus());
+    const Route r = route_of(g, is_gated, mode, have_planes, query_cus());
     if (!r.rows) *bytes = r.gemm_bytes + r.more_bytes;
     return EMU_STATUS_SUCCESS;
 }
@@ -308,7 +320,7 @@ emu_status_t emu_act_backward2(int64_t rows, int64_t cols, const float* v, int64
 emu_status_t emu_sgemm_act_route(emu_op_t transB, int64_t M, int64_t N, int64_t K, int* few)
 {
     if (!valid_op(transB) || M < 0 || N < 0 || K < 0 || few == nullptr) return EMU_STATUS_INVALID_VALUE;
-    *few = few_rows(M, N, K) ? 1 : 0;
+    *few = few_rows(M, N, K, false) ? 1 : 0;
     return EMU_STATUS_SUCCESS;
 }
 
@@ -320,7 +332,7 @@ emu_status_t emu_sgemm_act_workspace(emu_op_t transB, int64_t M, int64_t N, int6
         return EMU_STATUS_INVALID_VALUE;
     return product_workspace(gemm_args(transB == EMU_OP_T, M, N, K, A, lda, nullptr, 0,
                                        has_planes ? kSomePlanes : nullptr),
-                             mode, has_planes != 0, bytes);
+                             false, mode, has_planes != 0, bytes);
 }
 
 emu_status_t emu_sgemm_act(emu_op_t transB, int64_t M, int64_t N, int64_t K, const float* A, int64_t lda,
@@ -351,7 +363,7 @@ emu_status_t emu_sgemm_gated_workspace(int64_t M, int64_t F, int64_t K, const fl
         (has_planes && mode == EMU_MODE_NATIVE_F32) || F > kMaxCols)
         return EMU_STATUS_INVALID_VALUE;
     return product_workspace(gemm_args(true, M, 2 * F, K, A, lda, nullptr, 0, has_planes ? kSomePlanes : nullptr),
-                             mode, has_planes != 0, bytes);
+                             true, mode, has_planes != 0, bytes);
 }
 
 emu_status_t emu_sgemm_gated(int64_t M, int64_t F, int64_t K, const float* A, int64_t lda, const float* W,

@@ -353,7 +353,7 @@ def test_planes_bitwise(mode):
 
 
 # (M, N, K): every tile split, the last round split, 64- and 128-row tiles, none
-@pytest.mark.parametrize("M,N,K", [(6144, 1024, 1024), (768, 512, 4096), (700, 640, 2048), (3300, 1200, 512), (9000, 260, 96)])
+@pytest.mark.parametrize("M,N,K", [(6144, 1024, 1024), (768, 512, 4096), (700, 640, 2048), (3300, 1200, 512), (2000, 640, 2048), (20000, 260, 160)])
 def test_auto_plans(M, N, K):
     """The K split plans of AUTO with the fused epilogues: bit for bit
     emu_sgemm's product where the epilogue adds one rounding, and the gated
