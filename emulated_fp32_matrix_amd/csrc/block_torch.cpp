@@ -129,7 +129,11 @@ bool wants_grad(std::initializer_list<const Tensor*> ts)
 void claim_leaves(const OnDevice& on, std::initializer_list<const Tensor*> ts)
 {
     hipStreamCaptureStatus status = hipStreamCaptureStatusNone;
-    if (hipStreamIsCapturing(on.stream, &status) != hipSuccess || status == hipStreamCaptureStatusNone) return;
+    if (hipStreamIsCapturing(on.stream, &status) != hipSuccess) {
+        (void)hipGetLastError();   // (must not surface in a later launch check)
+        return;
+    }
+    if (status == hipStreamCaptureStatusNone) return;
     for (const Tensor* t : ts) {
         if (!t->defined() || !t->requires_grad() || !t->is_leaf()) continue;
         const auto node = torch::autograd::impl::try_get_grad_accumulator(*t);

@@ -39,6 +39,9 @@ hipStream_t stream_of(void* s) { return static_cast<hipStream_t>(s); }
 
 // Columns of the element-wise passes are indexed with 32 bits.
 constexpr int64_t kMaxCols = (int64_t)1 << 30;
+// The emulated kernel addresses a tile's 128 rows of A with 32-bit byte
+// offsets.
+constexpr int64_t kMaxK = ((int64_t)1 << 23) - 4;
 
 int bands_of(emu_mode_t mode)
 {
@@ -347,7 +350,7 @@ emu_status_t emu_sgemm_act(emu_op_t transB, int64_t M, int64_t N, int64_t K, con
         bad_array(C, M, N, ldc) || bad_optional(Z, N, ldz) || bad_optional(R, N, ldr) || bad_planes(planes, mode) ||
         (has_c && K > 0 && (A == nullptr || (B == nullptr && planes == nullptr))))
         return EMU_STATUS_INVALID_VALUE;
-    if (N > kMaxCols || K > kMaxCols) return EMU_STATUS_NOT_SUPPORTED;
+    if (N > kMaxCols || K > kMaxK) return EMU_STATUS_NOT_SUPPORTED;
     if (!has_c) return EMU_STATUS_SUCCESS;
     const BlockEpilogue ep{(int)act, 0, bias, Z, ldz, R, ldr, C, ldc};
     return product(gemm_args(transB == EMU_OP_T, M, N, K, A, lda, B, ldb, planes), N, ep, mode, workspace,
@@ -372,7 +375,7 @@ emu_status_t emu_sgemm_gated(int64_t M, int64_t F, int64_t K, const float* A, in
                              size_t workspace_bytes, void* stream)
 {
     if (!valid_mode(mode) || !valid_act(act) || M < 0 || F < 0 || K < 0) return EMU_STATUS_INVALID_VALUE;
-    if (F > kMaxCols || K > kMaxCols) return EMU_STATUS_NOT_SUPPORTED;
+    if (F > kMaxCols || K > kMaxK) return EMU_STATUS_NOT_SUPPORTED;
     const bool has_c = M > 0 && F > 0;
     if (lda < max1(K) || (planes == nullptr && ldw < max1(K)) || bad_array(C, M, F, ldc) ||
         bad_optional(Z, 2 * F, ldz) || bad_planes(planes, mode) ||

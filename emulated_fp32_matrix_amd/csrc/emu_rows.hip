@@ -154,16 +154,26 @@ void launch(int64_t M, int64_t N, int64_t K, const float* A, int64_t lda, const 
 hipError_t launch_rows_gemm(bool trans_b, int64_t M, int64_t N, int64_t K, const float* A, int64_t lda,
                             const float* B, int64_t ldb, const BlockEpilogue& ep, hipStream_t s)
 {
-    // (gridDim.y holds the row blocks)
-    if ((M + 63) / 64 > 65535 || 2 * N >= ((int64_t)1 << 31) || K >= ((int64_t)1 << 30) || (ep.gated && !trans_b))
-        return hipErrorInvalidValue;
-    if (ep.gated)
-        launch<true, true>(M, N, K, A, lda, B, ldb, ep, s);
-    else if (trans_b)
-        launch<true, false>(M, N, K, A, lda, B, ldb, ep, s);
-    else
-        launch<false, false>(M, N, K, A, lda, B, ldb, ep, s);
-    return hipGetLastError();
+    if (2 * N >= ((int64_t)1 << 31) || K >= ((int64_t)1 << 30) || (ep.gated && !trans_b)) return hipErrorInvalidValue;
+    // (gridDim.y holds the row blocks: 65,535 of 64 at most per launch)
+    const int64_t most = (int64_t)65535 * 64;
+    for (int64_t m = 0; m < M; m += most) {
+        const int64_t rows = M - m < most ? M - m : most;
+        BlockEpilogue e = ep;
+        e.C = ep.C + m * ep.ldc;
+        if (ep.Z != nullptr) e.Z = ep.Z + m * ep.ldz;
+        if (ep.R != nullptr) e.R = ep.R + m * ep.ldr;
+        const float* a = A != nullptr ? A + m * lda : nullptr;   // (null with K = 0)
+        if (ep.gated)
+            launch<true, true>(rows, N, K, a, lda, B, ldb, e, s);
+        else if (trans_b)
+            launch<true, false>(rows, N, K, a, lda, B, ldb, e, s);
+        else
+            launch<false, false>(rows, N, K, a, lda, B, ldb, e, s);
+        const hipError_t r = hipGetLastError();
+        if (r != hipSuccess) return r;
+    }
+    return hipSuccess;
 }
 
 }  // namespace emu

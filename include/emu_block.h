@@ -136,7 +136,8 @@ emu_status_t emu_act_backward2(int64_t rows, int64_t cols, const float* v, int64
  * ldb are not read.  NULL: the call splits op(B) into the workspace.
  * K == 0: z = bias.  M == 0 or N == 0: nothing is done.
  * Errors: EMU_STATUS_INVALID_VALUE as emu_sgemm_ex and for a bad act, NULL
- * required pointers or leading dimensions below their bounds.
+ * required pointers or leading dimensions below their bounds;
+ * EMU_STATUS_NOT_SUPPORTED for K above 8,388,604 or N above 2^30.
  */
 emu_status_t emu_sgemm_act_workspace(emu_op_t transB, int64_t M, int64_t N, int64_t K, const float* A,
                                      int64_t lda, int has_planes, emu_mode_t mode, size_t* bytes);

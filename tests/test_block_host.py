@@ -126,6 +126,15 @@ def test_wide_layer_norm_not_supported():
     assert lib.emu_layer_norm_backward_workspace(4, wide, ctypes.byref(out)) == UNSUPPORTED
 
 
+def test_long_inner_dimension_not_supported():
+    k = 1 << 23
+    assert lib.emu_sgemm_act(1, 4, 6, k, FAKE, k, FAKE, k, None, None, 1, None, 6, None, 6, FAKE, 6, 1, None, 0, None) == UNSUPPORTED
+    assert lib.emu_sgemm_gated(4, 6, k, FAKE, k, FAKE, k, None, None, 1, None, 12, FAKE, 6, 1, None, 0, None) == UNSUPPORTED
+    ld = 1 << 24
+    assert lib.emu_wgrad(64, 6, 8, FAKE, ld, FAKE, 8, FAKE, 8, None, None, 0, None) == UNSUPPORTED
+    assert lib.emu_wgrad(64, 6, 8, FAKE, 6, FAKE, ld, FAKE, 8, None, None, 0, None) == UNSUPPORTED
+
+
 def _bytes(fn, *args):
     out = ctypes.c_size_t(0)
     assert fn(*args, ctypes.byref(out)) == 0

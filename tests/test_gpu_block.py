@@ -621,6 +621,61 @@ def test_streams_and_interleaved_calls():
             assert all(torch.equal(a, b) for a, b in zip(one, got))
 
 
+def test_host_threads_at_once():
+    """Training steps from four host threads, each on its own stream: the
+    gradients of the steps alone."""
+    import threading
+
+    block = _block()
+    torch.manual_seed(5)
+    ffns = [block.EmuGatedFFN(64, 96, device="cuda:0") for _ in range(4)]
+    xs = [_randn(i, 150 + 400 * i, 64) for i in range(4)]
+
+    def step(i):
+        x = xs[i].clone().requires_grad_(True)
+        y = ffns[i](x)
+        return [t.detach() for t in (y, *torch.autograd.grad((y * y).sum(), [x, *ffns[i].parameters()]))]
+
+    alone = [step(i) for i in range(4)]
+    torch.cuda.synchronize()
+    got, failed = [None] * 4, []
+
+    def work(i):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                for _ in range(5):
+                    got[i] = step(i)
+            s.synchronize()
+        except Exception as e:   # noqa: BLE001 (reported by the main thread)
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
+    for a, b in zip(alone, got):
+        assert all(torch.equal(u, v) for u, v in zip(a, b))
+
+
+def test_one_tensor_in_several_places():
+    """x as input and residual, one weight in two layers: their gradients add
+    up."""
+    block = _block()
+    x, w = _randn(1, 200, 64).requires_grad_(True), _randn(2, 64, 64, scale=0.125).requires_grad_(True)
+    g = _randn(3, 200, 64)
+    y = block.linear_act(block.linear_act(x, w, None, "silu", x), w, None, "tanh", x)
+    dx, dw = torch.autograd.grad(y, (x, w), g)
+    x64, w64 = x.detach().double().requires_grad_(True), w.detach().double().requires_grad_(True)
+    f = lambda t, name: ref.act(name, t @ w64.t()) + x64
+    wx, ww = torch.autograd.grad(f(f(x64, "silu"), "tanh"), (x64, w64), g.double())
+    # two layers of products of 64 terms: each relative error near 1e-7
+    for got, want in ((dx, wx), (dw, ww)):
+        assert float((got.double() - want).norm() / want.norm()) <= 2e-6
+
+
 def test_graphs_replay_and_share_nothing():
     """Two captured graphs (inference, and a training step's forward and
     backward) replayed in turn, on two streams, with eager work between: each
