@@ -83,11 +83,18 @@ bool few_rows(int64_t M, int64_t N, int64_t K, bool is_gated)
     return us < emu::api_predict_us(M, N, K) + 10.0 * (double)N * (double)K / 4.0e6;
 }
 
+// Where an explicit emulated mode takes the one-launch kernel (the same bits).
+bool few_tiles(int64_t M, int64_t N, int64_t K, int bands, bool have_planes)
+{
+    return (M + 31) / 32 * ((N + 31) / 32) <= 4096;
+}
+
 size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // How one product with its epilogue runs.
 struct Route {
     bool rows;                 // the one-launch FP32 kernel
+    bool few;                  // the one-launch emulated kernel, in
     emu_mode_t mode;           // else: the product's mode,
     emu::GemmPlan plan;        // its plan,
     size_t gemm_bytes;         // and the workspace: the product's own, then
@@ -118,6 +125,8 @@ Route route_of(const emu::GemmArgs& g, bool is_gated, emu_mode_t mode, bool have
     r.rows = g.K == 0 || (automatic && !have_planes && few_rows(g.M, g.N, g.K, is_gated));
     if (r.rows) return r;
     r.mode = !automatic ? mode : have_planes ? EMU_MODE_BF16X9 : (emu_mode_t)emu::api_select_mode(g.M, g.N, g.K);
+    r.few = !automatic && bands_of(r.mode) != 0 && few_tiles(g.M, g.N, g.K, bands_of(r.mode), have_planes);
+    if (r.few) return r;
     if (r.mode == EMU_MODE_NATIVE_F32) {
         r.gemm_bytes = round256(emu::gemm_native_f32_workspace_bytes(g));
         r.ld = (g.N + 3) & ~(int64_t)3;
@@ -173,6 +182,9 @@ emu_status_t product(emu::GemmArgs g, int64_t n_out, const BlockEpilogue& ep, em
     const Route r = route_of(g, ep.gated != 0, mode, g.Bplanes != nullptr, dev.num_cu);
     if (r.rows)
         return from_hip(emu::launch_rows_gemm(g.trans_b, g.M, n_out, g.K, g.A, g.lda, g.B, g.ldb, ep, s));
+    if (r.few)
+        return from_hip(emu::launch_few_gemm(bands_of(r.mode), g.trans_b, g.M, n_out, g.K, g.A, g.lda, g.B, g.ldb,
+                                             g.Bplanes, ep, s));
     if (bad_workspace(ws, ws_bytes, r.gemm_bytes + r.more_bytes)) return EMU_STATUS_INVALID_VALUE;
     float* more = reinterpret_cast<float*>(static_cast<char*>(ws) + r.gemm_bytes);
     void* gws = r.gemm_bytes > 0 ? ws : nullptr;

@@ -80,6 +80,11 @@ hipError_t launch_gated_backward2(int64_t M, int64_t F, const float* V, int64_t 
 hipError_t launch_rows_gemm(bool trans_b, int64_t M, int64_t N, int64_t K, const float* A, int64_t lda,
                             const float* B, int64_t ldb, const BlockEpilogue& ep, hipStream_t s);
 
+// The emulated product (nbands of the mode) and its epilogue in one launch, for
+// few rows, from B as above or from its planes.
+hipError_t launch_few_gemm(int nbands, bool trans_b, int64_t M, int64_t N, int64_t K, const float* A, int64_t lda,
+                           const float* B, int64_t ldb, const uint16_t* planes, const BlockEpilogue& ep, hipStream_t s);
+
 // Leading dimensions of the weight-gradient product: its 32-row slabs are
 // addressed with 32-bit byte offsets.
 constexpr int64_t kWgradMaxLd = ((int64_t)1 << 31) / (4 * 32) - 128;
