@@ -86,7 +86,7 @@ bool few_rows(int64_t M, int64_t N, int64_t K, bool is_gated)
 // Where an explicit emulated mode takes the one-launch kernel (the same bits).
 bool few_tiles(int64_t M, int64_t N, int64_t K, int bands, bool have_planes)
 {
-    return (M + 31) / 32 * ((N + 31) / 32) <= 4096;
+    return K >= 4 && N >= 4 && (M + 31) / 32 * ((N + 31) / 32) <= 4096;
 }
 
 size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }

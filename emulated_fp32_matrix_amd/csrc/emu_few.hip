@@ -23,13 +23,14 @@ namespace {
 
 constexpr int FT = 32;                   // rows and columns of a workgroup's tile
 constexpr int FPS = FT * LDS_ROW;        // elements per plane of 32 rows x 32 k
-constexpr int kFeeders = 256;            // threads that load and split
+constexpr int kGroups = 2;               // groups of 256 threads that load and split
+constexpr int kFeeders = 256 * kGroups;
 
 // Where the B operand comes from.
 enum { FB_ROWS = 0, FB_COLS = 1, FB_PLANES = 2 };   // N x K, K x N, planes
 
 template <int NB, int KC, int SRC, bool GATED>
-__global__ __launch_bounds__(512) void few_gemm_kernel(int64_t M, int N, int K, const float* __restrict__ A,
+__global__ __launch_bounds__(256 + kFeeders) void few_gemm_kernel(int64_t M, int N, int K, const float* __restrict__ A,
                                                        int64_t lda, const float* __restrict__ B, int64_t ldb,
                                                        const uint16_t* __restrict__ planes, BlockEpilogue ep)
 {
@@ -102,93 +103,100 @@ __global__ __launch_bounds__(512) void few_gemm_kernel(int64_t M, int N, int K, 
         for (int c = 0; c <= chunks; ++c) __syncthreads();
     };
     auto feed = [&]() __attribute__((always_inline)) {
-        // 16-byte loads of B per thread and chunk
-        constexpr int PB = SRC == FB_PLANES ? S * NP * FPS * 2 / (16 * kFeeders) : S;
-        static_assert(S % 2 == 0, "pairs of k of a K x N operand; planes in whole rounds");
+        // quads of A and 16-byte loads of B per thread and chunk
+        constexpr int PA = S / kGroups;
+        constexpr int PB = SRC == FB_PLANES ? S * NP * FPS * 2 / (16 * kFeeders) : PA;
+        static_assert(PA % 2 == 0 && PA * kGroups == S, "pairs of k of a K x N operand; planes in whole rounds");
         struct Chunk {
-            f32x4_t a[S];
+            f32x4_t a[PA];
             f32x4_t b[PB];
         };
-        const int f = t - kFeeders;
+        const int f = t - 256;
         const int nk = (K + BK - 1) / BK;
-        const int row = f >> 3, kq = (f & 7) * 4;
-        // rows and columns past the end repeat the last one; they are not stored
+        const int grp = f >> 8, row = (f & 255) >> 3, kq = (f & 7) * 4;
+        // a thread's quad j of A (and of an N x K operand) is row `row`, from
+        // this k of the chunk on
+        auto k_of = [&](int j) __attribute__((always_inline)) { return 32 * (kGroups * j + grp) + kq; };
+        // of a K x N operand: columns nq .. nq + 3 of this k, and of the next
+        // with the next j
+        const int pair = 2 * (f >> 3), nq = n0 + kq;
+        auto kn_of = [&](int j) __attribute__((always_inline)) { return 64 * kGroups * (j >> 1) + pair + (j & 1); };
+        // rows and columns past the end repeat the last ones; they are not stored
         const float* arow = A + (m0 + row < M ? m0 + row : M - 1) * lda;
-        const float* brow = nullptr;
-        int64_t ldk = 0;
-        int pair = 0, nq = 0;
+        const float* brow = B;
         if constexpr (SRC == FB_ROWS) {
             int64_t n = n0 + (GATED ? row & 15 : row);
             if (n >= N) n = N - 1;
             brow = B + (n + (GATED && row >= 16 ? N : 0)) * ldb;
-        } else if constexpr (SRC == FB_COLS) {
-            pair = 2 * row;   // two k's, four columns
-            nq = n0 + kq;
-            brow = B;
-            ldk = ldb;
         }
-        // The loads carry no branches between lanes, which would make them
-        // wait for one another, and no selects: what lies behind K reads
-        // the last element again and is cleared when it is split.
-        auto quad_at = []<bool WHOLE>(const float* row, int i, int n) __attribute__((always_inline)) {
-            f32x4_t v;
-            if constexpr (WHOLE) {
-                v = *reinterpret_cast<const f32x4u_t*>(row + i);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = row[i + e < n ? i + e : n - 1];
-            }
-            return v;
+        // The same loads in every chunk: no branches and no masks, which would
+        // make them wait for one another.  A quad that crosses K (or N, of
+        // a K x N operand) is read from K - 4 on instead and moved up when
+        // it is split (up4); K and, there, N are 4 or more.
+        auto quad_at = [](const float* row, int i, int n) __attribute__((always_inline)) {
+            return (f32x4_t)*reinterpret_cast<const f32x4u_t*>(row + (i < n - 4 ? i : n - 4));
         };
-        const bool full = SRC != FB_COLS || n0 + FT <= N;
-        auto fetch = [&]<bool WHOLE>(int k0, Chunk& v) __attribute__((always_inline)) {
+        // Elements i .. i + 3 of a row of n from the quad read for them;
+        // zeros behind n.
+        auto up4 = [](f32x4_t v, int i, int n) __attribute__((always_inline)) {
+            const int d = i - (n - 4);   // up by d, if positive
+            const bool one = d > 0 && (d & 1) != 0, two = d > 0 && (d & 2) != 0, out = d >= 4;
+            f32x4_t r;
 #pragma unroll
-            for (int s = 0; s < S; ++s) v.a[s] = quad_at.template operator()<WHOLE>(arow, k0 + 32 * s + kq, K);
-            if constexpr (SRC == FB_ROWS) {
+            for (int e = 0; e < 4; ++e) v[e] = one ? (e < 3 ? v[e < 3 ? e + 1 : 3] : 0.0f) : v[e];
 #pragma unroll
-                for (int s = 0; s < S; ++s) v.b[s] = quad_at.template operator()<WHOLE>(brow, k0 + 32 * s + kq, K);
-            } else if constexpr (SRC == FB_COLS) {
-#pragma unroll
-                for (int j = 0; j < S; ++j) {
-                    const int k = k0 + 64 * (j >> 1) + pair + (j & 1);
-                    v.b[j] = quad_at.template operator()<WHOLE>(brow + (WHOLE || k < K ? k : K - 1) * ldk, nq, N);
-                }
+            for (int e = 0; e < 4; ++e) {
+                const float x = two ? (e < 2 ? v[e < 2 ? e + 2 : 3] : 0.0f) : v[e];
+                r[e] = out ? 0.0f : x;
             }
+            return r;
         };
         auto load = [&](int c, Chunk& v) __attribute__((always_inline)) {
-            // (past the end chunk 0 again: a load that may be left out would
-            // make the wait for the one before it a wait for both)
-            if (c >= chunks) c = 0;
             const int k0 = c * KC;
-            if (full && k0 + KC <= K)
-                fetch.template operator()<true>(k0, v);
-            else
-                fetch.template operator()<false>(k0, v);
-            if constexpr (SRC == FB_PLANES) {
+#pragma unroll
+            for (int j = 0; j < PA; ++j) v.a[j] = quad_at(arow, k0 + k_of(j), K);
+            if constexpr (SRC == FB_ROWS) {
+#pragma unroll
+                for (int j = 0; j < PB; ++j) v.b[j] = quad_at(brow, k0 + k_of(j), K);
+            } else if constexpr (SRC == FB_COLS) {
+#pragma unroll
+                for (int j = 0; j < PB; ++j) {
+                    const int k = k0 + kn_of(j);
+                    v.b[j] = quad_at(brow + (k < K ? k : K - 1) * ldb, nq, N);
+                }
+            } else {
 #pragma unroll
                 for (int j = 0; j < PB; ++j) {
                     const int e = (j * kFeeders + f) * 8;   // element of the chunk's S x NP planes
                     const int s = e / (NP * FPS), r = e % (NP * FPS);
-                    const int kt = c * S + s;
-                    v.b[j] = kt >= nk ? f32x4_t{}
-                                      : *reinterpret_cast<const f32x4_t*>(
-                                            planes + (((int64_t)(tn >> 2) * nk + kt) * NP + r / FPS) * PS +
-                                            (tn & 3) * FPS + r % FPS);
+                    const int kt = c * S + s < nk ? c * S + s : nk - 1;
+                    v.b[j] = *reinterpret_cast<const f32x4_t*>(
+                        planes + (((int64_t)(tn >> 2) * nk + kt) * NP + r / FPS) * PS + (tn & 3) * FPS + r % FPS);
                 }
             }
         };
         auto put = [&](int c, Chunk& v, uint16_t* buf) __attribute__((always_inline)) {
             if (c >= chunks) return;
-            if (c * KC + KC > K) {
-                const int left = K - c * KC;
+            const int k0 = c * KC;
+            if (k0 + KC > K) {
 #pragma unroll
-                for (int s = 0; s < S; ++s)
+                for (int j = 0; j < PA; ++j) v.a[j] = up4(v.a[j], k0 + k_of(j), K);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if (32 * s + kq + e >= left) v.a[s][e] = 0.0f;
-                        if (SRC == FB_ROWS && 32 * s + kq + e >= left) v.b[s][e] = 0.0f;
-                        if (SRC == FB_COLS && 64 * (s >> 1) + pair + (s & 1) >= left) v.b[s][e] = 0.0f;
+                for (int j = 0; j < PB; ++j) {
+                    if constexpr (SRC == FB_ROWS) {
+                        v.b[j] = up4(v.b[j], k0 + k_of(j), K);
+                    } else {
+                        // (a row of a K x N operand, or a 32-wide piece of planes)
+                        const bool inside =
+                            SRC == FB_COLS ? k0 + kn_of(j) < K : c * S + (j * kFeeders + f) * 8 / (NP * FPS) < nk;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) v.b[j][e] = inside ? v.b[j][e] : 0.0f;
                     }
+                }
+            }
+            if (SRC == FB_COLS && n0 + FT > N) {
+#pragma unroll
+                for (int j = 0; j < PB; ++j) v.b[j] = up4(v.b[j], nq, N);
             }
             auto quad = [&](f32x4_t x, uint16_t* dst) __attribute__((always_inline)) {
                 uint32_t w0[NP], w1[NP];
@@ -198,14 +206,14 @@ __global__ __launch_bounds__(512) void few_gemm_kernel(int64_t M, int N, int K, 
                 for (int pl = 0; pl < NP; ++pl) *reinterpret_cast<u32x2_t*>(dst + pl * FPS) = u32x2_t{w0[pl], w1[pl]};
             };
 #pragma unroll
-            for (int s = 0; s < S; ++s) quad(v.a[s], buf + s * PIECE + plane_elem(row, kq));
+            for (int j = 0; j < PA; ++j) quad(v.a[j], buf + (kGroups * j + grp) * PIECE + plane_elem(row, kq));
             if constexpr (SRC == FB_ROWS) {
 #pragma unroll
-                for (int s = 0; s < S; ++s) quad(v.b[s], buf + s * PIECE + NP * FPS + plane_elem(row, kq));
+                for (int j = 0; j < PB; ++j) quad(v.b[j], buf + (kGroups * j + grp) * PIECE + NP * FPS + plane_elem(row, kq));
             } else if constexpr (SRC == FB_COLS) {
 #pragma unroll
-                for (int j = 0; j < S; j += 2) {
-                    const int k = 32 * j + pair;   // within the chunk
+                for (int j = 0; j < PB; j += 2) {
+                    const int k = kn_of(j);
                     uint16_t* dst = buf + (k >> 5) * PIECE + NP * FPS;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -231,16 +239,16 @@ __global__ __launch_bounds__(512) void few_gemm_kernel(int64_t M, int N, int K, 
         put(0, v[0], sm);
         load(2, v[0]);
         __syncthreads();
-        for (int c = 0; c < chunks; c += 2) {
+        for (int c = 0;; c += 2) {
             // chunk c is multiplied, c + 1 split, c + 3 requested
             put(c + 1, v[1], sm + BUF);
             load(c + 3, v[1]);
             __syncthreads();
-            if (c + 1 < chunks) {
-                put(c + 2, v[0], sm);
-                load(c + 4, v[0]);
-                __syncthreads();
-            }
+            if (c + 1 >= chunks) break;
+            put(c + 2, v[0], sm);
+            load(c + 4, v[0]);
+            __syncthreads();
+            if (c + 2 >= chunks) break;
         }
     };
     if (wave >= 4) {
@@ -300,7 +308,7 @@ void launch_bands(bool trans_b, int64_t M, int64_t N, int64_t K, const float* A,
     const int64_t cols = ep.gated ? FT / 2 : FT;
     const dim3 grid((unsigned)((N + cols - 1) / cols), (unsigned)((M + FT - 1) / FT));
     auto go = [&]<int SRC, bool GATED>() {
-        hipLaunchKernelGGL((few_gemm_kernel<NB, KC, SRC, GATED>), grid, dim3(512), 0, s, M, (int)N, (int)K, A, lda, B, ldb,
+        hipLaunchKernelGGL((few_gemm_kernel<NB, KC, SRC, GATED>), grid, dim3(256 + kFeeders), 0, s, M, (int)N, (int)K, A, lda, B, ldb,
                            planes, ep);
     };
     if (ep.gated && planes != nullptr)
@@ -320,7 +328,7 @@ void launch_bands(bool trans_b, int64_t M, int64_t N, int64_t K, const float* A,
 hipError_t launch_few_gemm(int nbands, bool trans_b, int64_t M, int64_t N, int64_t K, const float* A, int64_t lda,
                            const float* B, int64_t ldb, const uint16_t* planes, const BlockEpilogue& ep, hipStream_t s)
 {
-    if (M > (int64_t)65535 * FT || 2 * N >= ((int64_t)1 << 31) || K < 1 || K >= ((int64_t)1 << 30) ||
+    if (M > (int64_t)65535 * FT || 2 * N >= ((int64_t)1 << 31) || K < 4 || (!trans_b && N < 4) || K >= ((int64_t)1 << 30) ||
         (ep.gated && !trans_b && planes == nullptr))
         return hipErrorInvalidValue;
     switch (nbands) {
