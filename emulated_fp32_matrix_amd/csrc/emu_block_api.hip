@@ -54,47 +54,63 @@ int bands_of(emu_mode_t mode)
     }
 }
 
-// Where EMU_MODE_AUTO takes the one-launch FP32 kernel: where it is predicted
-// faster than what emu_sgemm's AUTO runs with the epilogue.  Its time is a
-// launch and, per workgroup of a CU, a latency and K; a workgroup has 64 rows
-// (or 32, 16) and 16 columns, or 32 where that still leaves every CU one and
-// in a gated projection (launch_rows_gemm).  Fitted to ten (K, N) and M = 1
-// .. 6,144, within a tenth of the measured times; the slower of the two was
-// taken only where they are as near.  Measured (us, this kernel / the emulated
-// one with AUTO's plan): 1 x 512 x 256 3.6 / 12.1, 6,144 x 64 x 64 5.2 / 11.8,
-// 2,048 x 512 x 256 12.1 / 17.7, 4,096 x 512 x 256 27.4 / 19.2, 512 x 1024 x
-// 1024 19.8 / 30.8, 1,024 x 1024 x 1024 44.4 / 40.1, 16 x 1024 x 4096 16.6 /
-// 47.2, 64 x 1024 x 4096 41.1 / 46.3.
-bool few_rows(int64_t M, int64_t N, int64_t K, bool is_gated)
+// A product's kernels by predicted time (us), fitted to ten (K, N) and M = 1
+// .. 8,192; a slower one is taken only where two are within a tenth.
+//
+// The one-launch FP32 kernel (launch_rows_gemm): a launch and, per workgroup
+// of a CU, a latency and K; a workgroup has 64 rows (or 32, 16) and 16
+// columns, or 32 where that still leaves every CU one and in a gated
+// projection.
+double rows_us(int64_t M, int64_t N, int64_t K, bool is_gated)
 {
-    if (M == 0 || N == 0 || K == 0 || M > ((int64_t)1 << 20)) return false;
     const double m64 = (double)((M + 63) / 64), n32 = (double)((N + 31) / 32), n16 = (double)((N + 15) / 16);
-    double us;
     if (M > 32 && (is_gated || m64 * n32 >= 256.0)) {
         const double rounds = std::ceil(m64 * n32 / 256.0);
-        us = 2.3 + rounds * (0.9 + 0.0162 * (double)K);
-    } else {
-        const double groups = m64 * n16 / 256.0;
-        const double per_k = M <= 16 ? 0.0034 : M <= 32 ? 0.0057 : 0.0094;
-        us = 2.4 + (groups < 1.0 ? 1.0 : groups) * (0.75 + per_k * (double)K);
+        return 2.3 + rounds * (0.9 + 0.0162 * (double)K);
     }
-    // (the library's model leaves out the traffic of the weights' split: 10
-    // bytes per element)
-    return us < emu::api_predict_us(M, N, K) + 10.0 * (double)N * (double)K / 4.0e6;
+    const double groups = m64 * n16 / 256.0;
+    const double per_k = M <= 16 ? 0.0034 : M <= 32 ? 0.0057 : 0.0094;
+    return 2.4 + (groups < 1.0 ? 1.0 : groups) * (0.75 + per_k * (double)K);
 }
 
-// Where an explicit emulated mode takes the one-launch kernel (the same bits).
-bool few_tiles(int64_t M, int64_t N, int64_t K, int bands, bool have_planes)
+// The one-launch emulated kernel (launch_few_gemm) with its better tile, 32 x
+// 32 or (wide) 64 x 64: rounds of a workgroup per CU, each a latency and its
+// chunks of 128 or 64 k.
+double few_us(int64_t M, int64_t N, int64_t K, int bands, bool& wide)
 {
-    return K >= 4 && N >= 4 && (M + 31) / 32 * ((N + 31) / 32) <= 4096;
+    const int i = bands >= 5 ? 0 : bands >= 3 ? 1 : 2;
+    constexpr double narrow_c[3] = {1.0, 0.95, 0.72}, wide_c[3] = {1.3, 1.17, 0.93};
+    const double narrow = 0.5 + std::ceil((double)((M + 31) / 32 * ((N + 31) / 32)) / 256.0) *
+                                    (2.4 + narrow_c[i] * (double)((K + 127) / 128));
+    const double broad = 0.5 + std::ceil((double)((M + 63) / 64 * ((N + 63) / 64)) / 256.0) *
+                                   (3.0 + wide_c[i] * (double)((K + 63) / 64));
+    wide = broad < narrow;
+    return wide ? broad : narrow;
 }
+
+// The emulated kernel of 128-wide tiles without a K split: its launch (and
+// the weights' split's, with 10 bytes per element), then rounds of tiles of
+// 128 or 64 rows.
+double tiles_us(int64_t M, int64_t N, int64_t K, int bands, bool have_planes)
+{
+    const int i = bands >= 5 ? 0 : bands >= 3 ? 1 : 2;
+    constexpr double tall_c[3] = {1.95, 1.65, 1.4}, low_c[3] = {1.1, 1.05, 1.0};
+    const double n = (double)((N + 127) / 128), steps = (double)((K + 31) / 32);
+    const double tall = std::ceil((double)((M + 127) / 128) * n / 256.0) * tall_c[i];
+    const double low = std::ceil((double)((M + 63) / 64) * n / 256.0) * low_c[i];
+    return (have_planes ? 5.0 : 8.0 + 10.0 * (double)N * (double)K / 4.0e6) + (low < tall ? low : tall) * steps;
+}
+
+// Below these the kernels' formulas are not asked: the emulated one-launch
+// kernel reads four k (and columns of a K x N operand) at a time.
+bool few_runs(int64_t M, int64_t N, int64_t K) { return K >= 4 && N >= 4 && M <= ((int64_t)1 << 20); }
 
 size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // How one product with its epilogue runs.
 struct Route {
     bool rows;                 // the one-launch FP32 kernel
-    bool few;                  // the one-launch emulated kernel, in
+    bool few, wide;            // the one-launch emulated kernel, and its tile, in
     emu_mode_t mode;           // else: the product's mode,
     emu::GemmPlan plan;        // its plan,
     size_t gemm_bytes;         // and the workspace: the product's own, then
@@ -122,11 +138,32 @@ Route route_of(const emu::GemmArgs& g, bool is_gated, emu_mode_t mode, bool have
 {
     Route r{};
     const bool automatic = mode == EMU_MODE_AUTO;
-    r.rows = g.K == 0 || (automatic && !have_planes && few_rows(g.M, g.N, g.K, is_gated));
-    if (r.rows) return r;
-    r.mode = !automatic ? mode : have_planes ? EMU_MODE_BF16X9 : (emu_mode_t)emu::api_select_mode(g.M, g.N, g.K);
-    r.few = !automatic && bands_of(r.mode) != 0 && few_tiles(g.M, g.N, g.K, bands_of(r.mode), have_planes);
-    if (r.few) return r;
+    r.rows = g.K == 0;
+    if (r.rows || g.M == 0 || g.N == 0) return r;
+    if (automatic) {
+        // what emu_sgemm's AUTO would run (with its K split plan; the
+        // library's model leaves out the traffic of the weights' split)
+        // against the one-launch kernels.  Measured (us, FP32 / nine
+        // products in one launch / AUTO's plan): 1 x 512 x 256 3.6 / 6.8 /
+        // 12.1, 2,048 x 512 x 256 12.1 / 13.3 / 17.7, 512 x 1024 x 1024 19.8 /
+        // 22.1 / 30.8, 64 x 1024 x 4096 41.1 / 12.1 / 46.3.
+        const double plan = emu::api_predict_us(g.M, g.N, g.K) + (have_planes ? -3.5 : 10.0 * (double)g.N * (double)g.K / 4.0e6);
+        const double rows = have_planes || g.M > ((int64_t)1 << 20) ? plan : rows_us(g.M, g.N, g.K, is_gated);
+        const double few = few_runs(g.M, g.N, g.K) ? few_us(g.M, g.N, g.K, 5, r.wide) : plan;
+        r.rows = rows < plan && rows <= few;
+        r.few = !r.rows && 1.05 * few < plan;   // (the predictions' error)
+        r.mode = have_planes || r.few ? EMU_MODE_BF16X9 : (emu_mode_t)emu::api_select_mode(g.M, g.N, g.K);
+    } else {
+        // the same bits either way.  Measured with nine products (us, one
+        // launch / 128-wide tiles): 1 x 1024 x 1024 10.4 / 41.8, 1,024 x 1024
+        // x 1024 25.5 / 41.6, 2,048 x 1024 x 1024 49.8 / 46.9, 4,096 x 512 x
+        // 256 15.2 / 24.6, 8,192 x 512 x 256 28.1 / 28.0.
+        r.mode = mode;
+        const int bands = bands_of(mode);
+        r.few = bands != 0 && few_runs(g.M, g.N, g.K) &&
+                1.05 * few_us(g.M, g.N, g.K, bands, r.wide) < tiles_us(g.M, g.N, g.K, bands, have_planes);
+    }
+    if (r.rows || r.few) return r;
     if (r.mode == EMU_MODE_NATIVE_F32) {
         r.gemm_bytes = round256(emu::gemm_native_f32_workspace_bytes(g));
         r.ld = (g.N + 3) & ~(int64_t)3;
@@ -183,7 +220,7 @@ emu_status_t product(emu::GemmArgs g, int64_t n_out, const BlockEpilogue& ep, em
     if (r.rows)
         return from_hip(emu::launch_rows_gemm(g.trans_b, g.M, n_out, g.K, g.A, g.lda, g.B, g.ldb, ep, s));
     if (r.few)
-        return from_hip(emu::launch_few_gemm(bands_of(r.mode), g.trans_b, g.M, n_out, g.K, g.A, g.lda, g.B, g.ldb,
+        return from_hip(emu::launch_few_gemm(bands_of(r.mode), r.wide, g.trans_b, g.M, n_out, g.K, g.A, g.lda, g.B, g.ldb,
                                              g.Bplanes, ep, s));
     if (bad_workspace(ws, ws_bytes, r.gemm_bytes + r.more_bytes)) return EMU_STATUS_INVALID_VALUE;
     float* more = reinterpret_cast<float*>(static_cast<char*>(ws) + r.gemm_bytes);
@@ -211,7 +248,7 @@ emu_status_t product_workspace(const emu::GemmArgs& g, bool is_gated, emu_mode_t
     *bytes = 0;
     if (g.M == 0 || g.N == 0) return EMU_STATUS_SUCCESS;
     const Route r = route_of(g, is_gated, mode, have_planes, query_cus());
-    if (!r.rows) *bytes = r.gemm_bytes + r.more_bytes;
+    *bytes = r.gemm_bytes + r.more_bytes;   // (none for one launch)
     return EMU_STATUS_SUCCESS;
 }
 
@@ -335,7 +372,9 @@ emu_status_t emu_act_backward2(int64_t rows, int64_t cols, const float* v, int64
 emu_status_t emu_sgemm_act_route(emu_op_t transB, int64_t M, int64_t N, int64_t K, int* few)
 {
     if (!valid_op(transB) || M < 0 || N < 0 || K < 0 || few == nullptr) return EMU_STATUS_INVALID_VALUE;
-    *few = few_rows(M, N, K, false) ? 1 : 0;
+    const Route r = route_of(gemm_args(transB == EMU_OP_T, M, N, K, nullptr, max1(K), nullptr, 0, nullptr), false,
+                             EMU_MODE_AUTO, false, query_cus());
+    *few = M > 0 && N > 0 && K > 0 && r.rows ? 1 : r.few ? 2 : 0;
     return EMU_STATUS_SUCCESS;
 }
 

@@ -81,8 +81,9 @@ hipError_t launch_rows_gemm(bool trans_b, int64_t M, int64_t N, int64_t K, const
                             const float* B, int64_t ldb, const BlockEpilogue& ep, hipStream_t s);
 
 // The emulated product (nbands of the mode) and its epilogue in one launch, for
-// few rows, from B as above or from its planes.
-hipError_t launch_few_gemm(int nbands, bool trans_b, int64_t M, int64_t N, int64_t K, const float* A, int64_t lda,
+// few rows, from B as above or from its planes, in tiles of 64 x 64 (wide) or
+// 32 x 32.  K at least 4, and N, of a K x N operand.
+hipError_t launch_few_gemm(int nbands, bool wide, bool trans_b, int64_t M, int64_t N, int64_t K, const float* A, int64_t lda,
                            const float* B, int64_t ldb, const uint16_t* planes, const BlockEpilogue& ep, hipStream_t s);
 
 // Leading dimensions of the weight-gradient product: its 32-row slabs are

@@ -456,22 +456,34 @@ __global__ __launch_bounds__(512, 1) void gemm_bf16_pp_kernel(Params p, const ui
                     // ups) by scalar loads under one wait, which never waits
                     // for the direct loads in flight (a wait per 8 columns:
                     // 2,325 us instead of 2,258 on the gated 552,960 x 256 ->
-                    // 2 x 512)
+                    // 2 x 512).  Tiles of 64 rows load 8 words at a time:
+                    // the 32 registers cost their main loop spills (2,048 x
+                    // 4096 -> 1024: 165 us instead of 155).
                     const float* b = be.bias + n0 + gw * (EPI == EPI_GATED ? 16 : 32);
-                    i32x16_t bw[2];
-                    scalar_load16x2(b, EPI == EPI_GATED ? b + p.N : b + 16, bw[0], bw[1]);
+                    const float* b1 = EPI == EPI_GATED ? b + p.N : b + 16;
                     const bool upper = (lane >> 5) != 0;
+                    auto add = [&](int q, int e, int lo, int hi) __attribute__((always_inline)) {
+                        // (opaque copies: otherwise the two selects fold
+                        // into an index and a chain of compares)
+                        asm("" : "+s"(lo));
+                        asm("" : "+s"(hi));
+                        z[q][e] = z[q][e] + __int_as_float(upper ? hi : lo);
+                    };
+                    if constexpr (TH == 128) {
+                        i32x16_t bw[2];
+                        scalar_load16x2(b, b1, bw[0], bw[1]);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
+                        for (int q = 0; q < 4; ++q)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            // (opaque copies: otherwise the two selects fold
-                            // into an index and a chain of compares)
-                            int lo = bw[q >> 1][8 * (q & 1) + e], hi = bw[q >> 1][8 * (q & 1) + 4 + e];
-                            asm("" : "+s"(lo));
-                            asm("" : "+s"(hi));
-                            z[q][e] = z[q][e] + __int_as_float(upper ? hi : lo);
+                            for (int e = 0; e < 4; ++e) add(q, e, bw[q >> 1][8 * (q & 1) + e], bw[q >> 1][8 * (q & 1) + 4 + e]);
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const i32x8_t bw = scalar_load8((q >= 2 ? b1 : b) + 8 * (q & 1));
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) add(q, e, bw[e], bw[4 + e]);
                         }
+                    }
                 } else {
 #pragma unroll
                     for (int q = 0; q < 4; ++q)

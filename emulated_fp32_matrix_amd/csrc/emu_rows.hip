@@ -1,7 +1,8 @@
 // The product of few rows with its epilogue in one launch (emu_sgemm_act and
 // emu_sgemm_gated of include/emu_block.h in EMU_MODE_AUTO): one token, or the
 // tokens of a few atoms, where a launch and one memory latency are most of
-// the time.
+// the time.  (Where weights and rows are more, EMU_MODE_AUTO takes the
+// emulated kernel of few rows, emu_few.hip.)
 //
 // FP32 on v_mfma_f32_16x16x4_f32, operands read from memory to registers as
 // they are: no split of the weights, no LDS tiles, no second launch.  A

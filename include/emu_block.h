@@ -127,10 +127,11 @@ emu_status_t emu_act_backward2(int64_t rows, int64_t cols, const float* v, int64
  *
  * mode: as emu_sgemm's, and the product is emu_sgemm's in the explicit modes,
  * bit for bit (a row of C never depends on the other rows).  EMU_MODE_AUTO: for few
- * rows (where a cost model predicts it faster: emu_sgemm_act_route) an FP32
- * matrix-instruction kernel that reads the operands as they are and runs as
- * one launch, otherwise what emu_sgemm's AUTO runs, its K split plan
- * included.
+ * rows (where a cost model predicts it faster: emu_sgemm_act_route) one launch
+ * that reads the operands as they are, on FP32 matrix instructions or as
+ * BF16X9, otherwise what emu_sgemm's AUTO runs, its K split plan included.
+ * The explicit emulated modes take such a launch for few rows too, with the
+ * same bits.
  * planes: op(B) split by emu_presplit_b in `mode` (an emulated one), or in
  * BF16X9 for EMU_MODE_AUTO, which then runs BF16X9 whatever the shape; B and
  * ldb are not read.  NULL: the call splits op(B) into the workspace.
@@ -146,8 +147,9 @@ emu_status_t emu_sgemm_act(emu_op_t transB, int64_t M, int64_t N, int64_t K, con
                            const float* bias, emu_act_t act, float* Z, int64_t ldz, const float* R,
                            int64_t ldr, float* C, int64_t ldc,
                            emu_mode_t mode, void* workspace, size_t workspace_bytes, void* stream);
-/* *few_rows = 1 where AUTO takes the one-launch FP32 kernel for this shape,
- * else 0 (then AUTO is emu_sgemm_select's mode).  A host function. */
+/* *few_rows = 1 where AUTO takes the one-launch FP32 kernel for this shape, 2
+ * where it takes the one-launch BF16X9 kernel, else 0 (then AUTO is
+ * emu_sgemm_select's mode).  A host function. */
 emu_status_t emu_sgemm_act_route(emu_op_t transB, int64_t M, int64_t N, int64_t K, int* few_rows);
 
 /* ---- gated feed-forward projection ---------------------------------------------

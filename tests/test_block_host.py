@@ -171,6 +171,7 @@ def test_workspace_queries():
     few = ctypes.c_int(-1)
     assert lib.emu_sgemm_act_route(1, 1, 512, 256, ctypes.byref(few)) == 0 and few.value == 1
     assert lib.emu_sgemm_act_route(1, 552960, 512, 256, ctypes.byref(few)) == 0 and few.value == 0
+    assert lib.emu_sgemm_act_route(1, 64, 4096, 1024, ctypes.byref(few)) == 0 and few.value == 2
     assert lib.emu_sgemm_act_route(1, 1, 512, -1, ctypes.byref(few)) == INVALID
 
 

@@ -352,6 +352,73 @@ def test_planes_bitwise(mode):
         block.gated_linear(x, w, b, mode=mode, planes=pb)
 
 
+# one row, rows and columns past a tile's end, k past a chunk's, widths below
+# four, tiles of 32 x 32 and of 64 x 64
+FEW = [(1, 4, 4), (1, 3, 7), (5, 2, 3), (33, 5, 6), (31, 37, 129), (65, 96, 64), (64, 64, 127), (130, 70, 387),
+       (257, 513, 34), (1000, 640, 130), (700, 500, 261), (2000, 260, 72)]
+
+
+@pytest.mark.parametrize("mode", ["BF16X9", "BF16X6", "BF16X3", "BF16X1"])
+def test_few_rows_in_the_explicit_modes(mode):
+    """One launch for few rows gives emu_sgemm's product bit for bit: both
+    layouts of B, planes, z, the residual and the gated product; inf and NaN
+    stay in their rows and columns."""
+    import emulated_fp32_matrix_amd as emu
+
+    block = _block()
+    for M, N, K in FEW:
+        x, w, b, r = _linear_case(M, N, K, True)
+        t = emu.sgemm(x, w, mode=mode, trans_b=True)
+        pb = emu.presplit_b(w, mode=mode, trans_b=True)
+        say(f"{M}x{N}x{K} {mode}")
+        assert torch.equal(block.linear_act(x, w, b, residual=r, mode=mode), (t + b) + r), (M, N, K)
+        assert torch.equal(block.linear_act(x, w, b, residual=r, mode=mode, planes=pb), (t + b) + r), (M, N, K)
+        for trans_b, op in ((True, w), (False, w.t().contiguous())):
+            c, z = _raw_linear(x, op, trans_b, b, 0, mode)
+            assert torch.equal(c, t + b) and torch.equal(z, t + b), (M, N, K, trans_b)
+        F = N // 2
+        wg, bg = w[:2 * F].contiguous(), b[:2 * F].contiguous()
+        zz = (t + b)[:, :2 * F]
+        want = torch.relu(zz[:, :F]) * zz[:, F:]
+        assert torch.equal(block.gated_linear(x, wg, bg, "relu", mode=mode), want), (M, N, K)
+        pg = block.presplit_gated(wg, mode)
+        assert torch.equal(block.gated_linear(x, wg, bg, "relu", mode=mode, planes=pg), want), (M, N, K)
+        xg = x.clone().requires_grad_(True)
+        assert torch.equal(block.gated_linear(xg, wg, bg, "relu", mode=mode), want), (M, N, K)
+    x, w, b, r = _linear_case(70, 70, 130, True)
+    x[3, 5], x[40, 129], w[9, 0] = float("inf"), float("nan"), float("-inf")
+    t = emu.sgemm(x, w, mode=mode, trans_b=True)
+    c, z = _raw_linear(x, w, True, b, 0, mode)
+    cn, _ = _raw_linear(x, w.t().contiguous(), False, b, 0, mode)
+    bad = ~torch.isfinite(t)
+    assert int(bad.sum()) == 2 * 70 + 68 and torch.equal(bad, ~torch.isfinite(c)) and torch.equal(bad, ~torch.isfinite(cn))
+    assert torch.equal(c[~bad], (t + b)[~bad]) and torch.equal(cn[~bad], c[~bad])
+    assert torch.equal(torch.isnan(t), torch.isnan(c)) and torch.equal(torch.isnan(c), torch.isnan(cn))
+
+
+@pytest.mark.parametrize("M,N,K", [(40, 4096, 600), (129, 771, 387), (1000, 640, 260), (70, 64, 2050)])
+def test_few_rows_in_auto(M, N, K):
+    """AUTO's one launch against the 64-bit form, and with nine products (route
+    2) BF16X9's bits; the gated product of the same weight."""
+    block = _block()
+    few = ctypes.c_int(-1)
+    assert block._lib.emu_sgemm_act_route(1, M, N, K, ctypes.byref(few)) == 0
+    say(f"{M}x{N}x{K}: route {few.value}")
+    assert few.value != 0
+    x, w, b, r = _linear_case(M, N, K, True)
+    y = block.linear_act(x, w, b, "identity", r)
+    if few.value == 2:
+        assert torch.equal(y, block.linear_act(x, w, b, "identity", r, mode="BF16X9"))
+    z, zb = ref.product(x.double(), w.double(), b, "AUTO")
+    want = z + r.double()
+    _within("sum", y, (want, 1.01 * (zb + U * want.abs())))
+    F = N // 2
+    wg, bg = w[:2 * F].contiguous(), b[:2 * F].contiguous()
+    z, zb = ref.product(x.double(), wg.double(), bg, "AUTO")
+    a, u, ab, ub = torch.relu(z[:, :F]), z[:, F:], zb[:, :F], zb[:, F:]
+    _within("gated", block.gated_linear(x, wg, bg, "relu"), (a * u, 1.01 * (ab * (u.abs() + ub) + a * ub) + U * (a * u).abs() + 1e-30))
+
+
 # (M, N, K): every tile split, the last round split, 64- and 128-row tiles, none
 @pytest.mark.parametrize("M,N,K", [(6144, 1024, 1024), (768, 512, 4096), (700, 640, 2048), (3300, 1200, 512), (2000, 640, 2048), (20000, 260, 160)])
 def test_auto_plans(M, N, K):
