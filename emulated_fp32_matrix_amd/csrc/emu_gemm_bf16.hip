@@ -26,9 +26,9 @@
 //     v_mfma_f32_32x32x16_bf16 tiles with one FP32 accumulator per band
 //     (5 x 2 x 16 = 160 registers in the nine-product mode).
 //   * k-contiguous A (the forward and input-gradient GEMMs): the waves form
-//     two groups that take turns (gemm_bf16_pp_kernel): while one group's
-//     waves issue MFMAs, the other group's waves, one per SIMD beside them,
-//     load, split and store.  Otherwise (A transposed or not 16-byte
+//     two groups that take turns (gemm_bf16_pp_kernel in emu_gemm_pp.h):
+//     while one group's waves issue MFMAs, the other group's waves, one per
+//     SIMD beside them, load, split and store.  Otherwise (A transposed or not 16-byte
 //     addressable) A is pre-split like B and gemm_bf16_kernel runs, one
 //     barrier per step, the split work interleaved with the MFMAs.
 //   * Epilogue: bands are recombined smallest first (t = S_{n-1},
