@@ -66,7 +66,8 @@ double rows_us(int64_t M, int64_t N, int64_t K, bool is_gated)
     const double m64 = (double)((M + 63) / 64), n32 = (double)((N + 31) / 32), n16 = (double)((N + 15) / 16);
     if (M > 32 && (is_gated || m64 * n32 >= 256.0)) {
         const double rounds = std::ceil(m64 * n32 / 256.0);
-        return 2.3 + rounds * (0.9 + 0.0162 * (double)K);
+        // (beyond two the reads of A and the stores weigh more)
+        return 2.3 + rounds * (0.9 + 0.0162 * (double)K) * (rounds > 2.0 ? 1.45 : 1.0);
     }
     const double groups = m64 * n16 / 256.0;
     const double per_k = M <= 16 ? 0.0034 : M <= 32 ? 0.0057 : 0.0094;
@@ -80,25 +81,25 @@ double few_us(int64_t M, int64_t N, int64_t K, int bands, bool& wide)
 {
     const int i = bands >= 5 ? 0 : bands >= 3 ? 1 : 2;
     constexpr double narrow_c[3] = {1.0, 0.95, 0.72}, wide_c[3] = {1.3, 1.17, 0.93};
-    const double narrow = 0.5 + std::ceil((double)((M + 31) / 32 * ((N + 31) / 32)) / 256.0) *
-                                    (2.4 + narrow_c[i] * (double)((K + 127) / 128));
-    const double broad = 0.5 + std::ceil((double)((M + 63) / 64 * ((N + 63) / 64)) / 256.0) *
-                                   (3.0 + wide_c[i] * (double)((K + 63) / 64));
+    // (with two planes a CU holds two workgroups)
+    auto rounds = [&](int64_t tiles) { return std::ceil((double)tiles / 256.0) * (i == 2 && tiles > 256 ? 0.8 : 1.0); };
+    const double narrow = 0.5 + rounds((M + 31) / 32 * ((N + 31) / 32)) * (2.4 + narrow_c[i] * (double)((K + 127) / 128));
+    const double broad = 0.5 + rounds((M + 63) / 64 * ((N + 63) / 64)) * (3.0 + wide_c[i] * (double)((K + 63) / 64));
     wide = broad < narrow;
     return wide ? broad : narrow;
 }
 
 // The emulated kernel of 128-wide tiles without a K split: its launch (and
 // the weights' split's, with 10 bytes per element), then rounds of tiles of
-// 128 or 64 rows.
+// 128 or 64 rows, each its k-steps and an epilogue.
 double tiles_us(int64_t M, int64_t N, int64_t K, int bands, bool have_planes)
 {
     const int i = bands >= 5 ? 0 : bands >= 3 ? 1 : 2;
-    constexpr double tall_c[3] = {1.95, 1.65, 1.4}, low_c[3] = {1.1, 1.05, 1.0};
+    constexpr double tall_c[3] = {1.72, 1.44, 1.1}, low_c[3] = {1.0, 0.92, 0.78};
     const double n = (double)((N + 127) / 128), steps = (double)((K + 31) / 32);
-    const double tall = std::ceil((double)((M + 127) / 128) * n / 256.0) * tall_c[i];
-    const double low = std::ceil((double)((M + 63) / 64) * n / 256.0) * low_c[i];
-    return (have_planes ? 5.0 : 8.0 + 10.0 * (double)N * (double)K / 4.0e6) + (low < tall ? low : tall) * steps;
+    const double tall = std::ceil((double)((M + 127) / 128) * n / 256.0) * (tall_c[i] * steps + 4.0);
+    const double low = std::ceil((double)((M + 63) / 64) * n / 256.0) * (low_c[i] * steps + 2.5);
+    return (have_planes ? 4.5 : 8.0 + 10.0 * (double)N * (double)K / 4.0e6) + (low < tall ? low : tall);
 }
 
 // Below these the kernels' formulas are not asked: the emulated one-launch
@@ -147,7 +148,11 @@ Route route_of(const emu::GemmArgs& g, bool is_gated, emu_mode_t mode, bool have
         // products in one launch / AUTO's plan): 1 x 512 x 256 3.6 / 6.8 /
         // 12.1, 2,048 x 512 x 256 12.1 / 13.3 / 17.7, 512 x 1024 x 1024 19.8 /
         // 22.1 / 30.8, 64 x 1024 x 4096 41.1 / 12.1 / 46.3.
-        const double plan = emu::api_predict_us(g.M, g.N, g.K) + (have_planes ? -3.5 : 10.0 * (double)g.N * (double)g.K / 4.0e6);
+        double plan = emu::api_predict_us(g.M, g.N, g.K) + (have_planes ? -3.5 : 10.0 * (double)g.N * (double)g.K / 4.0e6);
+        if (emu::api_select_mode(g.M, g.N, g.K) == EMU_MODE_NATIVE_F32)
+            plan += 4.0 + 8.0 * (double)g.M * (double)g.N / 4.5e6;   // the epilogue, a pass of its own
+        else if (emu::api_plan(g.M, g.N, g.K, true, num_cu).split == 1)
+            plan = std::fmax(plan, tiles_us(g.M, g.N, g.K, 5, have_planes));
         const double rows = have_planes || g.M > ((int64_t)1 << 20) ? plan : rows_us(g.M, g.N, g.K, is_gated);
         const double few = few_runs(g.M, g.N, g.K) ? few_us(g.M, g.N, g.K, 5, r.wide) : plan;
         r.rows = rows < plan && rows <= few;
