@@ -81,26 +81,37 @@ double few_us(int64_t M, int64_t N, int64_t K, int bands, bool& wide)
 {
     const int i = bands >= 5 ? 0 : bands >= 3 ? 1 : 2;
     constexpr double narrow_c[3] = {1.0, 0.95, 0.72}, wide_c[3] = {1.3, 1.17, 0.93};
-    // (with two planes a CU holds two workgroups)
-    auto rounds = [&](int64_t tiles) { return std::ceil((double)tiles / 256.0) * (i == 2 && tiles > 256 ? 0.8 : 1.0); };
-    const double narrow = 0.5 + rounds((M + 31) / 32 * ((N + 31) / 32)) * (2.4 + narrow_c[i] * (double)((K + 127) / 128));
-    const double broad = 0.5 + rounds((M + 63) / 64 * ((N + 63) / 64)) * (3.0 + wide_c[i] * (double)((K + 63) / 64));
+    const double chunks = wide_c[i] * (double)((K + 63) / 64);
+    const int64_t tiles32 = (M + 31) / 32 * ((N + 31) / 32), tiles64 = (M + 63) / 64 * ((N + 63) / 64);
+    // (more wide tiles than CUs, or any with two planes, share a CU in pairs)
+    const double narrow = 0.5 + std::ceil((double)tiles32 / 256.0) * (i == 2 && tiles32 > 256 ? 0.8 : 1.0) *
+                                    (2.4 + narrow_c[i] * (double)((K + 127) / 128));
+    const double broad =
+        0.5 + std::ceil((double)tiles64 / 256.0) * (tiles64 <= 256 ? 3.0 + chunks
+                                                    : i == 2       ? 0.8 * (3.0 + chunks)
+                                                                   : 2.0 + 0.92 * chunks);
     wide = broad < narrow;
     return wide ? broad : narrow;
 }
 
 // The emulated kernel of 128-wide tiles without a K split: its launch (and
-// the weights' split's, with 10 bytes per element), then rounds of tiles of
-// 128 or 64 rows, each its k-steps and an epilogue.
-double tiles_us(int64_t M, int64_t N, int64_t K, int bands, bool have_planes)
+// the weights' split's, with 10 bytes per element; where A is copied to
+// aligned rows, that launch's), then rounds of tiles of 128 or 64 rows, each
+// its k-steps and an epilogue.
+double tiles_us(int64_t M, int64_t N, int64_t K, int bands, bool have_planes, bool copies_a)
 {
     const int i = bands >= 5 ? 0 : bands >= 3 ? 1 : 2;
     constexpr double tall_c[3] = {1.72, 1.44, 1.1}, low_c[3] = {1.0, 0.92, 0.78};
     const double n = (double)((N + 127) / 128), steps = (double)((K + 31) / 32);
     const double tall = std::ceil((double)((M + 127) / 128) * n / 256.0) * (tall_c[i] * steps + 4.0);
     const double low = std::ceil((double)((M + 63) / 64) * n / 256.0) * (low_c[i] * steps + 2.5);
-    return (have_planes ? 4.5 : 8.0 + 10.0 * (double)N * (double)K / 4.0e6) + (low < tall ? low : tall);
+    return (have_planes ? 4.5 : 8.0 + 10.0 * (double)N * (double)K / 4.0e6) +
+           (copies_a ? 4.0 + 8.0 * (double)M * (double)K / 4.0e6 : 0.0) + (low < tall ? low : tall);
 }
+
+// The emulated one-launch kernel is taken where it is predicted this much
+// faster: the predictions' error.
+constexpr double kFewError = 1.1;
 
 // Below these the kernels' formulas are not asked: the emulated one-launch
 // kernel reads four k (and columns of a K x N operand) at a time.
@@ -146,27 +157,30 @@ Route route_of(const emu::GemmArgs& g, bool is_gated, emu_mode_t mode, bool have
         // library's model leaves out the traffic of the weights' split)
         // against the one-launch kernels.  Measured (us, FP32 / nine
         // products in one launch / AUTO's plan): 1 x 512 x 256 3.6 / 6.8 /
-        // 12.1, 2,048 x 512 x 256 12.1 / 13.3 / 17.7, 512 x 1024 x 1024 19.8 /
+        // 12.1, 2,048 x 512 x 256 12.1 / 9.4 / 17.7, 512 x 1024 x 1024 19.8 /
         // 22.1 / 30.8, 64 x 1024 x 4096 41.1 / 12.1 / 46.3.
+        const bool copies = (g.K & 3) != 0;   // (by the shape alone: AUTO's bits do not depend on addresses)
         double plan = emu::api_predict_us(g.M, g.N, g.K) + (have_planes ? -3.5 : 10.0 * (double)g.N * (double)g.K / 4.0e6);
         if (emu::api_select_mode(g.M, g.N, g.K) == EMU_MODE_NATIVE_F32)
             plan += 4.0 + 8.0 * (double)g.M * (double)g.N / 4.5e6;   // the epilogue, a pass of its own
         else if (emu::api_plan(g.M, g.N, g.K, true, num_cu).split == 1)
-            plan = std::fmax(plan, tiles_us(g.M, g.N, g.K, 5, have_planes));
+            plan = std::fmax(plan, tiles_us(g.M, g.N, g.K, 5, have_planes, copies));
+        if (copies) plan = std::fmax(plan, emu::api_predict_us(g.M, g.N, g.K) + 4.0 + 8.0 * (double)g.M * (double)g.K / 4.0e6);
         const double rows = have_planes || g.M > ((int64_t)1 << 20) ? plan : rows_us(g.M, g.N, g.K, is_gated);
         const double few = few_runs(g.M, g.N, g.K) ? few_us(g.M, g.N, g.K, 5, r.wide) : plan;
         r.rows = rows < plan && rows <= few;
-        r.few = !r.rows && 1.05 * few < plan;   // (the predictions' error)
+        r.few = !r.rows && kFewError * few < plan;
         r.mode = have_planes || r.few ? EMU_MODE_BF16X9 : (emu_mode_t)emu::api_select_mode(g.M, g.N, g.K);
     } else {
         // the same bits either way.  Measured with nine products (us, one
         // launch / 128-wide tiles): 1 x 1024 x 1024 10.4 / 41.8, 1,024 x 1024
-        // x 1024 25.5 / 41.6, 2,048 x 1024 x 1024 49.8 / 46.9, 4,096 x 512 x
-        // 256 15.2 / 24.6, 8,192 x 512 x 256 28.1 / 28.0.
+        // x 1024 24.4 / 41.6, 3,000 x 1024 x 1024 67.4 / 63.0, 4,096 x 256 x
+        // 512 14.5 / 24.1, 8,192 x 256 x 512 26.1 / 28.0, 100,000 x 64 x 64
+        // 22.5 / 47.4.
         r.mode = mode;
         const int bands = bands_of(mode);
         r.few = bands != 0 && few_runs(g.M, g.N, g.K) &&
-                1.05 * few_us(g.M, g.N, g.K, bands, r.wide) < tiles_us(g.M, g.N, g.K, bands, have_planes);
+                kFewError * few_us(g.M, g.N, g.K, bands, r.wide) < tiles_us(g.M, g.N, g.K, bands, have_planes, needs_copy(g));
     }
     if (r.rows || r.few) return r;
     if (r.mode == EMU_MODE_NATIVE_F32) {

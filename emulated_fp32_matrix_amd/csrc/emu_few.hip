@@ -11,13 +11,16 @@
 // (three of them), 1, 3 and the pair 0, 4 (two each), with six 2, 1 and 0.
 // T = 2: 64 rows and 64 columns, an MFMA tile with all its bands per wave,
 // half the splitting per element for shapes that have such tiles for every CU
-// (1,024 x 1024 -> 1024, nine products: 25.5 us, T = 1: 43.1).
-// The other eight waves feed them: each chunk of k of A and B (128, T = 2: 64)
+// (1,024 x 1024 -> 1024, nine products: 24.4 us, T = 1: 43.1).
+// The other waves feed them: each chunk of k of A and B (128, T = 2: 64 or 32)
 // is read from memory as it is (any alignment; zeros behind K), split to its
 // BF16 planes in registers and written to LDS, one chunk ahead of the products,
-// its loads two chunks ahead (four feeding waves instead: 12.0 us, not 10.4,
-// for 1 x 1024 -> 1024).  Weights that come as planes are copied.  No
-// workspace, no launch for the weights' split.
+// its loads two chunks ahead.  Eight feeding waves (four: 12.0 us, not 10.4,
+// for 1 x 1024 -> 1024), or four with chunks of 32 where there are more tiles
+// than CUs: half the LDS, so that two workgroups share a CU and one's products
+// run beside the other's waits (5,003 x 387 -> 771, six products: 42 us, and
+// 61 with the 128-wide tiles; 20,000 x 64 -> 64 9.4 -> 7.4).  Weights that come
+// as planes are copied.  No workspace, no launch for the weights' split.
 // What bounds it: the split, about 10 vector instructions per element of 64
 // (128) rows per chunk, with the MFMAs on the same SIMDs: 0.85 us per chunk
 // with nine products, 0.72 with three.  64 x 1024 -> 4096, nine products:
@@ -29,23 +32,22 @@ namespace {
 
 constexpr int FT = 32;                   // rows and columns of an MFMA tile
 constexpr int FPS = FT * LDS_ROW;        // elements per plane of 32 rows x 32 k
-constexpr int kFeeders = 512;            // threads that load and split
-constexpr int kThreads = 256 + kFeeders;
 
 // Where the B operand comes from.
 enum { FB_ROWS = 0, FB_COLS = 1, FB_PLANES = 2 };   // N x K, K x N, planes
 
 // T: a workgroup's tile is 32 T rows by 32 T columns (gated: 16 T gates and
-// the same 16 T ups).
-template <int NB, int T, int SRC, bool GATED>
-__global__ __launch_bounds__(kThreads) void few_gemm_kernel(int64_t M, int N, int K, const float* __restrict__ A,
+// the same 16 T ups).  FEED: threads that load and split, two quads of each
+// operand per chunk.
+template <int NB, int T, int FEED, int SRC, bool GATED>
+__global__ __launch_bounds__(256 + FEED, FEED == 256 ? 4 : 1) void few_gemm_kernel(int64_t M, int N, int K, const float* __restrict__ A,
                                                             int64_t lda, const float* __restrict__ B, int64_t ldb,
                                                             const uint16_t* __restrict__ planes, BlockEpilogue ep)
 {
     static_assert(SRC != FB_COLS || !GATED, "the gated projection's weights are stored N x K");
     static_assert(T == 1 || T == 2, "one MFMA tile by its bands, or four");
     constexpr int NP = NB >= 3 ? 3 : NB;
-    constexpr int KC = 128 / T;            // k of a chunk
+    constexpr int KC = FEED / (4 * T);     // k of a chunk
     constexpr int S = KC / BK;             // 32-wide pieces of it
     constexpr int PLANE = T * FPS;         // elements of a plane of one piece
     constexpr int PIECE = 2 * NP * PLANE;  // A's planes, B's planes
@@ -78,35 +80,40 @@ __global__ __launch_bounds__(kThreads) void few_gemm_kernel(int64_t M, int N, in
         const int off0 = plane_elem(lane & 31, (lane >> 5) * 8), off1 = plane_elem(lane & 31, 16 + (lane >> 5) * 8);
         const uint16_t* const mine_a = sm + (T == 1 ? 0 : (wave & 1) * FPS);
         const uint16_t* const mine_b = sm + NP * PLANE + (T == 1 ? 0 : (wave >> 1) * FPS);
+        // Fragments are read a group ahead of their MFMAs: a group is a 16-wide
+        // k-step of the chunk (T = 1, of few MFMAs), or one plane u of A in it
+        // (T = 2), with B's planes at the step's first.
+        constexpr int NU = TOP - LOW + 1, PER = T == 1 ? 1 : NU, GROUPS = 2 * S * PER;
         bf16x8_t fa[2][NP], fb[2][NP];
-        __builtin_amdgcn_s_setprio(2);   // their SIMD's other waves split beside them
-        // The fragments of 16-wide k-step i of the chunk in buffer b.
-        auto read = [&](int b, int i) __attribute__((always_inline)) {
+        auto read = [&](int b, int g) __attribute__((always_inline)) {
+            const int i = g / PER;
             const int at = b * BUF + (i >> 1) * PIECE + (i & 1 ? off1 : off0);
 #pragma unroll
-            for (int u = LOW; u <= TOP; ++u) {
-                fa[i & 1][u] = *reinterpret_cast<const bf16x8_t*>(mine_a + at + u * PLANE);
-                fb[i & 1][u] = *reinterpret_cast<const bf16x8_t*>(mine_b + at + u * PLANE);
+            for (int v = TOP; v >= LOW; --v) {
+                if (g % PER == 0) fb[i & 1][v] = *reinterpret_cast<const bf16x8_t*>(mine_b + at + v * PLANE);
+                if (PER == 1 || v == TOP - g % PER)
+                    fa[g & 1][v] = *reinterpret_cast<const bf16x8_t*>(mine_a + at + v * PLANE);
             }
         };
+        __builtin_amdgcn_s_setprio(2);   // their SIMD's other waves split beside them
         __syncthreads();   // chunk 0 is there
         for (int c = 0; c < chunks; ++c) {
             const int b = c & 1;
             read(b, 0);
 #pragma unroll
-            for (int i = 0; i < 2 * S; ++i) {
-                if (i + 1 < 2 * S) read(b, i + 1);   // a step ahead of their use
+            for (int g = 0; g < GROUPS; ++g) {
+                if (g + 1 < GROUPS) read(b, g + 1);
                 __builtin_amdgcn_sched_barrier(0);
                 // (as in the 128-wide tiles: A's smallest plane first, and
                 // with it B's)
 #pragma unroll
-                for (int u = NP - 1; u >= 0; --u)
+                for (int u = TOP; u >= LOW; --u)
 #pragma unroll
-                    for (int v = NP - 1; v >= 0; --v)
+                    for (int v = TOP; v >= LOW; --v)
 #pragma unroll
                         for (int j = 0; j < n; ++j)
-                            if (bands[j] == u + v)
-                                acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[i & 1][v], fa[i & 1][u], acc[j], 0, 0, 0);
+                            if (bands[j] == u + v && (PER == 1 || u == TOP - g % PER))
+                                acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[g / PER & 1][v], fa[g & 1][u], acc[j], 0, 0, 0);
                 __builtin_amdgcn_sched_barrier(0);
             }
             __syncthreads();
@@ -137,8 +144,8 @@ __global__ __launch_bounds__(kThreads) void few_gemm_kernel(int64_t M, int N, in
     };
     auto feed = [&]() __attribute__((always_inline)) {
         // quads of A and 16-byte loads of B per thread and chunk
-        constexpr int PA = 32 * T * KC / 4 / kFeeders;
-        constexpr int PB = SRC == FB_PLANES ? S * NP * PLANE * 2 / (16 * kFeeders) : PA;
+        constexpr int PA = 32 * T * KC / 4 / FEED;
+        constexpr int PB = SRC == FB_PLANES ? S * NP * PLANE * 2 / (16 * FEED) : PA;
         static_assert(PA == 2, "a pair of k of a K x N operand");
         struct Chunk {
             f32x4_t a[PA];
@@ -147,18 +154,24 @@ __global__ __launch_bounds__(kThreads) void few_gemm_kernel(int64_t M, int N, in
         const int f = t - 256;
         const int nk = (K + BK - 1) / BK;
         // a thread's quad j of A (and of an N x K operand): this row, in
-        // piece piece_of(j) four k from kq on
-        const int row = (f >> 3) & (32 * T - 1), kq = (f & 7) * 4;
-        auto piece_of = [&](int j) __attribute__((always_inline)) { return T == 1 ? 2 * j + (f >> 8) : j; };
+        // this piece four k from kq on
+        const int kq = (f & 7) * 4;
+        auto row_of = [&](int j) __attribute__((always_inline)) { return (j * (FEED / 8) + (f >> 3)) % (32 * T); };
+        auto piece_of = [&](int j) __attribute__((always_inline)) { return (j * (FEED / 8) + (f >> 3)) / (32 * T); };
         // of a K x N operand: columns nq .. nq + 3 of chunk rows pair, pair + 1
-        const int pair = 2 * (f >> (T == 1 ? 3 : 4)), nr = (f & (8 * T - 1)) * 4, nq = n0 + nr;
+        const int pair = f / (8 * T) * 2, nr = f % (8 * T) * 4, nq = n0 + nr;
         // rows and columns past the end repeat the last ones; they are not stored
-        const float* arow = A + (m0 + row < M ? m0 + row : M - 1) * lda;
-        const float* brow = B;
-        if constexpr (SRC == FB_ROWS) {
-            int64_t n = n0 + (GATED ? (row >> 5) * 16 + (row & 15) : row);
-            if (n >= N) n = N - 1;
-            brow = B + (n + (GATED && (row & 16) != 0 ? N : 0)) * ldb;
+        const float *arow[PA], *brow[PA];
+#pragma unroll
+        for (int j = 0; j < PA; ++j) {
+            const int row = row_of(j);
+            arow[j] = A + (m0 + row < M ? m0 + row : M - 1) * lda;
+            brow[j] = B;
+            if constexpr (SRC == FB_ROWS) {
+                int64_t n = n0 + (GATED ? (row >> 5) * 16 + (row & 15) : row);
+                if (n >= N) n = N - 1;
+                brow[j] = B + (n + (GATED && (row & 16) != 0 ? N : 0)) * ldb;
+            }
         }
         // The same loads in every chunk: no branches and no masks, which would
         // make them wait for one another.  A quad that crosses K (or N, of
@@ -183,18 +196,18 @@ __global__ __launch_bounds__(kThreads) void few_gemm_kernel(int64_t M, int N, in
             return r;
         };
         // element j of the thread's share of the chunk's planes of B
-        auto plane_at = [&](int j) __attribute__((always_inline)) { return (j * kFeeders + f) * 8; };
+        auto plane_at = [&](int j) __attribute__((always_inline)) { return (j * FEED + f) * 8; };
         auto load = [&](int c, Chunk& v) __attribute__((always_inline)) {
             const int k0 = c * KC;
 #pragma unroll
-            for (int j = 0; j < PA; ++j) v.a[j] = quad_at(arow, k0 + 32 * piece_of(j) + kq, K);
+            for (int j = 0; j < PA; ++j) v.a[j] = quad_at(arow[j], k0 + 32 * piece_of(j) + kq, K);
 #pragma unroll
             for (int j = 0; j < PB; ++j) {
                 if constexpr (SRC == FB_ROWS) {
-                    v.b[j] = quad_at(brow, k0 + 32 * piece_of(j) + kq, K);
+                    v.b[j] = quad_at(brow[j], k0 + 32 * piece_of(j) + kq, K);
                 } else if constexpr (SRC == FB_COLS) {
                     const int k = k0 + pair + j;
-                    v.b[j] = quad_at(brow + (k < K ? k : K - 1) * ldb, nq, N);
+                    v.b[j] = quad_at(B + (k < K ? k : K - 1) * ldb, nq, N);
                 } else {
                     const int s = plane_at(j) / (NP * PLANE), r = plane_at(j) % (NP * PLANE);
                     const int kt = c * S + s < nk ? c * S + s : nk - 1;
@@ -233,7 +246,7 @@ __global__ __launch_bounds__(kThreads) void few_gemm_kernel(int64_t M, int N, in
                 for (int pl = 0; pl < NP; ++pl) *reinterpret_cast<u32x2_t*>(dst + pl * PLANE) = u32x2_t{w0[pl], w1[pl]};
             };
 #pragma unroll
-            for (int j = 0; j < PA; ++j) quad(v.a[j], buf + piece_of(j) * PIECE + plane_elem(row, kq));
+            for (int j = 0; j < PA; ++j) quad(v.a[j], buf + piece_of(j) * PIECE + plane_elem(row_of(j), kq));
             uint16_t* const bufb = buf + NP * PLANE;
             if constexpr (SRC == FB_COLS) {
                 uint16_t* dst = bufb + (pair >> 5) * PIECE;
@@ -249,7 +262,7 @@ __global__ __launch_bounds__(kThreads) void few_gemm_kernel(int64_t M, int N, in
 #pragma unroll
                 for (int j = 0; j < PB; ++j) {
                     if constexpr (SRC == FB_ROWS)
-                        quad(v.b[j], bufb + piece_of(j) * PIECE + plane_elem(row, kq));
+                        quad(v.b[j], bufb + piece_of(j) * PIECE + plane_elem(row_of(j), kq));
                     else
                         *reinterpret_cast<f32x4_t*>(bufb + plane_at(j) / (NP * PLANE) * PIECE + plane_at(j) % (NP * PLANE)) =
                             v.b[j];
@@ -298,7 +311,7 @@ __global__ __launch_bounds__(kThreads) void few_gemm_kernel(int64_t M, int N, in
     // Lane l of a tile's register group q: row l % 32, columns 8 q + 4 (l /
     // 32) .. +3; gated: groups 0, 1 are the gates of 2, 3.
     constexpr int Q = GATED ? 2 : 4;   // register groups of a tile that become columns of C
-    for (int item = wave; item < T * T * Q; item += kThreads / 64) {
+    for (int item = wave; item < T * T * Q; item += (256 + FEED) / 64) {
         const int tile = item / Q, q0 = item % Q;
         const int64_t m = m0 + (tile % T) * FT + (lane & 31);
         const int col = n0 + (tile / T) * (GATED ? FT / 2 : FT) + 8 * q0 + 4 * (lane >> 5);
@@ -335,28 +348,30 @@ template <int NB>
 void launch_bands(bool wide, bool trans_b, int64_t M, int64_t N, int64_t K, const float* A, int64_t lda,
                   const float* B, int64_t ldb, const uint16_t* planes, const BlockEpilogue& ep, hipStream_t s)
 {
-    auto go = [&]<int T, int SRC, bool GATED>() {
+    auto go = [&]<int T, int FEED, int SRC, bool GATED>() {
         const int64_t cols = GATED ? FT * T / 2 : FT * T;
         const dim3 grid((unsigned)((N + cols - 1) / cols), (unsigned)((M + FT * T - 1) / (FT * T)));
-        hipLaunchKernelGGL((few_gemm_kernel<NB, T, SRC, GATED>), grid, dim3(kThreads), 0, s, M, (int)N, (int)K, A, lda, B,
-                           ldb, planes, ep);
+        hipLaunchKernelGGL((few_gemm_kernel<NB, T, FEED, SRC, GATED>), grid, dim3(256 + FEED), 0, s, M, (int)N, (int)K, A,
+                           lda, B, ldb, planes, ep);
     };
-    auto tile = [&]<int T>() {
+    auto tile = [&]<int T, int FEED>() {
         if (ep.gated && planes != nullptr)
-            go.template operator()<T, FB_PLANES, true>();
+            go.template operator()<T, FEED, FB_PLANES, true>();
         else if (ep.gated)
-            go.template operator()<T, FB_ROWS, true>();
+            go.template operator()<T, FEED, FB_ROWS, true>();
         else if (planes != nullptr)
-            go.template operator()<T, FB_PLANES, false>();
+            go.template operator()<T, FEED, FB_PLANES, false>();
         else if (trans_b)
-            go.template operator()<T, FB_ROWS, false>();
+            go.template operator()<T, FEED, FB_ROWS, false>();
         else
-            go.template operator()<T, FB_COLS, false>();
+            go.template operator()<T, FEED, FB_COLS, false>();
     };
-    if (wide)
-        tile.template operator()<2>();
-    else
-        tile.template operator()<1>();
+    if (!wide) return tile.template operator()<1, 512>();
+    if constexpr (NB >= 3) {
+        const int64_t tiles = (M + FT * 2 - 1) / (FT * 2) * (((ep.gated ? 2 * N : N) + FT * 2 - 1) / (FT * 2));
+        if (tiles > 256) return tile.template operator()<2, 256>();
+    }
+    tile.template operator()<2, 512>();
 }
 
 }  // namespace

@@ -353,9 +353,10 @@ def test_planes_bitwise(mode):
 
 
 # one row, rows and columns past a tile's end, k past a chunk's, widths below
-# four, tiles of 32 x 32 and of 64 x 64
+# four, tiles of 32 x 32 and of 64 x 64, fewer and more of them than CUs
 FEW = [(1, 4, 4), (1, 3, 7), (5, 2, 3), (33, 5, 6), (31, 37, 129), (65, 96, 64), (64, 64, 127), (130, 70, 387),
-       (257, 513, 34), (1000, 640, 130), (700, 500, 261), (2000, 260, 72)]
+       (257, 513, 34), (1000, 640, 130), (700, 500, 261), (2000, 260, 72),
+       (4109, 300, 66), (1100, 1102, 131)]
 
 
 @pytest.mark.parametrize("mode", ["BF16X9", "BF16X6", "BF16X3", "BF16X1"])
@@ -420,7 +421,7 @@ def test_few_rows_in_auto(M, N, K):
 
 
 # (M, N, K): every tile split, the last round split, 64- and 128-row tiles, none
-@pytest.mark.parametrize("M,N,K", [(6144, 1024, 1024), (768, 512, 4096), (700, 640, 2048), (3300, 1200, 512), (2000, 640, 2048), (20000, 260, 160)])
+@pytest.mark.parametrize("M,N,K", [(6144, 1024, 1024), (768, 512, 4096), (700, 640, 2048), (3300, 1200, 1024), (2000, 640, 2048), (20000, 260, 160)])
 def test_auto_plans(M, N, K):
     """The K split plans of AUTO with the fused epilogues: bit for bit
     emu_sgemm's product where the epilogue adds one rounding, and the gated
