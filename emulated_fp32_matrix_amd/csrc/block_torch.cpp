@@ -68,13 +68,15 @@ void check_like(const Tensor& t, const char* name, const Tensor& other)
 }
 
 // A tensor as a matrix of rows of `width` with unit stride: a view where its
-// strides allow one, otherwise a copy.
+// strides allow one, otherwise a copy (and of a view that stands for its
+// negative, as the imaginary part of a conjugate does).
 struct Rows {
     Tensor keep;
     int64_t n, width, ld;
     const float* data() const { return keep.numel() ? keep.const_data_ptr<float>() : nullptr; }
-    Rows(const Tensor& t, int64_t w) : keep(t), width(w)
+    Rows(const Tensor& given, int64_t w) : keep(given.is_neg() ? given.resolve_neg() : given), width(w)
     {
+        const Tensor t = keep;
         n = 1;
         for (int64_t d = 0; d + 1 < t.dim(); ++d) n *= t.size(d);
         ld = std::max<int64_t>(w, 1);
@@ -92,7 +94,7 @@ Tensor vector_of(const optional<Tensor>& t, const char* name, int64_t n, const T
     if (!t.has_value() || !t->defined()) return {};
     check_like(*t, name, like);
     TORCH_CHECK_VALUE(t->dim() == 1 && t->size(0) == n, name, " must be a vector of length ", n);
-    return t->contiguous();
+    return t->resolve_neg().contiguous();
 }
 
 const float* ptr(const Tensor& t) { return t.defined() ? t.const_data_ptr<float>() : nullptr; }
@@ -584,7 +586,8 @@ struct LayerNormBackward : Function<LayerNormBackward> {
         const int64_t cols = saved[1].size(-1);
         const Rows gy(saved[0], cols), x(saved[1], cols);
         const Tensor &w = saved[2], &stats = saved[3];
-        const Tensor p = p_in.defined() ? p_in.contiguous() : p_in, q = q_in.defined() ? q_in.contiguous() : q_in;
+        const auto plain = [](const Tensor& t) { return t.defined() ? t.resolve_neg().contiguous() : t; };
+        const Tensor p = plain(p_in), q = plain(q_in);
         variable_list out(5);
         if (ctx->needs_input_grad(0)) out[0] = at::empty(saved[1].sizes(), x.keep.options());
         if (ctx->needs_input_grad(1)) out[1] = at::empty(saved[1].sizes(), x.keep.options());

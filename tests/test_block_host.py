@@ -166,8 +166,8 @@ def test_workspace_queries():
     # no rows, nothing to hold
     assert _bytes(lib.emu_sgemm_act_workspace, 1, 0, 512, 256, None, 256, 0, 1) == 0
     assert _bytes(lib.emu_wgrad_workspace, 0, 512, 256) == 0
-    # the planes of op(B) at least
-    assert _bytes(lib.emu_sgemm_act_workspace, 1, 6144, 512, 256, FAKE, 256, 0, 1) >= 3 * 2 * 512 * 256
+    # the planes of op(B) at least (fewer rows take one launch without them)
+    assert _bytes(lib.emu_sgemm_act_workspace, 1, 552960, 512, 256, FAKE, 256, 0, 1) >= 3 * 2 * 512 * 256
     few = ctypes.c_int(-1)
     assert lib.emu_sgemm_act_route(1, 1, 512, 256, ctypes.byref(few)) == 0 and few.value == 1
     assert lib.emu_sgemm_act_route(1, 552960, 512, 256, ctypes.byref(few)) == 0 and few.value == 0

@@ -728,6 +728,25 @@ def test_host_threads_at_once():
         assert all(torch.equal(u, v) for u, v in zip(a, b))
 
 
+def test_views_that_stand_for_a_negative():
+    """The imaginary part of a conjugate is stored with the other sign."""
+    block = _block()
+
+    def negative(t):
+        v = torch.complex(torch.zeros_like(t), t).conj().imag
+        assert v.is_neg()
+        return v
+
+    x, w, b, r = _linear_case(40, 36, 64, True)
+    for f in (lambda x, w, b, r: block.linear_act(x, w, b, "silu", r), lambda x, w, b, r: block.gated_linear(x, w, b),
+              lambda x, w, b, r: block.layer_norm(r, b, b), lambda x, w, b, r: block.wgrad(r, x)[0]):
+        assert torch.equal(f(negative(x), negative(w), negative(b), negative(r)), f(-x, -w, -b, -r))
+    x1, x2 = x.clone().requires_grad_(True), x.clone().requires_grad_(True)
+    block.layer_norm(x1).backward(negative(x))
+    block.layer_norm(x2).backward(-x)
+    assert torch.equal(x1.grad, x2.grad)
+
+
 def test_one_tensor_in_several_places():
     """x as input and residual, one weight in two layers: their gradients add
     up."""
