@@ -8,7 +8,8 @@ to its inputs, and training on forces differentiates that gradient again
 ("Unlocking Tensor Core Performance for Machine Learning Interatomic
 Potentials", section "TF32x3 on Ampere GPUs").  Every function here is
 therefore differentiable twice (``create_graph=True``); a third derivative
-raises.
+raises, and so do forward-mode derivatives, tracing (``torch.jit.trace``,
+``make_fx``) and the transforms of ``torch.func`` (NotImplementedError).
 
     from emulated_fp32_matrix_amd import block
     n = block.layer_norm(x, weight, bias)

@@ -14,9 +14,12 @@
 // Potentials", section "TF32x3 on Ampere GPUs"); a third derivative raises.
 // In a backward pass that nothing differentiates (no create_graph) the
 // kernels are called directly, and the activation's backward pass may run
-// inside the weight gradient.
+// inside the weight gradient.  Forward-mode derivatives and tracing are
+// refused.
 #include <ATen/hip/impl/HIPStreamMasqueradingAsCUDA.h>
+#include <c10/core/impl/TorchDispatchModeTLS.h>
 #include <hip/hip_runtime_api.h>
+#include <torch/csrc/jit/frontend/tracer.h>
 #include <torch/extension.h>
 
 #include <stdexcept>
@@ -56,6 +59,34 @@ struct OnDevice {
     }
 };
 
+// Refuses to read a tensor for something that would have to see the kernels,
+// which write to memory that torch only saw being allocated: the output would
+// lack its tangent (forward-mode derivatives), or a recorded program would
+// return that memory without what is written to it.
+void check_readable(const Tensor& t)
+{
+    if (!t.defined()) return;
+    using c10::impl::TorchDispatchModeKey;
+    using c10::impl::TorchDispatchModeTLS;
+    TORCH_CHECK_NOT_IMPLEMENTED(!torch::jit::tracer::isTracing(), "the block operators cannot be traced by torch.jit");
+    if (TorchDispatchModeTLS::any_modes_set()) {
+        for (const auto key : {TorchDispatchModeKey::FAKE, TorchDispatchModeKey::PROXY, TorchDispatchModeKey::FUNCTIONAL})
+            TORCH_CHECK_NOT_IMPLEMENTED(!TorchDispatchModeTLS::get_mode(key).has_value(),
+                                        "the block operators cannot be traced: their kernels are no torch operators");
+    }
+    constexpr c10::DispatchKeySet wrappers({c10::DispatchKey::Python, c10::DispatchKey::Functionalize,
+                                            c10::DispatchKey::FuncTorchGradWrapper, c10::DispatchKey::FuncTorchBatched});
+    TORCH_CHECK_NOT_IMPLEMENTED(!t.key_set().has_any(wrappers),
+                                "the block operators take plain tensors, not those of a tracer, of a torch.func "
+                                "transform or of a subclass with its own dispatch");
+    TORCH_CHECK_NOT_IMPLEMENTED(!t._fw_grad(0).defined(), "the block operators have no forward-mode derivative");
+}
+
+void check_readable(const optional<Tensor>& t)
+{
+    if (t.has_value()) check_readable(*t);
+}
+
 void check(const Tensor& t, const char* name)
 {
     TORCH_CHECK_TYPE(t.defined() && t.scalar_type() == at::kFloat && t.is_cuda(), name, " must be a float32 CUDA tensor");
@@ -74,8 +105,10 @@ struct Rows {
     Tensor keep;
     int64_t n, width, ld;
     const float* data() const { return keep.numel() ? keep.const_data_ptr<float>() : nullptr; }
-    Rows(const Tensor& given, int64_t w) : keep(given.is_neg() ? given.resolve_neg() : given), width(w)
+    Rows(const Tensor& given, int64_t w) : width(w)
     {
+        check_readable(given);   // (gradients come here unchecked)
+        keep = given.is_neg() ? given.resolve_neg() : given;
         const Tensor t = keep;
         n = 1;
         for (int64_t d = 0; d + 1 < t.dim(); ++d) n *= t.size(d);
@@ -503,6 +536,10 @@ Tensor layer_call(const Tensor& x, const Tensor& weight, const optional<Tensor>&
                   const optional<Tensor>& residual_in, int64_t act, int64_t mode, bool is_gated,
                   const optional<Tensor>& planes)
 {
+    check_readable(x);
+    check_readable(weight);
+    check_readable(bias_in);
+    check_readable(residual_in);
     check(x, "x");
     check_like(weight, "weight", x);
     TORCH_CHECK_VALUE(weight.dim() == 2, "weight must be 2-D");
@@ -586,7 +623,10 @@ struct LayerNormBackward : Function<LayerNormBackward> {
         const int64_t cols = saved[1].size(-1);
         const Rows gy(saved[0], cols), x(saved[1], cols);
         const Tensor &w = saved[2], &stats = saved[3];
-        const auto plain = [](const Tensor& t) { return t.defined() ? t.resolve_neg().contiguous() : t; };
+        const auto plain = [](const Tensor& t) {
+            check_readable(t);
+            return t.defined() ? t.resolve_neg().contiguous() : t;
+        };
         const Tensor p = plain(p_in), q = plain(q_in);
         variable_list out(5);
         if (ctx->needs_input_grad(0)) out[0] = at::empty(saved[1].sizes(), x.keep.options());
@@ -652,6 +692,9 @@ struct LayerNorm : Function<LayerNorm> {
 
 Tensor layer_norm(const Tensor& x, const optional<Tensor>& weight_in, const optional<Tensor>& bias_in, double eps)
 {
+    check_readable(x);
+    check_readable(weight_in);
+    check_readable(bias_in);
     check(x, "x");
     TORCH_CHECK_VALUE(x.dim() >= 1 && x.size(-1) >= 1 && x.size(-1) <= EMU_LAYER_NORM_MAX_COLS,
                       "layer_norm takes 1 to ", EMU_LAYER_NORM_MAX_COLS, " features, not ", x.sizes());
@@ -671,6 +714,8 @@ Tensor layer_norm(const Tensor& x, const optional<Tensor>& weight_in, const opti
 
 std::tuple<Tensor, optional<Tensor>> wgrad(const Tensor& dz, const Tensor& x, bool want_db)
 {
+    check_readable(dz);
+    check_readable(x);
     check(dz, "dz");
     check_like(x, "x", dz);
     TORCH_CHECK_VALUE(dz.dim() == 2 && x.dim() == 2, "dz and x must be 2-D");
@@ -686,6 +731,8 @@ std::tuple<Tensor, optional<Tensor>> wgrad(const Tensor& dz, const Tensor& x, bo
 // dz = dy act'(z) for matrices, differentiable once.
 Tensor act_grad(const Tensor& dy, const Tensor& z, int64_t act)
 {
+    check_readable(dy);
+    check_readable(z);
     check(dy, "dy");
     check_like(z, "z", dy);
     TORCH_CHECK_VALUE(dy.dim() == 2 && dy.sizes() == z.sizes(), "dy and z must be matrices of one shape");
