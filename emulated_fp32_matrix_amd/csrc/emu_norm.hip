@@ -125,7 +125,21 @@ __global__ __launch_bounds__(SH::NT) void norm_kernel(int64_t rows, int cols, co
         if (rb + step < rows) load_row<SH>(nx, x + at(r + step) * ldx, li, cols);
         float s1[1] = {sum_of<SH>(v)};
         row_sum<SH>(s1, lds);
-        const float mu = s1[0] / n;
+        float mu = s1[0] / n;
+        // The sum's rounding, up to a few units of the mean, is a deviation of
+        // its own in a row far from zero (1,000,003 in all of 200 columns gave
+        // xhat = 1): the centred row's mean is added, which leaves the mean's
+        // own rounding.  (NaN where the row overflows: mu stays.)
+        float c = 0.0f;
+#pragma unroll
+        for (int j = 0; j < SH::NV; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                c = c + ((li + SH::LPR * j) * 4 + e < cols ? v[j][e] - mu : 0.0f);
+        float s0[1] = {c};
+        row_sum<SH>(s0, lds);
+        c = s0[0] / n;
+        if (c == c) mu = mu + c;
 #pragma unroll
         for (int j = 0; j < SH::NV; ++j)
 #pragma unroll

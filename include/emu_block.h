@@ -47,7 +47,9 @@ int emu_block_version(void);
  *   y = xhat * weight + bias.
  * weight, bias: cols floats, or NULL (1 and 0).  mean, rstd: rows floats that
  * receive mu and r, or NULL.  The row is held in registers: mean and squared
- * deviations are two sums over exact inputs, not a difference of moments.
+ * deviations are two sums over exact inputs, not a difference of moments, and
+ * the mean, corrected by that of the centred row, is good to its own rounding
+ * (in a row of one value it is that value).
  * y may be x.
  * Errors: EMU_STATUS_INVALID_VALUE for rows < 0, cols < 1, a leading
  * dimension < cols, eps < 0 or NaN, or (rows > 0) a NULL x or y;
