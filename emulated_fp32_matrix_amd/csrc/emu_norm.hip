@@ -235,7 +235,12 @@ __global__ __launch_bounds__(SH::NT) void norm_backward_kernel(
         float s[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int j = 0; j < SH::NV; ++j) {
-            h[j] = (h[j] - mu) * rs;                       // xhat (columns past the end meet dy = 0)
+            h[j] = (h[j] - mu) * rs;                       // xhat
+            // columns past the end meet dy = 0, but -mu rs may be infinite
+            if (cols != SH::COLS) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) h[j][e] = (li + SH::LPR * j) * 4 + e < cols ? h[j][e] : 0.0f;
+            }
             if (r < rows) {
                 aw[j] = aw[j] + g[j] * h[j];
                 ab[j] = ab[j] + g[j];

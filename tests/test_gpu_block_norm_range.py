@@ -1,4 +1,5 @@
-"""Layer norm of rows far from zero: the mean is good to its own rounding."""
+"""Layer norm of rows far from zero: the mean is good to its own rounding, and
+columns past a row's end never enter a result."""
 import pytest
 import torch
 
@@ -58,3 +59,26 @@ def test_mean_to_its_own_rounding():
         # half a unit of the sum's rounding, and the sum of the centred row:
         # 64 additions of terms near 1, 2^-18 of the offset's unit (2^-11)
         assert float((stats[0].double() - mu).abs().max()) <= 0.51 * 2.0**-11
+
+
+@pytest.mark.parametrize("cols", [50, 100, 200])
+def test_columns_past_the_end_stay_out(cols):
+    """Where mean times reciprocal deviation overflows, the columns that a
+    lane holds past the row's end must not turn the row's sums into NaN."""
+    block = _block()
+    x = torch.full((3, cols), 2.0**120, device="cuda:0")
+    x[1] = _randn(1, cols)
+    xg = x.clone().requires_grad_(True)
+    w = _randn(2, cols).requires_grad_(True)
+    dy = _randn(3, 3, cols)
+    dx, dw = torch.autograd.grad(block.layer_norm(xg, w, None), (xg, w), dy)
+    a = dy.double() * w.detach().double()
+    want = (a - a.mean(-1, keepdim=True)) * 1e-5**-0.5
+    bound = 192 * U * 1e-5**-0.5 * (a.abs() + a.abs().mean(-1, keepdim=True))
+    for r in (0, 2):
+        assert bool(torch.isfinite(dx[r]).all())
+        assert float(((dx[r].double() - want[r]).abs() / bound[r]).max()) <= 1.0
+    value, bnd = ref.norm_backward(x[1:2], w.detach(), dy[1:2], 1e-5)[0]
+    assert ref.worst(dx[1:2], value, bnd) <= 1.0
+    value, bnd = ref.norm_backward(x[1:2], w.detach(), dy[1:2], 1e-5)[1]
+    assert ref.worst(dw, value, bnd) <= 1.0   # (xhat is zero in the other rows)
