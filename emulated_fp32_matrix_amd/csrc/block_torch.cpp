@@ -185,7 +185,11 @@ void claim_leaves(const OnDevice& on, std::initializer_list<const Tensor*> ts)
 // out, connected to a tensor it was made from by a derivative that raises: a
 // gradient taken through it never goes missing silently.
 struct Refuse : Function<Refuse> {
-    static Tensor forward(AutogradContext*, const Tensor& out, const Tensor&) { return out.view_as(out); }
+    static Tensor forward(AutogradContext* ctx, const Tensor& out, const Tensor&)
+    {
+        ctx->mark_dirty({out});   // (out itself, not a view of it, which could not be changed in place)
+        return out;
+    }
     static variable_list backward(AutogradContext*, variable_list)
     {
         TORCH_CHECK(false, "the block operators are differentiable twice: a third derivative is not implemented");
@@ -207,13 +211,23 @@ void last_derivative(variable_list& outs, const variable_list& grads, const vari
 
 int op_of(bool trans) { return trans ? EMU_OP_T : EMU_OP_N; }
 
-// act(a @ op(w) + bias) + residual; z receives the pre-activation when
-// defined.  planes: op(w) split beforehand, or null.
+// An array of the rows of `like`, `cols` wide, in the shape of `like`.  (Made in
+// its shape: autograd lets no view that a Function returns be changed in place.)
+Tensor empty_shaped(const Tensor& like, int64_t cols)
+{
+    if (like.dim() == 2) return empty_rows(like.size(0), cols, like);
+    auto shape = like.sizes().vec();
+    shape.back() = cols;
+    return at::empty(shape, like.options());
+}
+
+// act(a @ op(w) + bias) + residual, in the shape of `like`; z receives the
+// pre-activation when defined.  planes: op(w) split beforehand, or null.
 Tensor product(const Rows& a, const Rows& w, bool trans, const Tensor& bias, int act, const Rows* residual,
-               const Tensor& z, int mode, const void* planes)
+               const Tensor& z, int mode, const void* planes, const Tensor& like)
 {
     const int64_t M = a.n, K = a.width, N = trans ? w.n : w.width;
-    Tensor c = empty_rows(M, N, a.keep);
+    Tensor c = empty_shaped(like, N);
     const int64_t ldn = std::max<int64_t>(N, 1);
     OnDevice on(a.keep);
     size_t bytes = 0;
@@ -227,10 +241,11 @@ Tensor product(const Rows& a, const Rows& w, bool trans, const Tensor& bias, int
     return c;
 }
 
-Tensor gated(const Rows& a, const Rows& w, const Tensor& bias, int act, const Tensor& z, int mode, const void* planes)
+Tensor gated(const Rows& a, const Rows& w, const Tensor& bias, int act, const Tensor& z, int mode, const void* planes,
+             const Tensor& like)
 {
     const int64_t M = a.n, K = a.width, F = w.n / 2;
-    Tensor c = empty_rows(M, F, a.keep);
+    Tensor c = empty_shaped(like, F);
     OnDevice on(a.keep);
     size_t bytes = 0;
     done(emu_sgemm_gated_workspace(M, F, K, a.data(), a.ld, planes != nullptr, (emu_mode_t)mode, &bytes),
@@ -305,9 +320,9 @@ Tensor act_backward(const Rows& dy, const Rows& z, int act, bool is_gated)
     return out;
 }
 
-Tensor norm_forward(const Rows& x, const Tensor& weight, const Tensor& bias, double eps, Tensor* stats)
+Tensor norm_forward(const Rows& x, const Tensor& weight, const Tensor& bias, double eps, Tensor* stats, const Tensor& like)
 {
-    Tensor y = empty_rows(x.n, x.width, x.keep);
+    Tensor y = empty_shaped(like, x.width);
     if (stats) *stats = at::empty({2, x.n}, x.keep.options());
     OnDevice on(x.keep);
     float* s = stats ? out_ptr(*stats) : nullptr;
@@ -321,11 +336,11 @@ struct NormGrads {
 };
 
 NormGrads norm_backward(const Rows& dy, const Rows& x, const Tensor& weight, const Tensor& stats, bool want_x,
-                        bool want_w, bool want_b)
+                        bool want_w, bool want_b, const Tensor& like)
 {
     NormGrads g;
     const auto opt = x.keep.options();
-    if (want_x) g.dx = empty_rows(x.n, x.width, x.keep);
+    if (want_x) g.dx = empty_shaped(like, x.width);
     if (want_w) g.dw = at::empty({x.width}, opt);
     if (want_b) g.db = at::empty({x.width}, opt);
     OnDevice on(x.keep);
@@ -351,7 +366,7 @@ struct Product : Function<Product> {
         ctx->save_for_backward({a, w});
         ctx->saved_data["trans"] = trans;
         ctx->saved_data["mode"] = mode;
-        return product(Rows(a, a.size(1)), Rows(w, w.size(1)), trans, {}, 0, nullptr, {}, (int)mode, nullptr);
+        return product(Rows(a, a.size(1)), Rows(w, w.size(1)), trans, {}, 0, nullptr, {}, (int)mode, nullptr, a);
     }
     static variable_list backward(AutogradContext* ctx, variable_list grads);
 };
@@ -360,7 +375,7 @@ struct Product : Function<Product> {
 Tensor product_of(const Tensor& a, const Tensor& w, bool trans, int64_t mode)
 {
     if (wants_grad({&a, &w})) return Product::apply(a, w, trans, mode);
-    return product(Rows(a, a.size(1)), Rows(w, w.size(1)), trans, {}, 0, nullptr, {}, (int)mode, nullptr);
+    return product(Rows(a, a.size(1)), Rows(w, w.size(1)), trans, {}, 0, nullptr, {}, (int)mode, nullptr, a);
 }
 
 // (dz^T x, column sums of dz): with P and q the gradients of the two, dz gets
@@ -461,17 +476,12 @@ struct Layer : Function<Layer> {
         if (is_gated || act != EMU_ACT_IDENTITY) z = empty_rows(x2.n, w2.n, x);
         const Tensor b = bias.value_or(Tensor());
         if (is_gated) {
-            y = gated(x2, w2, b, (int)act, z, (int)mode, pl);
+            y = gated(x2, w2, b, (int)act, z, (int)mode, pl, x);
         } else if (residual.has_value()) {
             const Rows r(*residual, w2.n);
-            y = product(x2, w2, true, b, (int)act, &r, z, (int)mode, pl);
+            y = product(x2, w2, true, b, (int)act, &r, z, (int)mode, pl, x);
         } else {
-            y = product(x2, w2, true, b, (int)act, nullptr, z, (int)mode, pl);
-        }
-        if (x.dim() != 2) {
-            auto shape = x.sizes().vec();
-            shape.back() = y.size(1);
-            y = y.view(shape);
+            y = product(x2, w2, true, b, (int)act, nullptr, z, (int)mode, pl, x);
         }
         ctx->save_for_backward({x, weight, z});
         return z.defined() ? variable_list{y, z} : variable_list{y};
@@ -512,8 +522,7 @@ struct Layer : Function<Layer> {
                 }
             }
             if (want_x)
-                out[0] = product(Rows(dz, weight.size(0)), Rows(weight, K), false, {}, 0, nullptr, {}, (int)mode, nullptr)
-                             .view(x.sizes());
+                out[0] = product(Rows(dz, weight.size(0)), Rows(weight, K), false, {}, 0, nullptr, {}, (int)mode, nullptr, x);
             return out;
         }
         const auto flat = [](const Tensor& t, int64_t n, int64_t width) { return t.dim() == 2 ? t : t.reshape({n, width}); };
@@ -563,19 +572,10 @@ Tensor layer_call(const Tensor& x, const Tensor& weight, const optional<Tensor>&
         return Layer::apply(x, weight, some(bias), some(residual), act, mode, is_gated, (int64_t)(uintptr_t)pl)[0];
     }
     const Rows x2(x, K), w2(weight, K);
-    Tensor y;
-    if (is_gated) {
-        y = gated(x2, w2, bias, (int)act, {}, (int)mode, pl);
-    } else if (residual.defined()) {
-        const Rows r(residual, wide);
-        y = product(x2, w2, true, bias, (int)act, &r, {}, (int)mode, pl);
-    } else {
-        y = product(x2, w2, true, bias, (int)act, nullptr, {}, (int)mode, pl);
-    }
-    if (x.dim() == 2) return y;
-    auto shape = x.sizes().vec();
-    shape.back() = y.size(1);
-    return y.view(shape);
+    if (is_gated) return gated(x2, w2, bias, (int)act, {}, (int)mode, pl, x);
+    if (!residual.defined()) return product(x2, w2, true, bias, (int)act, nullptr, {}, (int)mode, pl, x);
+    const Rows r(residual, wide);
+    return product(x2, w2, true, bias, (int)act, &r, {}, (int)mode, pl, x);
 }
 
 Tensor linear_act(const Tensor& x, const Tensor& weight, const optional<Tensor>& bias,
@@ -604,9 +604,9 @@ struct LayerNormBackward : Function<LayerNormBackward> {
         const Tensor w = weight.value_or(Tensor());
         ctx->save_for_backward({gy, x, w, stats});
         const int64_t cols = x.size(-1);
-        NormGrads g = norm_backward(Rows(gy, cols), Rows(x, cols), w, stats, want & 1, want & 2, want & 4);
+        NormGrads g = norm_backward(Rows(gy, cols), Rows(x, cols), w, stats, want & 1, want & 2, want & 4, x);
         variable_list out;
-        if (want & 1) out.push_back(g.dx.view(x.sizes()));
+        if (want & 1) out.push_back(g.dx);
         if (want & 2) out.push_back(g.dw);
         if (want & 4) out.push_back(g.db);
         return out;
@@ -656,11 +656,11 @@ struct LayerNorm : Function<LayerNorm> {
     {
         const Tensor w = weight.value_or(Tensor());
         Tensor stats;
-        Tensor y = norm_forward(Rows(x, x.size(-1)), w, bias.value_or(Tensor()), eps, &stats);
+        Tensor y = norm_forward(Rows(x, x.size(-1)), w, bias.value_or(Tensor()), eps, &stats, x);
         ctx->save_for_backward({x, w, stats});
         ctx->saved_data["weight"] = weight.has_value();
         ctx->saved_data["bias"] = bias.has_value();
-        return y.view(x.sizes());
+        return y;
     }
 
     static variable_list backward(AutogradContext* ctx, variable_list grads)
@@ -682,8 +682,8 @@ struct LayerNorm : Function<LayerNorm> {
             return out;
         }
         const int64_t cols = x.size(-1);
-        NormGrads g = norm_backward(Rows(gy, cols), Rows(x, cols), w, stats, want_x, want_w, want_b);
-        if (want_x) out[0] = g.dx.view(x.sizes());
+        NormGrads g = norm_backward(Rows(gy, cols), Rows(x, cols), w, stats, want_x, want_w, want_b, x);
+        out[0] = g.dx;
         out[1] = g.dw;
         out[2] = g.db;
         return out;
@@ -706,8 +706,7 @@ Tensor layer_norm(const Tensor& x, const optional<Tensor>& weight_in, const opti
         const auto some = [](const Tensor& t) { return t.defined() ? optional<Tensor>(t) : std::nullopt; };
         return LayerNorm::apply(x, some(weight), some(bias), eps);
     }
-    Tensor y = norm_forward(Rows(x, cols), weight, bias, eps, nullptr);
-    return x.dim() == 2 ? y : y.view(x.sizes());
+    return norm_forward(Rows(x, cols), weight, bias, eps, nullptr, x);
 }
 
 // ---- the pieces on their own -------------------------------------------------------------------
