@@ -278,13 +278,54 @@ def sgemm(a, b, mode="BF16X9", trans_a=False, trans_b=False, alpha=1.0, beta=0.0
     return c
 
 
+class WeightSource:
+    """Which weight a split was made of, for calls that pass both: the storage
+    (not kept alive), where the matrix lies in it as N x K, and its version."""
+
+    def __init__(self, weight):
+        from torch.multiprocessing.reductions import StorageWeakRef
+
+        # (a weak reference keeps the handle from being given to another storage)
+        self.storage = StorageWeakRef(weight.untyped_storage())
+        self.place = self._place(weight)
+        self.version = self._version(weight)
+
+    @staticmethod
+    def _place(w):
+        # (strides of a dimension of one element say nothing)
+        return (w.storage_offset(), tuple(w.shape), tuple(st for st, n in zip(w.stride(), w.shape) if n > 1), w.is_neg())
+
+    @staticmethod
+    def _version(w):
+        return None if w.is_inference() else w._version   # (inference tensors count none)
+
+    # the reference to the storage is counted: copies share this object, a
+    # pickle, which outlives the storage, holds None
+    def __copy__(self):
+        return self
+
+    def __deepcopy__(self, memo):
+        return self
+
+    def __reduce__(self):
+        return type(None), ()
+
+    def check(self, weight):
+        """ValueError unless ``weight`` (N x K) is the matrix that was split."""
+        if weight.untyped_storage()._cdata != self.storage.cdata or self._place(weight) != self.place:
+            raise ValueError("the planes are those of another weight, or of another layout of this one")
+        if self._version(weight) != self.version:
+            raise ValueError("the weight has changed since its planes were made: split it again")
+
+
 class PresplitB:
     """op(B) split once into the BF16 planes of ``mode`` (``presplit_b``):
     ``planes`` is a uint8 CUDA tensor in the library's own layout, valid for
-    GEMMs with this N, K and mode (``sgemm_presplit``)."""
+    GEMMs with this N, K and mode (``sgemm_presplit``).  ``source`` identifies
+    the matrix that was split."""
 
-    def __init__(self, planes, N, K, mode):
-        self.planes, self.N, self.K, self.mode = planes, int(N), int(K), mode
+    def __init__(self, planes, N, K, mode, source=None):
+        self.planes, self.N, self.K, self.mode, self.source = planes, int(N), int(K), mode, source
 
 
 def presplit_b(b, mode="BF16X9", trans_b=False, stream=None):
@@ -301,7 +342,7 @@ def presplit_b(b, mode="BF16X9", trans_b=False, stream=None):
                         planes.data_ptr(), _stream_handle(stream))
     if st != STATUS_SUCCESS:
         raise EmuError(st, "emu_presplit_b")
-    return PresplitB(planes, N, K, mode)
+    return PresplitB(planes, N, K, mode, WeightSource(b if trans_b else b.t()))
 
 
 def sgemm_presplit(a, pb, trans_a=False, alpha=1.0, beta=0.0, c=None, bias=None, ksplit=0,

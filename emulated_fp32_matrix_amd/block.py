@@ -39,7 +39,7 @@ import os
 
 import torch
 
-from . import _PKG, MODES, PresplitB, _i64, _lib, _mode, _vp
+from . import _PKG, MODES, PresplitB, WeightSource, _i64, _lib, _mode, _vp
 from .linear import EmuLinear
 
 ACTIVATIONS = {"identity": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4, "tanh": 5}
@@ -124,10 +124,11 @@ def _mode_of(mode) -> int:
 
 class PresplitGated:
     """A gated projection's weight split once into the BF16 planes of ``mode``
-    (``presplit_gated``); ``planes`` is in the library's own layout."""
+    (``presplit_gated``); ``planes`` is in the library's own layout,
+    ``source`` identifies the weight."""
 
-    def __init__(self, planes, F, K, mode):
-        self.planes, self.F, self.K, self.mode = planes, int(F), int(K), mode
+    def __init__(self, planes, F, K, mode, source=None):
+        self.planes, self.F, self.K, self.mode, self.source = planes, int(F), int(K), mode, source
 
 
 def _planes(given, kind, shape, weight, mode):
@@ -141,6 +142,10 @@ def _planes(given, kind, shape, weight, mode):
     split = _mode_of(given.mode)
     if mode != split and (mode, split) != (MODES["AUTO"], MODES["BF16X9"]):
         raise ValueError(f"the planes are split for {given.mode}")
+    # (the backward pass reads the weight: both have to be the same)
+    if given.source is None:
+        raise ValueError("the planes do not say which weight they are those of")
+    given.source.check(weight)
     return given.planes, mode
 
 
@@ -159,7 +164,8 @@ def linear_act(x, weight, bias=None, activation="identity", residual=None, mode=
     ``activation``: a key of ``ACTIVATIONS``.  ``residual``: the output's
     shape, or None.  ``planes``: ``presplit_b(weight, mode, trans_b=True)`` of
     a weight that does not change between calls (the forward product then
-    skips its split).  Differentiable twice with respect to every tensor."""
+    skips its split); planes of another weight, and of one changed in place
+    since, raise ValueError.  Differentiable twice with respect to every tensor."""
     m = _mode_of(mode)
     if planes is not None:
         planes, m = _planes(planes, PresplitB, (getattr(planes, "N", 0), getattr(planes, "K", 0)), weight, m)
@@ -181,7 +187,8 @@ def gated_linear(x, weight, bias=None, activation="silu", mode="AUTO", planes=No
 def presplit_gated(weight, mode="BF16X9"):
     """Split a gated projection's weight [2 F, in] once, for ``gated_linear``
     calls in ``mode`` (BF16X9, also for AUTO, BF16X6, BF16X3 or BF16X1)."""
-    return PresplitGated(_ops.presplit_gated(weight, _mode_of(mode)), weight.shape[0] // 2, weight.shape[1], mode)
+    return PresplitGated(_ops.presplit_gated(weight, _mode_of(mode)), weight.shape[0] // 2, weight.shape[1], mode,
+                         WeightSource(weight))
 
 
 def wgrad(dz, x, want_db=False):
