@@ -22,7 +22,10 @@ along the last dimension (others are copied); work runs on the device's
 current stream.  Calls allocate their outputs and workspaces with torch, so
 they can be captured in a graph, which then owns them; a training step is
 captured after the results of eager steps with the same parameters have been
-released (a capture that finds them alive is refused).  As with
+released (a differentiable call that is captured while an input, or anything
+it was made from, belongs to a living eager result is refused: the captured
+backward pass would end the process; capturing the backward pass of a forward
+pass that was not captured is not seen here, nor by torch's own functions).  As with
 :class:`EmuLinear`, ``mode`` picks the arithmetic of the products; the weight
 gradient's is FP32.
 

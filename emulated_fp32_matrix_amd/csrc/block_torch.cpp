@@ -23,6 +23,7 @@
 #include <torch/extension.h>
 
 #include <stdexcept>
+#include <unordered_set>
 
 #include "emu_block.h"
 
@@ -156,29 +157,48 @@ bool wants_grad(std::initializer_list<const Tensor*> ts)
     return false;
 }
 
-// Refuses a call captured in a graph whose leaves still belong to an eager
-// call.  A leaf's gradient node keeps the stream of the first call that used
-// the leaf, as long as any result of it lives; a captured backward pass would
+// Refuses a differentiable call captured in a graph whose inputs come from
+// outside of the capture.  A gradient node keeps the stream of the call that
+// made it (a leaf's, of the first call that used the leaf, as long as any
+// result of it lives); a captured backward pass that reaches the node would
 // make that stream wait for the captured one, and ending such a capture ends
-// the process.
+// the process.  Every node that the inputs lead to has to be on a stream of
+// this capture.
 void claim_leaves(const OnDevice& on, std::initializer_list<const Tensor*> ts)
 {
-    hipStreamCaptureStatus status = hipStreamCaptureStatusNone;
-    if (hipStreamIsCapturing(on.stream, &status) != hipSuccess) {
-        (void)hipGetLastError();   // (must not surface in a later launch check)
-        return;
-    }
-    if (status == hipStreamCaptureStatusNone) return;
-    for (const Tensor* t : ts) {
-        if (!t->defined() || !t->requires_grad() || !t->is_leaf()) continue;
-        const auto node = torch::autograd::impl::try_get_grad_accumulator(*t);
-        if (!node) continue;
-        const auto s = node->stream();
-        if (s.has_value() && c10::hip::HIPStreamMasqueradingAsCUDA(*s).stream() != on.stream)
-            TORCH_CHECK(false,
+    const auto capture_of = [](hipStream_t s) -> unsigned long long {
+        hipStreamCaptureStatus status = hipStreamCaptureStatusNone;
+        unsigned long long id = 0;
+        // (the default stream is never captured, and asking it may fail)
+        if (s == nullptr) return 0;
+        if (hipStreamGetCaptureInfo(s, &status, &id) != hipSuccess) {
+            (void)hipGetLastError();   // (must not surface in a later launch check)
+            return 0;
+        }
+        return status == hipStreamCaptureStatusActive ? id : 0;
+    };
+    const unsigned long long capture = capture_of(on.stream);
+    if (capture == 0) return;
+    std::unordered_set<torch::autograd::Node*> seen;
+    std::vector<std::shared_ptr<torch::autograd::Node>> todo;
+    const auto visit = [&](std::shared_ptr<torch::autograd::Node> node) {
+        if (node && seen.insert(node.get()).second) todo.push_back(std::move(node));
+    };
+    for (const Tensor* t : ts)
+        if (t->defined() && t->requires_grad())
+            visit(t->is_leaf() ? torch::autograd::impl::try_get_grad_accumulator(*t) : t->grad_fn());
+    while (!todo.empty()) {
+        const auto node = std::move(todo.back());
+        todo.pop_back();
+        const auto stream = node->stream();
+        if (stream.has_value()) {
+            const hipStream_t s = c10::hip::HIPStreamMasqueradingAsCUDA(*stream).stream();
+            TORCH_CHECK(s == on.stream || capture_of(s) == capture,
                         "capturing a differentiable call whose parameters or inputs still belong to the results of an "
-                        "earlier call on another stream: release those results first, or make the earlier call on the "
-                        "capturing stream");
+                        "earlier call on another stream: release those results (or detach the inputs) first, or make "
+                        "the earlier call on the capturing stream");
+        }
+        for (const auto& edge : node->next_edges()) visit(edge.function);
     }
 }
 
@@ -720,6 +740,7 @@ std::tuple<Tensor, optional<Tensor>> wgrad(const Tensor& dz, const Tensor& x, bo
     TORCH_CHECK_VALUE(dz.dim() == 2 && x.dim() == 2, "dz and x must be 2-D");
     TORCH_CHECK_VALUE(dz.size(0) == x.size(0), "row counts differ: ", dz.size(0), " vs ", x.size(0));
     if (wants_grad({&dz, &x})) {
+        claim_leaves(OnDevice(dz), {&dz, &x});
         variable_list g = WeightGrad::apply(dz, x, want_db, (int64_t)EMU_MODE_AUTO);
         return {g[0], want_db ? optional<Tensor>(g[1]) : std::nullopt};
     }
@@ -735,6 +756,7 @@ Tensor act_grad(const Tensor& dy, const Tensor& z, int64_t act)
     check(dy, "dy");
     check_like(z, "z", dy);
     TORCH_CHECK_VALUE(dy.dim() == 2 && dy.sizes() == z.sizes(), "dy and z must be matrices of one shape");
+    if (wants_grad({&dy, &z})) claim_leaves(OnDevice(dy), {&dy, &z});
     return ActBackward::apply(dy, z, act, false);
 }
 
