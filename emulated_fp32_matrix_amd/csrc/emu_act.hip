@@ -56,18 +56,19 @@ __device__ __forceinline__ f32x4_t add_bias(const BlockEpilogue& ep, f32x4_t t, 
     return t;
 }
 
+// t null: a product of zeros (K = 0).
 __global__ __launch_bounds__(256) void epilogue_kernel(int64_t M, int N, const float* t, int64_t ldt,
                                                        BlockEpilogue ep, int groups, int rows_per_wg)
 {
     with_act(ep.act, [&]<int ACT>() {
         each_group(M, groups, rows_per_wg, [&](int64_t r, int c) {
-            f32x4_t z = add_bias(ep, load4(t + r * ldt, c, N), 0, c, N);
+            f32x4_t z = add_bias(ep, t != nullptr ? load4(t + r * ldt, c, N) : f32x4_t{}, 0, c, N);
             if (ep.Z != nullptr) store4(ep.Z + r * ep.ldz, c, N, z);
             f32x4_t o;
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[e] = act_value<ACT>(z[e]);
             if (ep.gated) {
-                f32x4_t u = add_bias(ep, load4(t + r * ldt + N, c, N), N, c, N);
+                f32x4_t u = add_bias(ep, t != nullptr ? load4(t + r * ldt + N, c, N) : f32x4_t{}, N, c, N);
                 if (ep.Z != nullptr) store4(ep.Z + r * ep.ldz + N, c, N, u);
                 o = o * u;
             } else if (ep.R != nullptr) {

@@ -113,9 +113,17 @@ double tiles_us(int64_t M, int64_t N, int64_t K, int bands, bool have_planes, bo
 // faster: the predictions' error.
 constexpr double kFewError = 1.1;
 
+// Columns of a product past which the one-launch kernels are not taken: a
+// launch holds less than 2^32 threads along the columns, which the FP32 kernel
+// spends 32 on each.
+constexpr int64_t kOneLaunchCols = (int64_t)1 << 26;
+
 // Below these the kernels' formulas are not asked: the emulated one-launch
 // kernel reads four k (and columns of a K x N operand) at a time.
-bool few_runs(int64_t M, int64_t N, int64_t K) { return K >= 4 && N >= 4 && M <= ((int64_t)1 << 20); }
+bool few_runs(int64_t M, int64_t N, int64_t K)
+{
+    return K >= 4 && N >= 4 && M <= ((int64_t)1 << 20) && N <= kOneLaunchCols;
+}
 
 size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
 
@@ -166,7 +174,7 @@ Route route_of(const emu::GemmArgs& g, bool is_gated, emu_mode_t mode, bool have
         else if (emu::api_plan(g.M, g.N, g.K, true, num_cu).split == 1)
             plan = std::fmax(plan, tiles_us(g.M, g.N, g.K, 5, have_planes, copies));
         if (copies) plan = std::fmax(plan, emu::api_predict_us(g.M, g.N, g.K) + 4.0 + 8.0 * (double)g.M * (double)g.K / 4.0e6);
-        const double rows = have_planes || g.M > ((int64_t)1 << 20) ? plan : rows_us(g.M, g.N, g.K, is_gated);
+        const double rows = have_planes || g.M > ((int64_t)1 << 20) || g.N > kOneLaunchCols ? plan : rows_us(g.M, g.N, g.K, is_gated);
         const double few = few_runs(g.M, g.N, g.K) ? few_us(g.M, g.N, g.K, 5, r.wide) : plan;
         r.rows = rows < plan && rows <= few;
         r.few = !r.rows && kFewError * few < plan;
@@ -236,6 +244,8 @@ emu_status_t product(emu::GemmArgs g, int64_t n_out, const BlockEpilogue& ep, em
     emu::DeviceInfo dev;
     if (!emu::api_current_device(dev)) return EMU_STATUS_NOT_SUPPORTED;
     const Route r = route_of(g, ep.gated != 0, mode, g.Bplanes != nullptr, dev.num_cu);
+    if (r.rows && g.N > kOneLaunchCols)   // (K = 0)
+        return from_hip(emu::launch_epilogue(g.M, n_out, nullptr, 0, ep, s));
     if (r.rows)
         return from_hip(emu::launch_rows_gemm(g.trans_b, g.M, n_out, g.K, g.A, g.lda, g.B, g.ldb, ep, s));
     if (r.few)

@@ -54,7 +54,7 @@ hipError_t launch_zero(float* p, int64_t n, hipStream_t s);
 hipError_t launch_column_join(const float* part, int64_t parts, int64_t stride, int64_t total, int64_t cols,
                               float* out0, float* out1, hipStream_t s);
 
-// C from the product t (M x N, gated: M x 2N; ldt).
+// C from the product t (M x N, gated: M x 2N; ldt), or from zeros (t null).
 hipError_t launch_epilogue(int64_t M, int64_t N, const float* t, int64_t ldt, const BlockEpilogue& ep,
                            hipStream_t s);
 // The epilogue of a K-split launch's split tiles (emu_launch.h): t is the sum of
