@@ -281,6 +281,10 @@ struct WeightGrads {
     Tensor dw, db, dz;
 };
 
+// In the place of a weight gradient's x where only db is wanted: its rows, no
+// columns.
+Tensor no_columns(const Rows& x) { return at::empty({x.n, 0}, x.keep.options()); }
+
 WeightGrads weight_grad(const Rows& dz, const Rows& x, bool want_db)
 {
     const int64_t rows = dz.n, M = dz.width, N = x.width;
@@ -536,7 +540,7 @@ struct Layer : Function<Layer> {
                     dz = z.defined() ? act_backward(Rows(gy, N), Rows(z, z.size(1)), (int)act, is_gated) : gy;
                 if (gz.defined()) dz = dz.defined() ? dz + gz : gz;
                 if (want_w || want_b) {
-                    WeightGrads g = weight_grad(Rows(dz, weight.size(0)), x2, want_b);
+                    WeightGrads g = weight_grad(Rows(dz, weight.size(0)), want_w ? x2 : Rows(no_columns(x2), 0), want_b);
                     if (want_w) out[1] = g.dw;
                     out[2] = g.db;
                 }
@@ -553,7 +557,7 @@ struct Layer : Function<Layer> {
         if (gz.defined()) dz = dz.defined() ? dz + gz : gz;
         if (want_x) out[0] = Product::apply(dz, weight, false, mode).view(x.sizes());
         if (want_w || want_b) {
-            variable_list g = WeightGrad::apply(dz, flat(x, x2.n, K), want_b, mode);
+            variable_list g = WeightGrad::apply(dz, want_w ? flat(x, x2.n, K) : no_columns(x2), want_b, mode);
             if (want_w) out[1] = g[0];
             if (want_b) out[2] = g[1];
         }

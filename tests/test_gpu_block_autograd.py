@@ -1,4 +1,5 @@
-"""The block operators inside autograd: outputs changed in place."""
+"""The block operators inside autograd: outputs changed in place, frozen
+parameters."""
 import pytest
 import torch
 
@@ -76,3 +77,54 @@ def test_outputs_may_be_changed_in_place(name):
             # (negation and doubling are exact, sums of several paths may be ordered otherwise)
             assert float((got - one).detach().abs().max()) <= 8 * U * float(one.detach().abs().max())
             got.neg_()   # the last derivatives too
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("create_graph", [False, True])
+def test_bias_alone(gated, create_graph):
+    """The weight frozen, the bias trained: its gradient without the weight's
+    product, which would need an array of the weight's size."""
+    block = _block()
+    rows, K, N = 700, 2048, 4096
+    x, w, b = _randn(1, rows, K), _randn(2, N, K, scale=K**-0.5), _randn(3, N).requires_grad_(True)
+    f = (lambda: block.gated_linear(x, w, b)) if gated else (lambda: block.linear_act(x, w, b, "silu"))
+    y = f()
+    g = _randn(4, *y.shape)
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    (db,) = torch.autograd.grad(y, b, g, create_graph=create_graph)
+    used = torch.cuda.max_memory_allocated() - before
+    z, zb = ref.product(x.double(), w.double(), b, "AUTO")
+    F = N // 2
+    if gated:
+        d1, _, s1, _ = ref.slopes("silu", z[:, :F])
+        dz = torch.cat([g * z[:, F:] * d1, g * ref.act("silu", z[:, :F])], dim=1)
+        size = torch.cat([g.abs() * (z[:, F:].abs() + zb[:, F:]) * (24 * U * s1 + 1.2 * zb[:, :F]) + g.abs() * zb[:, F:] * d1.abs(),
+                          g.abs() * (ref.act_bound("silu", z[:, :F]) + 1.2 * zb[:, :F])], dim=1) + 2 * U * dz.abs()
+    else:
+        d1, _, s1, _ = ref.slopes("silu", z)
+        dz = g * d1
+        size = g.abs() * (24 * U * s1 + 1.2 * zb) + U * dz.abs()
+    assert ref.worst(db.detach(), dz.sum(0), (rows + 10) * U * dz.abs().sum(0) + 1.01 * size.sum(0) + 1e-30) <= 1.0
+    say(f"bias alone, gated {gated}, create_graph {create_graph}: {used} bytes")
+    # dz (rows x N) and, of the sums, at most 128 partial rows
+    assert used <= 4 * (rows * N + 130 * N) + (1 << 16)
+
+
+@pytest.mark.parametrize("bias_trained,weight_trained", [(True, False), (False, True), (True, True), (False, False)])
+def test_frozen_parameters(bias_trained, weight_trained):
+    """Only what is trained gets a gradient, and the one that it gets with
+    everything trained (the bias' to the order of its sum)."""
+    block = _block()
+    x, w, b, r = _randn(1, 300, 64), _randn(2, 80, 64, scale=0.125), _randn(3, 80), _randn(4, 300, 80)
+    g = _randn(5, 300, 80)
+    every = [t.clone().requires_grad_(True) for t in (x, w, b, r)]
+    full = torch.autograd.grad(block.linear_act(*every[:3], "gelu", every[3]), every, g)
+    some = [t.clone().requires_grad_(on) for t, on in zip((x, w, b, r), (True, weight_trained, bias_trained, False))]
+    y = block.linear_act(*some[:3], "gelu", some[3])
+    leaves = [t for t in some if t.requires_grad]
+    for create in (False, True):
+        for t, got in zip(leaves, torch.autograd.grad(y, leaves, g, create_graph=create, retain_graph=True)):
+            at = next(i for i, s in enumerate(some) if s is t)
+            assert float((got - full[at]).abs().max()) <= 64 * U * float(full[at].abs().max()) + (300 * U * float(g.abs().sum(0).max()) if at == 2 else 0)
