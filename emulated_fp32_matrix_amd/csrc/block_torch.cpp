@@ -285,8 +285,16 @@ struct WeightGrads {
 // columns.
 Tensor no_columns(const Rows& x) { return at::empty({x.n, 0}, x.keep.options()); }
 
-WeightGrads weight_grad(const Rows& dz, const Rows& x, bool want_db)
+// Rows as the weight gradient takes them: at most 16,777,088 elements apart
+// (include/emu_block.h), as a slice of a large tensor may not have them.
+Rows near_rows(const Rows& r)
 {
+    return r.n > 1 && r.ld > 16777088 && r.ld > r.width ? Rows(r.keep.contiguous(), r.width) : r;
+}
+
+WeightGrads weight_grad(const Rows& far_dz, const Rows& far_x, bool want_db)
+{
+    const Rows dz = near_rows(far_dz), x = near_rows(far_x);
     const int64_t rows = dz.n, M = dz.width, N = x.width;
     WeightGrads g;
     g.dw = empty_rows(M, N, dz.keep);
@@ -302,8 +310,9 @@ WeightGrads weight_grad(const Rows& dz, const Rows& x, bool want_db)
 
 // The same with the activation's (or the gated product's) backward pass
 // inside, which also gives dz.
-WeightGrads weight_grad_from(const Rows& dy, const Rows& z, int act, const Rows& x, bool want_db, bool is_gated)
+WeightGrads weight_grad_from(const Rows& far_dy, const Rows& z, int act, const Rows& far_x, bool want_db, bool is_gated)
 {
+    const Rows dy = near_rows(far_dy), x = near_rows(far_x);
     const int64_t rows = dy.n, M = dy.width, N = x.width, wide = z.width;
     WeightGrads g;
     g.dz = empty_rows(rows, wide, dy.keep);

@@ -128,3 +128,27 @@ def test_frozen_parameters(bias_trained, weight_trained):
         for t, got in zip(leaves, torch.autograd.grad(y, leaves, g, create_graph=create, retain_graph=True)):
             at = next(i for i, s in enumerate(some) if s is t)
             assert float((got - full[at]).abs().max()) <= 64 * U * float(full[at].abs().max()) + (300 * U * float(g.abs().sum(0).max()) if at == 2 else 0)
+
+
+def test_rows_far_apart():
+    """A slice whose rows lie further apart than the weight gradient's kernel
+    reaches: as input, as output gradient, and in wgrad."""
+    block = _block()
+    far = torch.zeros(5, 17_000_000, device="cuda:0")
+    far[:, :112] = _randn(1, 5, 112)
+    x, g = far[:, :64], far[:, 64:112]
+    for K in (64, 8):
+        w, b = _randn(2, 48, K, scale=0.125).requires_grad_(True), _randn(3, 48).requires_grad_(True)
+        got = torch.autograd.grad(block.linear_act(x[:, :K], w, b, "silu"), (w, b), g)
+        want = torch.autograd.grad(block.linear_act(x[:, :K].contiguous(), w, b, "silu"), (w, b), g.contiguous())
+        assert all(torch.equal(u, v) for u, v in zip(got, want))
+        y = block.linear_act(x[:, :K], w, b)
+        assert torch.equal(torch.autograd.grad(y, w, g)[0], block.wgrad(g.contiguous(), x[:, :K].contiguous())[0])
+    assert all(torch.equal(u, v) for u, v in zip(block.wgrad(g, x, True), block.wgrad(g.contiguous(), x.contiguous(), True)))
+    wg = _randn(4, 96, 64, scale=0.125).requires_grad_(True)
+    got = torch.autograd.grad(block.gated_linear(x, wg), wg, g)[0]
+    assert torch.equal(got, torch.autograd.grad(block.gated_linear(x.contiguous(), wg), wg, g.contiguous())[0])
+    far_x = far[:, 100:100 + 300]   # wider than the fused pass takes
+    w = _randn(5, 48, 300, scale=0.05).requires_grad_(True)
+    got = torch.autograd.grad(block.linear_act(far_x, w, None, "gelu"), w, g)[0]
+    assert torch.equal(got, torch.autograd.grad(block.linear_act(far_x.contiguous(), w, None, "gelu"), w, g.contiguous())[0])
