@@ -112,13 +112,25 @@ struct Rows {
         keep = given.is_neg() ? given.resolve_neg() : given;
         const Tensor t = keep;
         n = 1;
-        for (int64_t d = 0; d + 1 < t.dim(); ++d) n *= t.size(d);
         ld = std::max<int64_t>(w, 1);
-        if (t.dim() == 2 && (w <= 1 || t.stride(1) == 1) && (n <= 1 || t.stride(0) >= w)) {
-            if (n > 1) ld = std::max<int64_t>(t.stride(0), 1);
-        } else if (!t.is_contiguous()) {
-            keep = t.contiguous();
+        // one distance between rows, over the dimensions of more than one
+        // element from the last but one on: the innermost's, if the others'
+        // strides are what the rows before them take
+        bool one = w <= 1 || t.stride(t.dim() - 1) == 1;
+        int64_t step = 0;
+        for (int64_t d = t.dim() - 2; d >= 0; --d) {
+            if (t.size(d) > 1) {
+                if (n == 1)
+                    step = t.stride(d);
+                else
+                    one = one && t.stride(d) == step * n;
+            }
+            n *= t.size(d);
         }
+        if (n > 1 && one && step >= w)
+            ld = std::max<int64_t>(step, 1);
+        else if (!t.is_contiguous() && (n > 1 || !one))
+            keep = t.contiguous();
     }
 };
 

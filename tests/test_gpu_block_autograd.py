@@ -1,5 +1,5 @@
 """The block operators inside autograd: outputs changed in place, frozen
-parameters."""
+parameters, inputs that are views."""
 import pytest
 import torch
 
@@ -152,3 +152,25 @@ def test_rows_far_apart():
     w = _randn(5, 48, 300, scale=0.05).requires_grad_(True)
     got = torch.autograd.grad(block.linear_act(far_x, w, None, "gelu"), w, g)[0]
     assert torch.equal(got, torch.autograd.grad(block.linear_act(far_x.contiguous(), w, None, "gelu"), w, g.contiguous())[0])
+
+
+def test_rows_of_one_stride_are_not_copied():
+    """A slice of the last dimension of a 3-D tensor has rows a fixed distance
+    apart: read where they are."""
+    block = _block()
+    wide = _randn(1, 40, 50, 600)
+    x = wide[:, :, 44:556]
+    want = block.layer_norm(x.contiguous())
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    y = block.layer_norm(x)
+    assert torch.cuda.max_memory_allocated() - before <= 4 * y.numel() + 512
+    assert torch.equal(y, want)
+    w = _randn(2, 48, 512, scale=0.05)
+    for view in (wide[:, :, 44:556], wide[::2, :, 44:556], wide[:, ::2, 44:556], wide[:, :1, 44:556], wide[:1, :, 44:556],
+                 wide.transpose(0, 1)[:, :, 44:556], wide[:1].expand(3, 50, 600)[:, :, 44:556], wide[:, 0, 44:556], wide[0, 0, 44:556],
+                 wide[:0, :, 44:556], wide[:, :, None, 44:556]):
+        flat = view.contiguous()
+        assert torch.equal(block.layer_norm(view), block.layer_norm(flat))
+        assert torch.equal(block.linear_act(view, w, None, "silu", mode="BF16X9"), block.linear_act(flat, w, None, "silu", mode="BF16X9"))
