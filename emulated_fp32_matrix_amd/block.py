@@ -87,11 +87,6 @@ for _name, _types in _SIGNATURES.items():
     getattr(_lib, _name).restype = _int
 
 
-def emu_block_version() -> int:
-    return int(_lib.emu_block_version())
-
-
-
 def _load_ops():
     path = os.path.join(_PKG, "_block_ops.so")
     if not os.path.exists(path):

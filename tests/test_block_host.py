@@ -203,3 +203,8 @@ def test_modules_hold_the_parameters_of_their_torch_counterparts():
     assert {k: tuple(v.shape) for k, v in ffn.state_dict().items()} == {
         "norm.weight": (8,), "norm.bias": (8,), "w_in": (12, 8), "b_in": (12,), "out.weight": (8, 6), "out.bias": (8,)}
     assert set(block.EmuGatedFFN(8, 6, bias=False, norm=False).state_dict()) == {"w_in", "out.weight"}
+
+
+def test_every_function_is_defined_once():
+    names = re.findall(r"^(?:def|class) (\w+)", open(block.__file__).read(), flags=re.M)
+    assert len(names) == len(set(names)) and "emu_block_version" in names
