@@ -60,13 +60,15 @@ struct OnDevice {
     }
 };
 
-// Refuses to read a tensor for something that would have to see the kernels,
+const Tensor* given(const optional<Tensor>& t) { return t.has_value() ? &*t : nullptr; }
+
+// Refuses to read tensors for something that would have to see the kernels,
 // which write to memory that torch only saw being allocated: the output would
 // lack its tangent (forward-mode derivatives), or a recorded program would
-// return that memory without what is written to it.
-void check_readable(const Tensor& t)
+// return that memory without what is written to it.  (Called for every tensor
+// of a call from outside, and for the gradients that a backward pass is given.)
+void check_readable(std::initializer_list<const Tensor*> ts)
 {
-    if (!t.defined()) return;
     using c10::impl::TorchDispatchModeKey;
     using c10::impl::TorchDispatchModeTLS;
     TORCH_CHECK_NOT_IMPLEMENTED(!torch::jit::tracer::isTracing(), "the block operators cannot be traced by torch.jit");
@@ -77,15 +79,13 @@ void check_readable(const Tensor& t)
     }
     constexpr c10::DispatchKeySet wrappers({c10::DispatchKey::Python, c10::DispatchKey::Functionalize,
                                             c10::DispatchKey::FuncTorchGradWrapper, c10::DispatchKey::FuncTorchBatched});
-    TORCH_CHECK_NOT_IMPLEMENTED(!t.key_set().has_any(wrappers),
-                                "the block operators take plain tensors, not those of a tracer, of a torch.func "
-                                "transform or of a subclass with its own dispatch");
-    TORCH_CHECK_NOT_IMPLEMENTED(!t._fw_grad(0).defined(), "the block operators have no forward-mode derivative");
-}
-
-void check_readable(const optional<Tensor>& t)
-{
-    if (t.has_value()) check_readable(*t);
+    for (const Tensor* t : ts) {
+        if (t == nullptr || !t->defined()) continue;
+        TORCH_CHECK_NOT_IMPLEMENTED(!t->key_set().has_any(wrappers),
+                                    "the block operators take plain tensors, not those of a tracer, of a torch.func "
+                                    "transform or of a subclass with its own dispatch");
+        TORCH_CHECK_NOT_IMPLEMENTED(!t->_fw_grad(0).defined(), "the block operators have no forward-mode derivative");
+    }
 }
 
 void check(const Tensor& t, const char* name)
@@ -106,10 +106,8 @@ struct Rows {
     Tensor keep;
     int64_t n, width, ld;
     const float* data() const { return keep.numel() ? keep.const_data_ptr<float>() : nullptr; }
-    Rows(const Tensor& given, int64_t w) : width(w)
+    Rows(const Tensor& given, int64_t w) : keep(given.is_neg() ? given.resolve_neg() : given), width(w)
     {
-        check_readable(given);   // (gradients come here unchecked)
-        keep = given.is_neg() ? given.resolve_neg() : given;
         const Tensor t = keep;
         n = 1;
         ld = std::max<int64_t>(w, 1);
@@ -439,6 +437,7 @@ struct WeightGrad : Function<WeightGrad> {
         const auto saved = ctx->get_saved_variables();
         const Tensor &dz = saved[0], &x = saved[1], &P = grads[0];
         const Tensor q = grads.size() > 1 ? grads[1] : Tensor();
+        check_readable({&P, &q});
         const int64_t mode = ctx->saved_data["mode"].toInt();
         Tensor gdz, gx;
         if (ctx->needs_input_grad(0)) {
@@ -454,6 +453,7 @@ variable_list Product::backward(AutogradContext* ctx, variable_list grads)
 {
     const auto saved = ctx->get_saved_variables();
     const Tensor &a = saved[0], &w = saved[1], &g = grads[0];
+    check_readable({&g});
     const bool trans = ctx->saved_data["trans"].toBool();
     const int64_t mode = ctx->saved_data["mode"].toInt();
     Tensor ga, gw;
@@ -480,6 +480,7 @@ struct ActBackward : Function<ActBackward> {
         const auto saved = ctx->get_saved_variables();
         const emu_act_t act = (emu_act_t)ctx->saved_data["act"].toInt();
         const Tensor &dy_t = saved[0], &z_t = saved[1], &v_t = grads[0];
+        check_readable({&v_t});
         const Rows dy(dy_t, dy_t.size(1)), z(z_t, z_t.size(1)), v(v_t, v_t.size(1));
         variable_list out(4);
         if (ctx->needs_input_grad(0)) out[0] = empty_rows(dy.n, dy.width, dy.keep);
@@ -541,6 +542,7 @@ struct Layer : Function<Layer> {
         const bool is_gated = ctx->saved_data["gated"].toBool(), has_bias = ctx->saved_data["bias"].toBool();
         const bool has_res = ctx->saved_data["residual"].toBool();
         variable_list out(8);
+        check_readable({&gy, &gz});
         if (!gy.defined() && !gz.defined()) return out;
         const bool want_x = ctx->needs_input_grad(0), want_w = ctx->needs_input_grad(1);
         const bool want_b = has_bias && ctx->needs_input_grad(2);
@@ -590,10 +592,7 @@ Tensor layer_call(const Tensor& x, const Tensor& weight, const optional<Tensor>&
                   const optional<Tensor>& residual_in, int64_t act, int64_t mode, bool is_gated,
                   const optional<Tensor>& planes)
 {
-    check_readable(x);
-    check_readable(weight);
-    check_readable(bias_in);
-    check_readable(residual_in);
+    check_readable({&x, &weight, given(bias_in), given(residual_in)});
     check(x, "x");
     check_like(weight, "weight", x);
     TORCH_CHECK_VALUE(weight.dim() == 2, "weight must be 2-D");
@@ -668,10 +667,8 @@ struct LayerNormBackward : Function<LayerNormBackward> {
         const int64_t cols = saved[1].size(-1);
         const Rows gy(saved[0], cols), x(saved[1], cols);
         const Tensor &w = saved[2], &stats = saved[3];
-        const auto plain = [](const Tensor& t) {
-            check_readable(t);
-            return t.defined() ? t.resolve_neg().contiguous() : t;
-        };
+        check_readable({&v, &p_in, &q_in});
+        const auto plain = [](const Tensor& t) { return t.defined() ? t.resolve_neg().contiguous() : t; };
         const Tensor p = plain(p_in), q = plain(q_in);
         variable_list out(5);
         if (ctx->needs_input_grad(0)) out[0] = at::empty(saved[1].sizes(), x.keep.options());
@@ -716,6 +713,7 @@ struct LayerNorm : Function<LayerNorm> {
         const bool want_x = ctx->needs_input_grad(0), want_w = has_w && ctx->needs_input_grad(1);
         const bool want_b = has_b && ctx->needs_input_grad(has_w ? 2 : 1);
         variable_list out(4);
+        check_readable({&gy});
         if (!gy.defined() || !(want_x || want_w || want_b)) return out;
         if (at::GradMode::is_enabled()) {
             const int64_t want = (want_x ? 1 : 0) | (want_w ? 2 : 0) | (want_b ? 4 : 0);
@@ -737,9 +735,7 @@ struct LayerNorm : Function<LayerNorm> {
 
 Tensor layer_norm(const Tensor& x, const optional<Tensor>& weight_in, const optional<Tensor>& bias_in, double eps)
 {
-    check_readable(x);
-    check_readable(weight_in);
-    check_readable(bias_in);
+    check_readable({&x, given(weight_in), given(bias_in)});
     check(x, "x");
     TORCH_CHECK_VALUE(x.dim() >= 1 && x.size(-1) >= 1 && x.size(-1) <= EMU_LAYER_NORM_MAX_COLS,
                       "layer_norm takes 1 to ", EMU_LAYER_NORM_MAX_COLS, " features, not ", x.sizes());
@@ -758,8 +754,7 @@ Tensor layer_norm(const Tensor& x, const optional<Tensor>& weight_in, const opti
 
 std::tuple<Tensor, optional<Tensor>> wgrad(const Tensor& dz, const Tensor& x, bool want_db)
 {
-    check_readable(dz);
-    check_readable(x);
+    check_readable({&dz, &x});
     check(dz, "dz");
     check_like(x, "x", dz);
     TORCH_CHECK_VALUE(dz.dim() == 2 && x.dim() == 2, "dz and x must be 2-D");
@@ -776,8 +771,7 @@ std::tuple<Tensor, optional<Tensor>> wgrad(const Tensor& dz, const Tensor& x, bo
 // dz = dy act'(z) for matrices, differentiable once.
 Tensor act_grad(const Tensor& dy, const Tensor& z, int64_t act)
 {
-    check_readable(dy);
-    check_readable(z);
+    check_readable({&dy, &z});
     check(dy, "dy");
     check_like(z, "z", dy);
     TORCH_CHECK_VALUE(dy.dim() == 2 && dy.sizes() == z.sizes(), "dy and z must be matrices of one shape");
@@ -787,6 +781,7 @@ Tensor act_grad(const Tensor& dy, const Tensor& z, int64_t act)
 
 Tensor presplit_gated(const Tensor& w, int64_t mode)
 {
+    check_readable({&w});
     check(w, "weight");
     TORCH_CHECK_VALUE(w.dim() == 2 && w.size(0) % 2 == 0, "weight must hold as many gate rows as up rows");
     const Rows r(w, w.size(1));
