@@ -31,7 +31,8 @@ gradient's is FP32.
 
 The functions and their derivatives are native (``csrc/block_torch.cpp``);
 this module names them and holds the modules.  Wrong types raise TypeError,
-wrong shapes and names ValueError, a failing library call :class:`EmuError`.
+wrong shapes and names ValueError, a failing library call :class:`EmuError` (a
+RuntimeError; in a backward pass autograd passes on the RuntimeError alone).
 """
 from __future__ import annotations
 

@@ -129,7 +129,8 @@ __global__ __launch_bounds__(SH::NT) void norm_kernel(int64_t rows, int cols, co
         // The sum's rounding, up to a few units of the mean, is a deviation of
         // its own in a row far from zero (1,000,003 in all of 200 columns gave
         // xhat = 1): the centred row's mean is added, which leaves the mean's
-        // own rounding.  (NaN where the row overflows: mu stays.)
+        // own rounding.  (Not finite where the row is not or overflows: mu
+        // stays.)
         float c = 0.0f;
 #pragma unroll
         for (int j = 0; j < SH::NV; ++j)
@@ -139,7 +140,7 @@ __global__ __launch_bounds__(SH::NT) void norm_kernel(int64_t rows, int cols, co
         float s0[1] = {c};
         row_sum<SH>(s0, lds);
         c = s0[0] / n;
-        if (c == c) mu = mu + c;
+        if (__builtin_fabsf(c) < __builtin_inff()) mu = mu + c;
 #pragma unroll
         for (int j = 0; j < SH::NV; ++j)
 #pragma unroll

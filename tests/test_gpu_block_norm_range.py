@@ -82,3 +82,25 @@ def test_columns_past_the_end_stay_out(cols):
     assert ref.worst(dx[1:2], value, bnd) <= 1.0
     value, bnd = ref.norm_backward(x[1:2], w.detach(), dy[1:2], 1e-5)[1]
     assert ref.worst(dw, value, bnd) <= 1.0   # (xhat is zero in the other rows)
+
+
+def test_means_that_are_not_finite():
+    """An infinity, a NaN or a sum past FP32's range: the mean that the FP32
+    formula gives is kept, and the row's y is NaN; its neighbours are as alone."""
+    block = _block()
+    inf = float("inf")
+    for cols in (100, 256, 3000):
+        x = _randn(cols, 6, cols)
+        x[1] = 3e38
+        x[2] = -3e38
+        x[3, 7] = inf
+        x[4, 9] = float("nan")
+        stats = torch.empty(2, 6, device="cuda:0")
+        y = torch.empty_like(x)
+        assert block._lib.emu_layer_norm(6, cols, x.data_ptr(), cols, None, None, 1e-5, y.data_ptr(), cols, stats[0].data_ptr(),
+                                         stats[1].data_ptr(), torch.cuda.current_stream().cuda_stream or None) == 0
+        mean = stats[0].tolist()
+        assert mean[1] == inf and mean[2] == -inf and mean[3] == inf and mean[4] != mean[4]
+        assert bool(torch.isnan(y[1:5]).all())
+        for r in (0, 5):
+            assert torch.equal(y[r], block.layer_norm(x[r:r + 1])[0])
