@@ -1,5 +1,5 @@
 """Build the HIP library ``libemu_sgemm.so`` in-tree for gfx950, and the torch
-binding of its block operators, ``_block_ops.so`` (host code).
+binding of its block and attention operators, ``_block_ops.so`` (host code).
 
 Every ``csrc/*.hip`` file is compiled by hipcc to an object under
 ``_build/`` (in parallel, beside the binding's), then linked into the package
@@ -56,15 +56,14 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
-def _compile_ops(verbose: bool) -> str:
-    """The torch binding's object: g++, torch's headers."""
+def _compile_ops(src: str, verbose: bool) -> str:
+    """An object of the torch binding: g++, torch's headers."""
     import sysconfig
 
     import torch
     from torch.utils.cpp_extension import include_paths
 
-    src = os.path.join(CSRC, "block_torch.cpp")
-    obj = os.path.join(BUILD_DIR, "block_torch.cpp.o")
+    obj = os.path.join(BUILD_DIR, os.path.basename(src) + ".o")
     rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
     dirs = [os.path.join(ROOT, "include"), *include_paths(), sysconfig.get_paths()["include"],
             os.path.join(rocm, "include")]
@@ -82,14 +81,14 @@ def _compile_ops(verbose: bool) -> str:
     return obj
 
 
-def _link_ops(obj: str, verbose: bool) -> None:
+def _link_ops(objs: list[str], verbose: bool) -> None:
     import torch
 
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
     out = os.path.join(PKG, OPS_NAME)
     tmp = out + ".tmp"
     # libemu_sgemm.so lies beside it; torch's libraries are loaded before it
-    cmd = ["g++", "-shared", "-fPIC", obj, "-o", tmp, os.path.join(PKG, LIB_NAME), "-Wl,-rpath,$ORIGIN", f"-L{libs}",
+    cmd = ["g++", "-shared", "-fPIC", *objs, "-o", tmp, os.path.join(PKG, LIB_NAME), "-Wl,-rpath,$ORIGIN", f"-L{libs}",
            "-lc10", "-lc10_hip", "-ltorch", "-ltorch_cpu", "-ltorch_python", os.path.join(libs, "libamdhip64.so")]
     if verbose:
         print(" ".join(cmd), flush=True)
@@ -102,10 +101,11 @@ def build(verbose: bool = False) -> str:
     returns the library's path."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.hip")))
-    with cf.ThreadPoolExecutor(max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
-        ops = ex.submit(_compile_ops, verbose)
+    bindings = sorted(glob.glob(os.path.join(CSRC, "*_torch.cpp")))
+    with cf.ThreadPoolExecutor(max(1, min(len(srcs) + len(bindings), os.cpu_count() or 1))) as ex:
+        ops = [ex.submit(_compile_ops, s, verbose) for s in bindings]
         objs = list(ex.map(lambda s: _compile(s, verbose), srcs))
-        ops_obj = ops.result()
+        ops_objs = [o.result() for o in ops]
     out = os.path.join(PKG, LIB_NAME)
     tmp = out + ".tmp"
     cmd = [_hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", f"-Wl,-soname,{LIB_NAME}", *objs, "-o", tmp]
@@ -113,7 +113,7 @@ def build(verbose: bool = False) -> str:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
     os.replace(tmp, out)
-    _link_ops(ops_obj, verbose)
+    _link_ops(ops_objs, verbose)
     return out
 
 

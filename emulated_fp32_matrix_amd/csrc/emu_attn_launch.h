@@ -1,0 +1,110 @@
+// Internal interface between the C-ABI layer of the attention operators
+// (emu_attn_api.hip) and their kernels.  Not installed; callers use
+// include/emu_attention.h.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "emu_attention.h"
+
+namespace emu {
+
+// One attention call after validation.  A key and value head's rows are its
+// queries times the heads that share it: row r is query r / share, head
+// kv_head * share + r % share, so that the sharing heads read keys once.
+struct AttnArgs {
+    int batch, queries, keys, heads, kv_heads, share, dim;
+    int64_t rows;            // queries * share
+    float scale;
+    const float* bias;       // key bias or null
+    int64_t bias_b, bias_k;
+    const uint8_t* mask;     // key mask or null
+    int64_t mask_b, mask_k;
+    const void* lengths;     // or null
+    int lengths_64;
+};
+
+// How a pass is cut into pieces of work: a team of `waves` waves takes
+// `tiles` tiles of 16 (of its own side) per wave and one of `splits` ranges of
+// the other side.
+struct AttnPlan {
+    int waves, tiles, splits;
+    int64_t own;             // pieces along the team's own side
+};
+
+// Pass over rows (the keys stream by) and pass over keys (the rows stream by)
+// of the forward pass (order 0, rows only), its backward pass (1) and that
+// one's (2).
+AttnPlan attn_rows_plan(const AttnArgs& a, int order);
+AttnPlan attn_keys_plan(const AttnArgs& a, int order);
+
+// The forward pass; partial: null unless plan.splits > 1.
+size_t attn_forward_partial(const AttnArgs& a, const AttnPlan& p);
+hipError_t launch_attn_forward(const AttnArgs& a, const AttnPlan& p, emu_heads_t q, emu_heads_t k, emu_heads_t v,
+                               float* out, float* stats, float* partial, hipStream_t s);
+
+// Floats of partial sums (0 for one split): of a result with the queries'
+// shape, of one with the keys' shape, of the bias gradient.
+size_t attn_rows_partial(const AttnArgs& a, const AttnPlan& p);
+size_t attn_keys_partial(const AttnArgs& a, const AttnPlan& p);
+size_t attn_bias_partial(const AttnArgs& a, const AttnPlan& p);
+
+// delta: a float per row, written by the pass over rows and read by the pass
+// over keys.  dq may be null (then only delta is written).
+hipError_t launch_attn_backward_rows(const AttnArgs& a, const AttnPlan& p, emu_heads_t dout, emu_heads_t q,
+                                     emu_heads_t k, emu_heads_t v, const float* out, const float* stats,
+                                     float* delta, float* dq, float* partial, hipStream_t s);
+hipError_t launch_attn_backward_keys(const AttnArgs& a, const AttnPlan& p, emu_heads_t dout, emu_heads_t q,
+                                     emu_heads_t k, emu_heads_t v, const float* stats, const float* delta,
+                                     float* dk, float* dv, float* dbias, float* partial_k, float* partial_v,
+                                     float* partial_b, hipStream_t s);
+
+// The backward pass's backward pass.
+struct AttnSeconds {
+    emu_heads_t vq, vk, vv;  // data null: zeros
+    const float* vbias;      // or null
+    int64_t vbias_b, vbias_k;
+    emu_heads_t dout, q, k, v;
+    const float* out;
+    const float* stats;
+};
+// sums: [splits][rows of the call][2] partial sums over keys; delta as above.
+hipError_t launch_attn_second_sums(const AttnArgs& a, const AttnPlan& p, const AttnSeconds& t, float* delta,
+                                   float* sums, hipStream_t s);
+hipError_t launch_attn_second_rows(const AttnArgs& a, const AttnPlan& p, const AttnSeconds& t, const float* delta,
+                                   const float* sums, float* gdout, float* gq, float* partial_o, float* partial_q,
+                                   hipStream_t s);
+hipError_t launch_attn_second_keys(const AttnArgs& a, const AttnPlan& p, const AttnSeconds& t, const float* delta,
+                                   const float* sums, int sum_splits, float* gk, float* gv, float* gbias,
+                                   float* partial_k, float* partial_v, float* partial_b, hipStream_t s);
+
+// out[o][i] = sum over s of in[o][s][i], s in order; outer x inner results.
+hipError_t launch_attn_join(int64_t outer, int64_t splits, int64_t inner, const float* in, float* out, hipStream_t s);
+
+struct RotaryArgs {
+    int64_t batch, tokens;
+    int heads, dim, pairs, layout, inverse;
+    emu_heads_t x;
+    const int64_t* positions;
+    int64_t pos_b, pos_t;
+    const uint64_t* turns;
+    float magnitude;
+    float* y;
+};
+hipError_t launch_rotary(const RotaryArgs& a, hipStream_t s);
+
+struct DropoutArgs {
+    int64_t rows, cols;
+    const float* x;
+    int64_t ldx;
+    uint64_t threshold;      // of a 32-bit word: 0 .. 2^32
+    float scale;
+    const int64_t* seed;
+    const float* r;          // or null
+    int64_t ldr;
+    float* y;
+    int64_t ldy;
+};
+hipError_t launch_dropout(const DropoutArgs& a, hipStream_t s);
+
+}  // namespace emu
