@@ -87,6 +87,12 @@ struct Layout {
 
 size_t rows_of(const AttnArgs& a) { return (size_t)a.batch * a.queries * a.heads; }
 
+size_t forward_bytes(const AttnArgs& a)
+{
+    if (!has_rows(a) || emu::attn_whole(a, 0)) return 0;
+    return round256(emu::attn_forward_partial(a, emu::attn_rows_plan(a, 0)) * sizeof(float));
+}
+
 struct BackwardSpace {
     AttnPlan rows, keys;
     float *delta, *dq, *dk, *dv, *db;
@@ -94,6 +100,12 @@ struct BackwardSpace {
     BackwardSpace(const AttnArgs& a, void* ws) : rows(emu::attn_rows_plan(a, 1)), keys(emu::attn_keys_plan(a, 1))
     {
         Layout l(ws);
+        delta = dq = dk = dv = db = nullptr;
+        if (emu::attn_whole(a, 1)) {
+            db = l.take(emu::attn_whole_partial(a));
+            bytes = l.bytes;
+            return;
+        }
         delta = l.take(rows_of(a));
         dq = l.take(emu::attn_rows_partial(a, rows));
         dk = l.take(emu::attn_keys_partial(a, keys));
@@ -110,6 +122,12 @@ struct SecondSpace {
     SecondSpace(const AttnArgs& a, void* ws) : rows(emu::attn_rows_plan(a, 2)), keys(emu::attn_keys_plan(a, 2))
     {
         Layout l(ws);
+        delta = sums = go = gq = gk = gv = gb = nullptr;
+        if (emu::attn_whole(a, 2)) {
+            gb = l.take(emu::attn_whole_partial(a));
+            bytes = l.bytes;
+            return;
+        }
         delta = l.take(rows_of(a));
         sums = l.take(2 * rows.splits * rows_of(a));
         go = l.take(emu::attn_rows_partial(a, rows));
@@ -150,7 +168,7 @@ emu_status_t emu_cross_attention_workspace(const emu_attention_t* in, size_t* by
     const emu_status_t st = args_of(in, a);
     if (st != EMU_STATUS_SUCCESS) return st;
     if (bytes == nullptr) return EMU_STATUS_INVALID_VALUE;
-    *bytes = has_rows(a) ? round256(emu::attn_forward_partial(a, emu::attn_rows_plan(a, 0)) * sizeof(float)) : 0;
+    *bytes = forward_bytes(a);
     return EMU_STATUS_SUCCESS;
 }
 
@@ -163,11 +181,10 @@ emu_status_t emu_cross_attention(const emu_attention_t* in, emu_heads_t q, emu_h
     if (has_rows(a) && (q.data == nullptr || out == nullptr)) return EMU_STATUS_INVALID_VALUE;
     if (has_keys(a) && (k.data == nullptr || v.data == nullptr)) return EMU_STATUS_INVALID_VALUE;
     if (!has_rows(a)) return EMU_STATUS_SUCCESS;
-    const AttnPlan p = emu::attn_rows_plan(a, 0);
-    if (bad_workspace(workspace, workspace_bytes, round256(emu::attn_forward_partial(a, p) * sizeof(float))))
-        return EMU_STATUS_INVALID_VALUE;
+    if (bad_workspace(workspace, workspace_bytes, forward_bytes(a))) return EMU_STATUS_INVALID_VALUE;
     if (!on_gfx950()) return EMU_STATUS_NOT_SUPPORTED;
-    return from_hip(emu::launch_attn_forward(a, p, q, k, v, out, stats, static_cast<float*>(workspace), stream_of(stream)));
+    if (emu::attn_whole(a, 0)) return from_hip(emu::launch_whole_forward(a, q, k, v, out, stats, stream_of(stream)));
+    return from_hip(emu::launch_attn_forward(a, emu::attn_rows_plan(a, 0), q, k, v, out, stats, static_cast<float*>(workspace), stream_of(stream)));
 }
 
 emu_status_t emu_cross_attention_backward_workspace(const emu_attention_t* in, size_t* bytes)
@@ -199,6 +216,8 @@ emu_status_t emu_cross_attention_backward(const emu_attention_t* in, emu_heads_t
     const hipStream_t s = stream_of(stream);
     if (!rows) return zero_keys(a, dk, dv, dbias, s);
     const BackwardSpace w(a, workspace);
+    if (emu::attn_whole(a, 1))
+        return from_hip(emu::launch_whole_backward(a, dout, q, k, v, stats, dq, dk, dv, dbias, w.db, s));
     hipError_t e = emu::launch_attn_backward_rows(a, w.rows, dout, q, k, v, out, stats, w.delta, dq, w.dq, s);
     if (e == hipSuccess && keys_wanted)
         e = emu::launch_attn_backward_keys(a, w.keys, dout, q, k, v, stats, w.delta, dk, dv, dbias, w.dk, w.dv, w.db, s);
@@ -238,6 +257,7 @@ emu_status_t emu_cross_attention_backward2(const emu_attention_t* in, emu_heads_
     if (!rows) return zero_keys(a, gk, gv, gbias, s);
     const SecondSpace w(a, workspace);
     const emu::AttnSeconds x{vq, vk, vv, vbias, vbias_batch, vbias_key, dout, q, k, v, out, stats};
+    if (emu::attn_whole(a, 2)) return from_hip(emu::launch_whole_second(a, x, gdout, gq, gk, gv, gbias, w.gb, s));
     hipError_t e = emu::launch_attn_second_sums(a, w.rows, x, w.delta, w.sums, s);
     if (e == hipSuccess && rows_wanted)
         e = emu::launch_attn_second_rows(a, w.rows, x, w.delta, w.sums, gdout, gq, w.go, w.gq, s);

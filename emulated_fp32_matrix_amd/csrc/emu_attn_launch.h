@@ -78,6 +78,21 @@ hipError_t launch_attn_second_keys(const AttnArgs& a, const AttnPlan& p, const A
                                    const float* sums, int sum_splits, float* gk, float* gv, float* gbias,
                                    float* partial_k, float* partial_v, float* partial_b, hipStream_t s);
 
+// Short sequences, each direction in one launch: whether a call's are (order
+// as above), and the launches.  partial: floats of attn_whole_partial().
+bool attn_whole(const AttnArgs& a, int order);
+inline size_t attn_whole_partial(const AttnArgs& a)
+{
+    return a.kv_heads > 1 ? (size_t)a.batch * a.keys * a.kv_heads : 0;
+}
+hipError_t launch_whole_forward(const AttnArgs& a, emu_heads_t q, emu_heads_t k, emu_heads_t v, float* out, float* stats,
+                                hipStream_t s);
+hipError_t launch_whole_backward(const AttnArgs& a, emu_heads_t dout, emu_heads_t q, emu_heads_t k, emu_heads_t v,
+                                 const float* stats, float* dq, float* dk, float* dv, float* dbias, float* partial,
+                                 hipStream_t s);
+hipError_t launch_whole_second(const AttnArgs& a, const AttnSeconds& x, float* gdout, float* gq, float* gk, float* gv,
+                               float* gbias, float* partial, hipStream_t s);
+
 // out[o][i] = sum over s of in[o][s][i], s in order; outer x inner results.
 hipError_t launch_attn_join(int64_t outer, int64_t splits, int64_t inner, const float* in, float* out, hipStream_t s);
 

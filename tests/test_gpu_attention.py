@@ -86,6 +86,18 @@ SHAPES = [
     (1, 700, 24, 2, 1, 48, "bias"),
     (1, 1500, 2, 2, 2, 128, "mask"),
     (1, 513, 515, 1, 1, 20, "bias mask lengths"),
+    # at the edges of the one-launch kernels of short sequences (48 rows and keys, 32 of wide heads' second order)
+    (3, 16, 16, 2, 2, 64, "bias"),
+    (2, 15, 17, 3, 1, 40, "bias lengths"),
+    (3, 48, 47, 2, 2, 32, "bias"),
+    (2, 12, 48, 8, 2, 16, "bias mask"),
+    (2, 32, 32, 2, 2, 64, "bias lengths"),
+    (2, 33, 48, 2, 2, 64, "mask"),
+    (2, 47, 1, 2, 1, 32, "bias"),
+    (2, 1, 48, 4, 4, 50, "lengths"),
+    (2, 49, 48, 1, 1, 32, "bias"),
+    (2, 48, 49, 1, 1, 32, "bias"),
+    (2, 48, 48, 1, 1, 65, "bias"),
 ]
 
 
