@@ -226,7 +226,7 @@ __global__ __launch_bounds__(256) void forward_kernel(AttnArgs a, emu_heads_t q,
 }
 
 template <int ND, int NT>
-__global__ __launch_bounds__(256) void backward_kernel(AttnArgs a, emu_heads_t dout, emu_heads_t q, emu_heads_t k,
+__global__ __launch_bounds__(256, NT < 3 && ND * NT <= 4 ? 3 : ND * NT <= 8 ? 2 : 1) void backward_kernel(AttnArgs a, emu_heads_t dout, emu_heads_t q, emu_heads_t k,
                                                        emu_heads_t v, const float* stats, float* dq, float* dk,
                                                        float* dv, float* db)
 {
@@ -284,7 +284,7 @@ __global__ __launch_bounds__(256) void backward_kernel(AttnArgs a, emu_heads_t d
 }
 
 template <int ND, int NT>
-__global__ __launch_bounds__(256) void second_kernel(AttnArgs a, AttnSeconds x, float* go, float* gq, float* gk, float* gv,
+__global__ __launch_bounds__(256, NT < 3 && ND * NT <= 4 ? 2 : 1) void second_kernel(AttnArgs a, AttnSeconds x, float* go, float* gq, float* gk, float* gv,
                                                      float* gb)
 {
     using W = Whole<ND, NT>;
