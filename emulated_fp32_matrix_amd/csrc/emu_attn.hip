@@ -2,17 +2,18 @@
 //
 // One pass over the keys with the running maximum and sum of the softmax: a
 // wave keeps 16 or 32 rows, their queries in registers as the B operand and
-// their results as accumulators, both with the row across the lanes, so that
-// the softmax's maxima and factors are per lane and a score's registers are
-// the next product's operand (emu_attn_device.h).  A team's tile of keys and
-// values goes through LDS once for all of its rows.
+// their results as accumulators (emu_attn_device.h), on split operands
+// (emu_attn_split.h). A team's tile of keys and values is split once, on its
+// way to LDS, for all of its rows.
 //
 // Few rows are cut along the keys: each range leaves a maximum, a sum and an
 // unscaled result, and a second launch joins them in order.
-#include "emu_attn_device.h"
+#include "emu_attn_split.h"
 
 namespace emu {
 namespace {
+
+constexpr int kMostSplits = 64;
 
 // Partial results of a split: rows' results, then their maxima and sums.
 struct ForwardPartial {
@@ -26,66 +27,67 @@ __host__ __device__ __forceinline__ ForwardPartial forward_partial(const AttnArg
 }
 
 template <int ND, int W, int NQ>
-__global__ __launch_bounds__(256) void forward_kernel(AttnArgs a, AttnPlan plan, emu_heads_t q, emu_heads_t k,
-                                                      emu_heads_t v, float* out, float* stats, float* partial)
+__global__ __launch_bounds__(64 * W) void forward_kernel(AttnArgs a, AttnPlan plan, emu_heads_t q, emu_heads_t k,
+                                                         emu_heads_t v, float* out, float* stats, float* partial)
 {
     using T = Team<W>;
-    constexpr int LD = Head<ND>::LD, KT = StreamTile<ND, W>::kRows, NK = KT / 16;
-    __shared__ __attribute__((aligned(16))) float lds[T::kTeams][2 * KT * LD + KT];
-    float* const tk = lds[T::index()];
-    float* const tv = tk + KT * LD;
-    float* const term = tv + KT * LD;
+    using S = Stream<ND, W, 2, 1>;
+    __shared__ __attribute__((aligned(16))) char lds[S::kBuffers * S::kBytes];
+    S stream{lds};
     const int lane = threadIdx.x & 63, m = lane & 15, h = lane >> 4;
 
-    each_piece<W>((int64_t)a.batch * a.kv_heads * plan.own * plan.splits, [&](int64_t piece) {
+    T::each_piece((int64_t)a.batch * a.kv_heads * plan.own * plan.splits, [&](int64_t piece) {
         const Piece at = piece_of(a, plan, piece);
         const int limit = keys_of(a, at.b);
         int64_t lo, hi;
-        range_of(limit, KT, plan.splits, at.split, lo, hi);
+        range_of(limit, kStreamRows, plan.splits, at.split, lo, hi);
 
-        f32x4_t own[NQ][ND], acc[NQ][ND];
+        Split8 own[NQ][Heads<ND>::KS];
+        f32x4_t acc[NQ][ND];
         float most[NQ], sum[NQ];
         const int64_t r0 = (at.own * W + T::wave()) * (16 * NQ) + m;
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
             const int64_t r = r0 + 16 * n;
             const bool valid = r < a.rows;
-            load_own(own[n], row_ptr(q, at.b, row_at(a, at.g, valid ? r : 0)), valid, h, a.dim);
+            load_own<ND>(own[n], row_ptr(q, at.b, row_at(a, at.g, valid ? r : 0)), valid, h, a.dim);
             most[n] = minus_inf();
             sum[n] = 0.0f;
         }
         clear(acc);
 
-        for (int64_t k0 = lo; k0 < hi; k0 += KT) {
-            {
-                Tile<ND, KT, T::kThreads> fk, fv;
-                const auto takes_part = [&](int row) { return key_term(a, at.b, (int)k0 + row, limit) != minus_inf(); };
-                fk.fetch(T::thread(), a.dim, [&](int row) { return takes_part(row) ? key_ptr(k, at.b, at.g, k0 + row) : nullptr; });
-                fv.fetch(T::thread(), a.dim, [&](int row) { return takes_part(row) ? key_ptr(v, at.b, at.g, k0 + row) : nullptr; });
-                T::sync();   // the previous tile has been read
-                fk.put(T::thread(), tk);
-                fv.put(T::thread(), tv);
-                if (T::thread() < KT) term[T::thread()] = key_term(a, at.b, (int)k0 + T::thread(), limit);
-                T::sync();
-            }
-            f32x4_t s[NK][NQ];
+        const auto where = [&](int64_t first, int i, int row) {
+            return key_term(a, at.b, (int)first + row, limit) != minus_inf() ? key_ptr(i == 0 ? k : v, at.b, at.g, first + row)
+                                                                             : nullptr;
+        };
+        const auto number = [&](int64_t first, float* to) { to[0] = key_term(a, at.b, (int)first + T::thread(), limit); };
+        stream.run(lo, hi, a.dim, where, number, [&](int64_t, const uint16_t* arrays, const float* numbers) {
+            const Terms term(numbers, h);
+            f32x4_t s[2][NQ];
 #pragma unroll
-            for (int t = 0; t < NK; ++t) {
+            for (int t = 0; t < 2; ++t) {
 #pragma unroll
                 for (int n = 0; n < NQ; ++n) s[t][n] = f32x4_t{};
-                scores<ND, NQ>(tk + 16 * t * LD, m, h, own, s[t]);
-                const f32x4_t add = *reinterpret_cast<const f32x4_t*>(term + 16 * t + 4 * h);
+                scores<ND, S::kPiece, NQ>(arrays + 16 * t * S::RS, m, h, own, s[t]);
 #pragma unroll
                 for (int n = 0; n < NQ; ++n)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        s[t][n][j] = add[j] == minus_inf() ? minus_inf() : __builtin_fmaf(s[t][n][j], a.scale, add[j]);
+                    for (int j = 0; j < 4; ++j) s[t][n][j] = __builtin_fmaf(s[t][n][j], a.scale, term.of[t][j]);
             }
+            if (term.some) {
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) s[t][n][j] = term.dead(t, j) ? minus_inf() : s[t][n][j];
+            }
+            Split8 w[NQ];
 #pragma unroll
             for (int n = 0; n < NQ; ++n) {
                 float top = s[0][n][0];
 #pragma unroll
-                for (int t = 0; t < NK; ++t)
+                for (int t = 0; t < 2; ++t)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) top = __builtin_fmaxf(top, s[t][n][j]);
                 const float next = __builtin_fmaxf(most[n], column_max(top));
@@ -94,7 +96,7 @@ __global__ __launch_bounds__(256) void forward_kernel(AttnArgs a, AttnPlan plan,
                 most[n] = next;
                 float here = 0.0f;
 #pragma unroll
-                for (int t = 0; t < NK; ++t)
+                for (int t = 0; t < 2; ++t)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         s[t][n][j] = exp_of(s[t][n][j] - safe);
@@ -103,10 +105,10 @@ __global__ __launch_bounds__(256) void forward_kernel(AttnArgs a, AttnPlan plan,
                 sum[n] = __builtin_fmaf(sum[n], old, here);
 #pragma unroll
                 for (int t = 0; t < ND; ++t) acc[n][t] = acc[n][t] * old;
+                w[n] = split8(s[0][n], s[1][n]);
             }
-#pragma unroll
-            for (int t = 0; t < NK; ++t) results<ND, NQ>(tv + 16 * t * LD, m, h, s[t], acc);
-        }
+            results<ND, S::kPiece, NQ>(arrays + S::kArray, m, h, w, acc);
+        });
 
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
@@ -134,29 +136,44 @@ __global__ __launch_bounds__(256) void forward_kernel(AttnArgs a, AttnPlan plan,
     });
 }
 
-// The ranges' results of a row, joined: one wave per row.
+// The ranges' results of a row, joined in order: a workgroup per row, COLS
+// columns of it by 256 / COLS groups of ranges.
+template <int COLS>
 __global__ __launch_bounds__(256) void join_forward_kernel(AttnArgs a, AttnPlan plan, float* partial, float* out,
                                                            float* stats)
 {
+    constexpr int GROUPS = 256 / COLS;
+    __shared__ float parts[GROUPS][COLS];
+    static_assert(kMostSplits == 64, "a lane per range");
     const int64_t rows = (int64_t)a.batch * a.queries * a.heads;
     const ForwardPartial from = forward_partial(a, plan, partial);
-    const int lane = threadIdx.x & 63;
-    for (int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); row < rows; row += (int64_t)gridDim.x * 4) {
-        float most = minus_inf();
-        for (int s = 0; s < plan.splits; ++s) most = __builtin_fmaxf(most, from.ml[2 * (s * rows + row)]);
+    const int lane = threadIdx.x & 63, col = threadIdx.x % COLS, group = threadIdx.x / COLS;
+    for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+        const bool there = lane < plan.splits;
+        const float2 ml = there ? *reinterpret_cast<const float2*>(from.ml + 2 * (lane * rows + row)) : float2{minus_inf(), 0.0f};
+        float most = ml.x;
+#pragma unroll
+        for (int i = 1; i < 64; i *= 2) most = __builtin_fmaxf(most, __shfl_xor(most, i, 64));
         const float safe = most == minus_inf() ? 0.0f : most;
-        float sum = 0.0f, lo = 0.0f, hi = 0.0f;
-        for (int s = 0; s < plan.splits; ++s) {
-            const int64_t i = s * rows + row;
-            const float f = exp_of(from.ml[2 * i] - safe);
-            sum = __builtin_fmaf(from.ml[2 * i + 1], f, sum);
-            if (lane < a.dim) lo = __builtin_fmaf(from.o[i * a.dim + lane], f, lo);
-            if (lane + 64 < a.dim) hi = __builtin_fmaf(from.o[i * a.dim + lane + 64], f, hi);
-        }
+        const float f = there ? exp_of(ml.x - safe) : 0.0f;
+        const float sum = lane_sum<64>(ml.y * f);
         const float over = sum == 0.0f ? 0.0f : 1.0f / sum;
-        if (lane < a.dim) out[row * a.dim + lane] = lo * over;
-        if (lane + 64 < a.dim) out[row * a.dim + lane + 64] = hi * over;
-        if (stats != nullptr && lane == 0) {
+        float acc = 0.0f;
+        for (int s0 = 0; s0 < plan.splits; s0 += GROUPS) {   // (all lanes stay for the exchange)
+            const int s = s0 + group;
+            const float fs = __shfl(f, s & 63, 64);
+            if (s < plan.splits && col < a.dim) acc = __builtin_fmaf(from.o[(s * rows + row) * a.dim + col], fs, acc);
+        }
+        __syncthreads();   // the previous row's have been read
+        parts[group][col] = acc;
+        __syncthreads();
+        if (threadIdx.x < COLS && col < a.dim) {
+            float all = parts[0][col];
+#pragma unroll
+            for (int i = 1; i < GROUPS; ++i) all = all + parts[i][col];
+            out[row * a.dim + col] = all * over;
+        }
+        if (stats != nullptr && threadIdx.x == 0) {
             stats[2 * row] = safe;
             stats[2 * row + 1] = over;
         }
@@ -183,7 +200,7 @@ int splits_for(int64_t waves, int64_t other, int64_t least)
     int64_t s = waves > 0 ? 2048 / waves : 1;
     const int64_t most = other / least;
     if (s > most) s = most;
-    if (s > 64) s = 64;
+    if (s > kMostSplits) s = kMostSplits;
     return s < 1 ? 1 : (int)s;
 }
 
@@ -227,11 +244,17 @@ hipError_t launch_attn_forward(const AttnArgs& a, const AttnPlan& p, emu_heads_t
 {
     with_shape<2>(a.dim, p, [&]<int ND, int W, int NQ>() {
         const int64_t n = (int64_t)a.batch * a.kv_heads * p.own * p.splits;
-        forward_kernel<ND, W, NQ><<<attn_grid<W>(n), 256, 0, s>>>(a, p, q, k, v, out, stats, partial);
+        forward_kernel<ND, W, NQ><<<Team<W>::grid(n), 64 * W, 0, s>>>(a, p, q, k, v, out, stats, partial);
     });
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1) return e;
-    join_forward_kernel<<<join_grid(((int64_t)a.batch * a.queries * a.heads + 3) / 4), 256, 0, s>>>(a, p, partial, out, stats);
+    const unsigned grid = join_grid((int64_t)a.batch * a.queries * a.heads);
+    if (a.dim <= 32)
+        join_forward_kernel<32><<<grid, 256, 0, s>>>(a, p, partial, out, stats);
+    else if (a.dim <= 64)
+        join_forward_kernel<64><<<grid, 256, 0, s>>>(a, p, partial, out, stats);
+    else
+        join_forward_kernel<128><<<grid, 256, 0, s>>>(a, p, partial, out, stats);
     return hipGetLastError();
 }
 

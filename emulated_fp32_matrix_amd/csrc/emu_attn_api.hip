@@ -54,6 +54,8 @@ emu_status_t args_of(const emu_attention_t* in, AttnArgs& a)
     a.share = in->heads > 0 ? in->heads / in->kv_heads : 0;
     a.dim = in->dim;
     a.rows = in->queries * a.share;
+    // (r times the inverse's excess, below share, has to stay below 2^32)
+    if (a.share > 1 && a.rows <= ((int64_t)1 << 32) / a.share) a.share_inverse = (uint32_t)((((uint64_t)1 << 32) + a.share - 1) / a.share);
     a.scale = in->scale;
     a.bias = in->key_bias;
     a.bias_b = in->key_bias_batch;

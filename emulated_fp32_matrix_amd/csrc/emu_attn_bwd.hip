@@ -6,31 +6,30 @@
 // through LDS; it leaves dq, and delta = dout . out for the other), and one
 // over the keys (keys and values stay, queries and output gradients stream;
 // dk, dv and the bias gradient).  Layouts as in the forward pass.
-#include "emu_attn_device.h"
+#include "emu_attn_split.h"
 
 namespace emu {
 namespace {
 
 template <int ND, int W, int NQ>
-__global__ __launch_bounds__(256) void rows_kernel(AttnArgs a, AttnPlan plan, emu_heads_t dout, emu_heads_t q,
-                                                   emu_heads_t k, emu_heads_t v, const float* out, const float* stats,
-                                                   float* delta, float* dq, float* partial)
+__global__ __launch_bounds__(64 * W) void rows_kernel(AttnArgs a, AttnPlan plan, emu_heads_t dout, emu_heads_t q,
+                                                      emu_heads_t k, emu_heads_t v, const float* out, const float* stats,
+                                                      float* delta, float* dq, float* partial)
 {
     using T = Team<W>;
-    constexpr int LD = Head<ND>::LD, KT = StreamTile<ND, W>::kRows, NK = KT / 16;
-    __shared__ __attribute__((aligned(16))) float lds[T::kTeams][2 * KT * LD + KT];
-    float* const tk = lds[T::index()];
-    float* const tv = tk + KT * LD;
-    float* const term = tv + KT * LD;
+    using S = Stream<ND, W, 2, 1>;
+    __shared__ __attribute__((aligned(16))) char lds[S::kBuffers * S::kBytes];
+    S stream{lds};
     const int lane = threadIdx.x & 63, m = lane & 15, h = lane >> 4;
 
-    each_piece<W>((int64_t)a.batch * a.kv_heads * plan.own * plan.splits, [&](int64_t piece) {
+    T::each_piece((int64_t)a.batch * a.kv_heads * plan.own * plan.splits, [&](int64_t piece) {
         const Piece at = piece_of(a, plan, piece);
         const int limit = keys_of(a, at.b);
         int64_t lo, hi;
-        range_of(limit, KT, plan.splits, at.split, lo, hi);
+        range_of(limit, kStreamRows, plan.splits, at.split, lo, hi);
 
-        f32x4_t oq[NQ][ND], od[NQ][ND], acc[NQ][ND];
+        Split8 oq[NQ][Heads<ND>::KS], od[NQ][Heads<ND>::KS];
+        f32x4_t acc[NQ][ND];
         float top[NQ], over[NQ], del[NQ];
         const int64_t r0 = (at.own * W + T::wave()) * (16 * NQ) + m;
 #pragma unroll
@@ -39,52 +38,51 @@ __global__ __launch_bounds__(256) void rows_kernel(AttnArgs a, AttnPlan plan, em
             const bool valid = r < a.rows;
             const RowAt ra = row_at(a, at.g, valid ? r : 0);
             const int64_t row = row_index(a, at.b, ra);
-            load_own(oq[n], row_ptr(q, at.b, ra), valid, h, a.dim);
-            load_own(od[n], row_ptr(dout, at.b, ra), valid, h, a.dim);
-            float d = 0.0f;
-#pragma unroll
-            for (int c = 0; c < ND; ++c) {
-                const f32x4_t o = load4(out + row * a.dim, 16 * c + 4 * h, a.dim);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) d = __builtin_fmaf(od[n][c][e], o[e], d);
-            }
-            del[n] = column_sum(d);
+            load_own<ND>(oq[n], row_ptr(q, at.b, ra), valid, h, a.dim);
+            load_own<ND>(od[n], row_ptr(dout, at.b, ra), valid, h, a.dim);
+            del[n] = row_dot<ND>(row_ptr(dout, at.b, ra), out + row * a.dim, h, a.dim);
             top[n] = stats[2 * row];
             over[n] = stats[2 * row + 1];
             if (valid && h == 0 && at.split == 0) delta[row] = del[n];
         }
         clear(acc);
 
-        for (int64_t k0 = lo; k0 < hi && dq != nullptr; k0 += KT) {
-            {
-                Tile<ND, KT, T::kThreads> fk, fv;
-                const auto takes_part = [&](int row) { return key_term(a, at.b, (int)k0 + row, limit) != minus_inf(); };
-                fk.fetch(T::thread(), a.dim, [&](int row) { return takes_part(row) ? key_ptr(k, at.b, at.g, k0 + row) : nullptr; });
-                fv.fetch(T::thread(), a.dim, [&](int row) { return takes_part(row) ? key_ptr(v, at.b, at.g, k0 + row) : nullptr; });
-                T::sync();
-                fk.put(T::thread(), tk);
-                fv.put(T::thread(), tv);
-                if (T::thread() < KT) term[T::thread()] = key_term(a, at.b, (int)k0 + T::thread(), limit);
-                T::sync();
-            }
+        const auto where = [&](int64_t first, int i, int row) {
+            return key_term(a, at.b, (int)first + row, limit) != minus_inf() ? key_ptr(i == 0 ? k : v, at.b, at.g, first + row)
+                                                                             : nullptr;
+        };
+        const auto number = [&](int64_t first, float* to) { to[0] = key_term(a, at.b, (int)first + T::thread(), limit); };
+        stream.run(lo, dq != nullptr ? hi : lo, a.dim, where, number,
+                   [&](int64_t, const uint16_t* arrays, const float* numbers) {
+            const Terms term(numbers, h);
+            f32x4_t s[2][NQ], dp[2][NQ];
 #pragma unroll
-            for (int t = 0; t < NK; ++t) {
-                f32x4_t s[NQ], dp[NQ];
+            for (int t = 0; t < 2; ++t) {
 #pragma unroll
-                for (int n = 0; n < NQ; ++n) s[n] = dp[n] = f32x4_t{};
-                scores<ND, NQ>(tk + 16 * t * LD, m, h, oq, s);
-                scores<ND, NQ>(tv + 16 * t * LD, m, h, od, dp);
-                const f32x4_t add = *reinterpret_cast<const f32x4_t*>(term + 16 * t + 4 * h);
+                for (int n = 0; n < NQ; ++n) s[t][n] = dp[t][n] = f32x4_t{};
+                scores<ND, S::kPiece, NQ>(arrays + 16 * t * S::RS, m, h, oq, s[t]);
+                scores<ND, S::kPiece, NQ>(arrays + S::kArray + 16 * t * S::RS, m, h, od, dp[t]);
 #pragma unroll
                 for (int n = 0; n < NQ; ++n)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const float p = exp_of(__builtin_fmaf(s[n][j], a.scale, add[j]) - top[n]) * over[n];
-                        s[n][j] = add[j] == minus_inf() ? 0.0f : p * (dp[n][j] - del[n]);
+                        const float p = exp_of(__builtin_fmaf(s[t][n][j], a.scale, term.of[t][j]) - top[n]) * over[n];
+                        s[t][n][j] = p * (dp[t][n][j] - del[n]);
                     }
-                results<ND, NQ>(tk + 16 * t * LD, m, h, s, acc);
             }
-        }
+            if (term.some) {
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) s[t][n][j] = term.dead(t, j) ? 0.0f : s[t][n][j];
+            }
+            Split8 w[NQ];
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) w[n] = split8(s[0][n], s[1][n]);
+            results<ND, S::kPiece, NQ>(arrays, m, h, w, acc);
+        });
 
         if (dq == nullptr) return;
 #pragma unroll
@@ -99,25 +97,24 @@ __global__ __launch_bounds__(256) void rows_kernel(AttnArgs a, AttnPlan plan, em
 }
 
 template <int ND, int W, int NT>
-__global__ __launch_bounds__(256) void keys_kernel(AttnArgs a, AttnPlan plan, emu_heads_t dout, emu_heads_t q,
-                                                   emu_heads_t k, emu_heads_t v, const float* stats,
-                                                   const float* delta, float* dk, float* dv, float* db)
+__global__ __launch_bounds__(64 * W) void keys_kernel(AttnArgs a, AttnPlan plan, emu_heads_t dout, emu_heads_t q,
+                                                      emu_heads_t k, emu_heads_t v, const float* stats,
+                                                      const float* delta, float* dk, float* dv, float* db)
 {
     using T = Team<W>;
-    constexpr int LD = Head<ND>::LD, RT = StreamTile<ND, W>::kRows, NR = RT / 16;
-    __shared__ __attribute__((aligned(16))) float lds[T::kTeams][2 * RT * LD + 3 * RT];
-    float* const tq = lds[T::index()];
-    float* const td = tq + RT * LD;
-    float* const row_stats = td + RT * LD;   // maxima, 1 / sums, deltas
+    using S = Stream<ND, W, 2, 3>;
+    __shared__ __attribute__((aligned(16))) char lds[S::kBuffers * S::kBytes];
+    S stream{lds};
     const int lane = threadIdx.x & 63, m = lane & 15, h = lane >> 4;
 
-    each_piece<W>((int64_t)a.batch * a.kv_heads * plan.own * plan.splits, [&](int64_t piece) {
+    T::each_piece((int64_t)a.batch * a.kv_heads * plan.own * plan.splits, [&](int64_t piece) {
         const Piece at = piece_of(a, plan, piece);
         const int limit = keys_of(a, at.b);
         int64_t lo, hi;
-        range_of(a.rows, RT, plan.splits, at.split, lo, hi);
+        range_of(a.rows, kStreamRows, plan.splits, at.split, lo, hi);
 
-        f32x4_t ok[NT][ND], ov[NT][ND], ak[NT][ND], av[NT][ND];
+        Split8 ok[NT][Heads<ND>::KS], ov[NT][Heads<ND>::KS];
+        f32x4_t ak[NT][ND], av[NT][ND];
         float add[NT], bias[NT];
         const int64_t j0 = (at.own * W + T::wave()) * (16 * NT) + m;
 #pragma unroll
@@ -125,8 +122,8 @@ __global__ __launch_bounds__(256) void keys_kernel(AttnArgs a, AttnPlan plan, em
             const int64_t j = j0 + 16 * n;
             add[n] = j < a.keys ? key_term(a, at.b, (int)j, limit) : minus_inf();
             const bool valid = add[n] != minus_inf();
-            load_own(ok[n], key_ptr(k, at.b, at.g, valid ? j : 0), valid, h, a.dim);
-            load_own(ov[n], key_ptr(v, at.b, at.g, valid ? j : 0), valid, h, a.dim);
+            load_own<ND>(ok[n], key_ptr(k, at.b, at.g, valid ? j : 0), valid, h, a.dim);
+            load_own<ND>(ov[n], key_ptr(v, at.b, at.g, valid ? j : 0), valid, h, a.dim);
             bias[n] = 0.0f;
         }
         clear(ak);
@@ -134,52 +131,47 @@ __global__ __launch_bounds__(256) void keys_kernel(AttnArgs a, AttnPlan plan, em
         // (a team whose keys all take no part has zeros to write)
         if (at.own * W * 16 * NT >= limit) hi = lo;
 
-        for (int64_t r = lo; r < hi; r += RT) {
-            {
-                Tile<ND, RT, T::kThreads> fq, fd;
-                fq.fetch(T::thread(), a.dim, [&](int row) {
-                    return r + row < hi ? row_ptr(q, at.b, row_at(a, at.g, r + row)) : nullptr;
-                });
-                fd.fetch(T::thread(), a.dim, [&](int row) {
-                    return r + row < hi ? row_ptr(dout, at.b, row_at(a, at.g, r + row)) : nullptr;
-                });
-                T::sync();
-                fq.put(T::thread(), tq);
-                fd.put(T::thread(), td);
-                if (T::thread() < RT) {
-                    const int i = T::thread();
-                    const bool valid = r + i < hi;
-                    const int64_t row = valid ? row_index(a, at.b, row_at(a, at.g, r + i)) : 0;
-                    row_stats[i] = valid ? stats[2 * row] : 0.0f;
-                    row_stats[RT + i] = valid ? stats[2 * row + 1] : 0.0f;   // (so that p = 0)
-                    row_stats[2 * RT + i] = valid ? delta[row] : 0.0f;
-                }
-                T::sync();
-            }
+        const auto where = [&](int64_t first, int i, int row) {
+            return first + row < hi ? row_ptr(i == 0 ? q : dout, at.b, row_at(a, at.g, first + row)) : nullptr;
+        };
+        // maxima, 1 / sums, deltas; behind the last row p = e^-inf 0
+        const auto number = [&](int64_t first, float* to) {
+            const bool valid = first + T::thread() < hi;
+            const int64_t row = valid ? row_index(a, at.b, row_at(a, at.g, first + T::thread())) : 0;
+            to[0] = valid ? stats[2 * row] : __builtin_inff();
+            to[1] = valid ? stats[2 * row + 1] : 0.0f;
+            to[2] = valid ? delta[row] : 0.0f;
+        };
+        stream.run(lo, hi, a.dim, where, number, [&](int64_t, const uint16_t* arrays, const float* numbers) {
+            f32x4_t s[2][NT], dp[2][NT];
 #pragma unroll
-            for (int t = 0; t < NR; ++t) {
-                f32x4_t s[NT], dp[NT];
+            for (int t = 0; t < 2; ++t) {
 #pragma unroll
-                for (int n = 0; n < NT; ++n) s[n] = dp[n] = f32x4_t{};
-                scores<ND, NT>(tq + 16 * t * LD, m, h, ok, s);
-                scores<ND, NT>(td + 16 * t * LD, m, h, ov, dp);
-                const f32x4_t top = *reinterpret_cast<const f32x4_t*>(row_stats + 16 * t + 4 * h);
-                const f32x4_t over = *reinterpret_cast<const f32x4_t*>(row_stats + RT + 16 * t + 4 * h);
-                const f32x4_t del = *reinterpret_cast<const f32x4_t*>(row_stats + 2 * RT + 16 * t + 4 * h);
+                for (int n = 0; n < NT; ++n) s[t][n] = dp[t][n] = f32x4_t{};
+                scores<ND, S::kPiece, NT>(arrays + 16 * t * S::RS, m, h, ok, s[t]);
+                scores<ND, S::kPiece, NT>(arrays + S::kArray + 16 * t * S::RS, m, h, ov, dp[t]);
+                const float* const row = numbers + 16 * t + 4 * h;
+                const f32x4_t top = *reinterpret_cast<const f32x4_t*>(row);
+                const f32x4_t over = *reinterpret_cast<const f32x4_t*>(row + kStreamRows);
+                const f32x4_t del = *reinterpret_cast<const f32x4_t*>(row + 2 * kStreamRows);
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const bool dead = add[n] == minus_inf() || r + 16 * t + 4 * h + j >= hi;
-                        const float p = exp_of(__builtin_fmaf(s[n][j], a.scale, add[n]) - top[j]) * over[j];
-                        s[n][j] = dead ? 0.0f : p;
-                        dp[n][j] = dead ? 0.0f : p * (dp[n][j] - del[j]);
-                        bias[n] = bias[n] + dp[n][j];
+                        // (a key that takes no part has e^-inf; what NaN in a row leaves there is dropped at the end)
+                        s[t][n][j] = exp_of(__builtin_fmaf(s[t][n][j], a.scale, add[n]) - top[j]) * over[j];
+                        dp[t][n][j] = s[t][n][j] * (dp[t][n][j] - del[j]);
+                        bias[n] = bias[n] + dp[t][n][j];
                     }
-                results<ND, NT>(td + 16 * t * LD, m, h, s, av);
-                results<ND, NT>(tq + 16 * t * LD, m, h, dp, ak);
             }
-        }
+            Split8 w[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) w[n] = split8(s[0][n], s[1][n]);
+            results<ND, S::kPiece, NT>(arrays + S::kArray, m, h, w, av);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) w[n] = split8(dp[0][n], dp[1][n]);
+            results<ND, S::kPiece, NT>(arrays, m, h, w, ak);
+        });
 
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -191,8 +183,7 @@ __global__ __launch_bounds__(256) void keys_kernel(AttnArgs a, AttnPlan plan, em
 #pragma unroll
                 for (int t = 0; t < ND; ++t) ak[n][t] = av[n][t] = f32x4_t{};
             }
-            int64_t to = key_index(a, at.b, at.g, j);
-            to += at.split * ((int64_t)a.batch * a.keys * a.kv_heads);
+            const int64_t to = key_index(a, at.b, at.g, j) + at.split * ((int64_t)a.batch * a.keys * a.kv_heads);
             if (dk != nullptr) store_own(ak[n], a.scale, dk + to * a.dim, h, a.dim);
             if (dv != nullptr) store_own(av[n], 1.0f, dv + to * a.dim, h, a.dim);
             // (bias partials: [batch][split][key head][key], joined over the middle two)
@@ -210,7 +201,7 @@ hipError_t launch_attn_backward_rows(const AttnArgs& a, const AttnPlan& p, emu_h
 {
     with_shape<2>(a.dim, p, [&]<int ND, int W, int NQ>() {
         const int64_t n = (int64_t)a.batch * a.kv_heads * p.own * p.splits;
-        rows_kernel<ND, W, NQ><<<attn_grid<W>(n), 256, 0, s>>>(a, p, dout, q, k, v, out, stats, delta, dq, partial);
+        rows_kernel<ND, W, NQ><<<Team<W>::grid(n), 64 * W, 0, s>>>(a, p, dout, q, k, v, out, stats, delta, dq, partial);
     });
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && p.splits > 1 && dq != nullptr)
@@ -229,7 +220,7 @@ hipError_t launch_attn_backward_keys(const AttnArgs& a, const AttnPlan& p, emu_h
     float* const to_b = join_bias ? partial_b : dbias;
     with_shape<1>(a.dim, p, [&]<int ND, int W, int NT>() {
         const int64_t n = (int64_t)a.batch * a.kv_heads * p.own * p.splits;
-        keys_kernel<ND, W, NT><<<attn_grid<W>(n), 256, 0, s>>>(a, p, dout, q, k, v, stats, delta, to_k, to_v, to_b);
+        keys_kernel<ND, W, NT><<<Team<W>::grid(n), 64 * W, 0, s>>>(a, p, dout, q, k, v, stats, delta, to_k, to_v, to_b);
     });
     hipError_t e = hipGetLastError();
     const int64_t n = (int64_t)a.batch * a.keys * a.kv_heads * a.dim;

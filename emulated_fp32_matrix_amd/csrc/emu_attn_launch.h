@@ -15,6 +15,7 @@ namespace emu {
 struct AttnArgs {
     int batch, queries, keys, heads, kv_heads, share, dim;
     int64_t rows;            // queries * share
+    uint32_t share_inverse;  // ceil(2^32 / share) where r / share is the upper half of r times it, else 0
     float scale;
     const float* bias;       // key bias or null
     int64_t bias_b, bias_k;

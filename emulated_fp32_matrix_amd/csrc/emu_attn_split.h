@@ -1,0 +1,322 @@
+// Products of the attention kernels on split operands (gfx950 only).
+//
+// Each FP32 value is split into three BF16 pieces, hi = R(x), mid = R(x - hi),
+// lo = x - hi - mid (R: round to nearest even; exact for |x| from 2^-110, below
+// which the lowest pieces run out of BF16's subnormals), and a product is the
+// six products of pieces down to 2^-16 of it, accumulated in FP32 by
+// v_mfma_f32_16x16x32_bf16. What is left out is at most 2^-25 of |a b|, half
+// of FP32's own rounding. A value beyond BF16's largest finite number has hi =
+// that number; infinities give NaN.
+//
+// Why not the FP32 matrix instruction: it has 1/16 of the rate, 6/16 of it per
+// product, and it keeps its SIMD's vector unit from other waves' work
+// (measured on 4,096 keys by 2,048 rows of 64: matrix busy + vector active =
+// 0.96 with two waves a SIMD), where the softmax and the splits of one wave
+// run beside the BF16 products of another.
+//
+// Layouts: lane l has A[l % 16][8 (l / 16) + i] and B[8 (l / 16) + i][l % 16], i
+// = 0..7. Scores: i is d within the step. Results: i < 4 is streamed row 4 (l /
+// 16) + i of the first 16, i >= 4 row 4 (l / 16) + i - 4 of the second, which
+// a score's registers hold; A comes from the same row-major tile by the LDS's
+// transposing read.
+#pragma once
+
+#include "emu_attn_device.h"
+
+namespace emu {
+
+typedef short i16x4_t __attribute__((ext_vector_type(4)));
+
+// Four (eight) values' pieces.
+struct Split4 {
+    u32x2_t p[3];
+};
+struct Split8 {
+    bf16x8_t p[3];
+};
+
+template <bool LIMIT>
+__device__ __forceinline__ void split2(float x0, float x1, uint32_t& hi, uint32_t& mid, uint32_t& lo)
+{
+    hi = LIMIT ? pack_bf16x2(clamp_sat(x0), clamp_sat(x1)) : pack_bf16x2(x0, x1);
+    const float r0 = x0 - __uint_as_float(hi << 16), r1 = x1 - __uint_as_float(hi & 0xffff0000u);
+    mid = pack_bf16x2(r0, r1);
+    lo = pack_bf16x2(r0 - __uint_as_float(mid << 16), r1 - __uint_as_float(mid & 0xffff0000u));
+}
+
+__device__ __forceinline__ Split4 split4(f32x4_t v)
+{
+    uint32_t a[3], b[3];
+    split2<true>(v[0], v[1], a[0], a[1], a[2]);
+    split2<true>(v[2], v[3], b[0], b[1], b[2]);
+    Split4 s;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) s.p[i] = u32x2_t{a[i], b[i]};
+    return s;
+}
+
+// LIMIT: values may pass BF16's largest.
+template <bool LIMIT = false>
+__device__ __forceinline__ Split8 split8(f32x4_t u, f32x4_t v)
+{
+    uint32_t x[4][3];
+    split2<LIMIT>(u[0], u[1], x[0][0], x[0][1], x[0][2]);
+    split2<LIMIT>(u[2], u[3], x[1][0], x[1][1], x[1][2]);
+    split2<LIMIT>(v[0], v[1], x[2][0], x[2][1], x[2][2]);
+    split2<LIMIT>(v[2], v[3], x[3][0], x[3][1], x[3][2]);
+    Split8 s;
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+        s.p[i] = __builtin_bit_cast(bf16x8_t, u32x4_t{x[0][i], x[1][i], x[2][i], x[3][i]});
+    return s;
+}
+
+__device__ __forceinline__ f32x4_t mfma32(bf16x8_t a, bf16x8_t b, f32x4_t c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// acc[n] += a . b[n], the smallest products first.
+template <int NT>
+__device__ __forceinline__ void product6(const bf16x8_t (&a)[3], const Split8* const (&b)[NT], f32x4_t* const (&acc)[NT])
+{
+    constexpr int ia[6] = {2, 0, 1, 1, 0, 0}, ib[6] = {0, 2, 1, 0, 1, 0};
+#pragma unroll
+    for (int i = 0; i < 6; ++i)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) *acc[n] = mfma32(a[ia[i]], b[n]->p[ib[i]], *acc[n]);
+}
+
+// ND tiles of 16 cover a head; scores take KS steps of 32 of it. A tile in LDS
+// has [array][piece][row][RS]: RS is eight more than a multiple of 32, so that
+// the 16 rows of a score's reads lie on different banks.
+template <int ND>
+struct Heads {
+    static constexpr int KS = (ND + 1) / 2, RS = 32 * KS + 8;
+};
+
+// A wave's own row as the B operand of scores; not `valid`: zeros.
+template <int ND>
+__device__ __forceinline__ void load_own(Split8 (&f)[Heads<ND>::KS], const float* row, bool valid, int h, int dim)
+{
+#pragma unroll
+    for (int c = 0; c < Heads<ND>::KS; ++c)
+        f[c] = valid ? split8<true>(load4(row, 32 * c + 8 * h, dim), load4(row, 32 * c + 8 * h + 4, dim))
+                     : split8(f32x4_t{}, f32x4_t{});
+}
+
+// acc[n] += (the 16 streamed rows at `tile`) . own[n]; PS: elements of a piece
+template <int ND, int PS, int NT>
+__device__ __forceinline__ void scores(const uint16_t* tile, int m, int h, const Split8 (&own)[NT][Heads<ND>::KS],
+                                       f32x4_t (&acc)[NT])
+{
+    const uint16_t* const at = tile + m * Heads<ND>::RS + 8 * h;
+    f32x4_t* to[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) to[n] = &acc[n];
+#pragma unroll
+    for (int c = 0; c < Heads<ND>::KS; ++c) {
+        bf16x8_t a[3];
+        const Split8* b[NT];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) a[i] = *reinterpret_cast<const bf16x8_t*>(at + i * PS + 32 * c);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) b[n] = &own[n][c];
+        product6<NT>(a, b, to);
+    }
+}
+
+// acc[n] += (the 32 streamed rows at `tile`)^T . w[n]
+template <int ND, int PS, int NT>
+__device__ __forceinline__ void results(const uint16_t* tile, int m, int h, const Split8 (&w)[NT], f32x4_t (&acc)[NT][ND])
+{
+    typedef __attribute__((address_space(3))) i16x4_t lds_t;
+    constexpr int RS = Heads<ND>::RS;
+    const uint16_t* const at = tile + (4 * h + (m >> 2)) * RS + 4 * (m & 3);
+    const Split8* b[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) b[n] = &w[n];
+#pragma unroll
+    for (int t = 0; t < ND; ++t) {
+        bf16x8_t a[3];
+        f32x4_t* to[NT];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            const i16x4_t u = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t*)(at + i * PS + 16 * t));
+            const i16x4_t v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t*)(at + i * PS + 16 * RS + 16 * t));
+            a[i] = __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(u, v, 0, 1, 2, 3, 4, 5, 6, 7));
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) to[n] = &acc[n][t];
+        product6<NT>(a, b, to);
+    }
+}
+
+// A result's column to a row of `dim` floats, times f.
+template <int ND>
+__device__ __forceinline__ void store_own(const f32x4_t (&acc)[ND], float f, float* row, int h, int dim)
+{
+#pragma unroll
+    for (int t = 0; t < ND; ++t) store4(row, 16 * t + 4 * h, dim, acc[t] * f);
+}
+
+// A row's product with another, both in memory, in all of its lanes.
+template <int ND>
+__device__ __forceinline__ float row_dot(const float* x, const float* y, int h, int dim)
+{
+    float sum = 0.0f;
+#pragma unroll
+    for (int t = 0; t < ND; ++t) {
+        const f32x4_t u = load4(x, 16 * t + 4 * h, dim), v = load4(y, 16 * t + 4 * h, dim);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum = __builtin_fmaf(u[e], v[e], sum);
+    }
+    return column_sum(sum);
+}
+
+template <int ND, int NT>
+__device__ __forceinline__ void clear(f32x4_t (&acc)[NT][ND])
+{
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int t = 0; t < ND; ++t) acc[n][t] = f32x4_t{};
+}
+
+// ---- the streamed side ------------------------------------------------------------
+//
+// N arrays of rows and X numbers per row, 32 at a time. Where registers allow,
+// the next tile is requested before the present one is used; a team of more
+// than one wave has two buffers in LDS where they leave room for two
+// workgroups, so that one barrier a tile does.
+
+constexpr int kStreamRows = 32;
+
+template <int ND, int W, int N, int X>
+struct Stream {
+    using T = Team<W>;
+    static constexpr int RS = Heads<ND>::RS, kPiece = kStreamRows * RS, kArray = 3 * kPiece;
+    static constexpr int kQuads = 8 * Heads<ND>::KS, kAll = kStreamRows * kQuads, kEach = (kAll + T::kThreads - 1) / T::kThreads;
+    static constexpr int kBytes = N * kArray * 2 + X * kStreamRows * 4;
+    static constexpr bool kAhead = N * kEach <= 16;
+    static constexpr int kBuffers = W > 1 && kAhead && 2 * kBytes <= 80 * 1024 ? 2 : 1;
+    static_assert(kBytes % 16 == 0, "buffers stay aligned");
+
+    char* base;
+    int turn = 0;
+
+    struct Tile {
+        f32x4_t v[kEach];
+    };
+
+    // where(i, row): array i's row, null for a row of zeros
+    template <class F>
+    __device__ __forceinline__ void fetch(Tile& t, int i, int dim, F&& where)
+    {
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) {
+            const int at = T::thread() + e * T::kThreads, row = at / kQuads, col = at % kQuads * 4;
+            const float* p = kAll % T::kThreads != 0 && at >= kAll ? nullptr : where(i, row);
+            t.v[e] = p != nullptr ? load4(p, col, dim) : f32x4_t{};
+        }
+    }
+    __device__ __forceinline__ void put(const Tile& t, uint16_t* array)
+    {
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) {
+            const int at = T::thread() + e * T::kThreads, row = at / kQuads, col = at % kQuads * 4;
+            const Split4 s = split4(t.v[e]);
+            if (kAll % T::kThreads != 0 && at >= kAll) continue;
+#pragma unroll
+            for (int i = 0; i < 3; ++i) *reinterpret_cast<u32x2_t*>(array + i * kPiece + row * RS + col) = s.p[i];
+        }
+    }
+
+    // f(first row, arrays, numbers) for the tiles of lo .. hi: array i at
+    // arrays + i kArray, its number x of row r at numbers + x kStreamRows + r.
+    // where(first, i, row) as above; number(first, numbers): those of row
+    // first + thread.
+    template <class P, class Q, class F>
+    __device__ __forceinline__ void run(int64_t lo, int64_t hi, int dim, P&& where, Q&& number, F&& f)
+    {
+        Tile tiles[kAhead ? N : 1];
+        float numbers[X];
+        const auto request = [&](int64_t first) {
+            if constexpr (kAhead) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) fetch(tiles[i], i, dim, [&](int a, int row) { return where(first, a, row); });
+            }
+            if (T::thread() < kStreamRows) number(first, numbers);
+        };
+        if (lo < hi) request(lo);
+        for (int64_t first = lo; first < hi; first += kStreamRows) {
+            if (kBuffers == 1) T::sync();   // the previous tile has been read
+            char* const buffer = base + (kBuffers == 2 ? (turn ^= 1) * kBytes : 0);
+            uint16_t* const arrays = reinterpret_cast<uint16_t*>(buffer);
+            float* const nums = reinterpret_cast<float*>(buffer + N * kArray * 2);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                if constexpr (!kAhead) fetch(tiles[0], i, dim, [&](int a, int row) { return where(first, a, row); });
+                put(tiles[kAhead ? i : 0], arrays + i * kArray);
+            }
+            if (T::thread() < kStreamRows) {
+#pragma unroll
+                for (int i = 0; i < X; ++i) nums[i * kStreamRows + T::thread()] = numbers[i];
+            }
+            T::sync();
+            if (first + kStreamRows < hi) request(first + kStreamRows);
+            f(first, (const uint16_t*)arrays, (const float*)nums);
+        }
+    }
+};
+
+// Whether any key of a tile of 32 takes no part, and the terms of a lane's keys.
+struct Terms {
+    f32x4_t of[2];
+    bool some;
+    __device__ __forceinline__ Terms(const float* term, int h)
+    {
+        of[0] = *reinterpret_cast<const f32x4_t*>(term + 4 * h);
+        of[1] = *reinterpret_cast<const f32x4_t*>(term + 16 + 4 * h);
+        bool any = false;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) any = any || of[t][j] == minus_inf();
+        some = __any(any) != 0;
+    }
+    __device__ __forceinline__ bool dead(int t, int j) const { return of[t][j] == minus_inf(); }
+};
+
+// f.template operator()<ND, W, NT>() for a head and plan; WIDE: tiles of 16
+// per wave that the registers hold of heads above 64, as the plan has it.
+template <int WIDE, class F>
+inline void with_shape(int dim, const AttnPlan& p, F&& f)
+{
+    const auto tiles = [&]<int ND>() {
+        if constexpr (ND <= 4 || WIDE == 2) {
+            if (p.tiles == 2) {
+                if (p.waves == 1) return f.template operator()<ND, 1, 2>();
+                return f.template operator()<ND, 4, 2>();
+            }
+        }
+        if (p.waves == 1) return f.template operator()<ND, 1, 1>();
+        return f.template operator()<ND, 4, 1>();
+    };
+    if (dim <= 16)
+        tiles.template operator()<1>();
+    else if (dim <= 32)
+        tiles.template operator()<2>();
+    else if (dim <= 48)
+        tiles.template operator()<3>();
+    else if (dim <= 64)
+        tiles.template operator()<4>();
+    else if (dim <= 80)
+        tiles.template operator()<5>();
+    else if (dim <= 96)
+        tiles.template operator()<6>();
+    else
+        tiles.template operator()<8>();
+}
+
+}  // namespace emu

@@ -3,9 +3,12 @@ arithmetic of the same formulas may be off.
 
 ``Bounded`` carries a value and a bound of its error through each operation
 (running error analysis): an FP32 operation adds u = 2^-24 of its result's
-size, a sum of n products in any order n u of the sum of their absolute
-values, on top of what its operands bring.  The bound is first order, times
-1.01 for the rest.
+size, a sum of n numbers in any order n u of the sum of their absolute values,
+on top of what its operands bring.  A matrix product of n terms adds (2 n + 10)
+u of the sum of |a b|: 2 u an addition on the matrix unit, as for the GEMMs
+(tests/gpu_helpers.py); split operands leave out 2^-25 of |a b|, and their six
+products' additions, 6 / 32 n instructions, are fewer than 2 n.  The bound is
+first order, times 1.01 for the rest.
 """
 import math
 
@@ -35,7 +38,7 @@ class Bounded:
 
     def __matmul__(self, o):
         a, b = self.v.abs(), o.v.abs()
-        n = self.v.shape[-1] + 2
+        n = 2 * self.v.shape[-1] + 10
         return Bounded(self.v @ o.v, self.e @ b + a @ o.e + n * U * (a @ b))
 
     def sum(self, dim, keepdim=False, extra=0):
