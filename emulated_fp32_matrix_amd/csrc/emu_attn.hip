@@ -14,6 +14,7 @@ namespace emu {
 namespace {
 
 constexpr int kMostSplits = 64;
+constexpr float kSlack = 4.0f;
 
 // Partial results of a split: rows' results, then their maxima and sums.
 struct ForwardPartial {
@@ -27,13 +28,14 @@ __host__ __device__ __forceinline__ ForwardPartial forward_partial(const AttnArg
 }
 
 template <int ND, int W, int NQ>
-__global__ __launch_bounds__(64 * W) void forward_kernel(AttnArgs a, AttnPlan plan, emu_heads_t q, emu_heads_t k,
+__global__ __launch_bounds__(64 * W, attn_waves(AttnPass::forward, ND)) void forward_kernel(AttnArgs a, AttnPlan plan, emu_heads_t q, emu_heads_t k,
                                                          emu_heads_t v, float* out, float* stats, float* partial)
 {
     using T = Team<W>;
-    using S = Stream<ND, W, 2, 1>;
+    using S = Stream<ND, W, 2, 1, true>;
     __shared__ __attribute__((aligned(16))) char lds[S::kBuffers * S::kBytes];
     S stream{lds};
+    stream.clear();
     const int lane = threadIdx.x & 63, m = lane & 15, h = lane >> 4;
 
     T::each_piece((int64_t)a.batch * a.kv_heads * plan.own * plan.splits, [&](int64_t piece) {
@@ -56,12 +58,8 @@ __global__ __launch_bounds__(64 * W) void forward_kernel(AttnArgs a, AttnPlan pl
         }
         clear(acc);
 
-        const auto where = [&](int64_t first, int i, int row) {
-            return key_term(a, at.b, (int)first + row, limit) != minus_inf() ? key_ptr(i == 0 ? k : v, at.b, at.g, first + row)
-                                                                             : nullptr;
-        };
         const auto number = [&](int64_t first, float* to) { to[0] = key_term(a, at.b, (int)first + T::thread(), limit); };
-        stream.run(lo, hi, a.dim, where, number, [&](int64_t, const uint16_t* arrays, const float* numbers) {
+        stream.run_keys(a, at, lo, hi, number, [&](int64_t, const uint16_t* arrays, const float* numbers) {
             const Terms term(numbers, h);
             f32x4_t s[2][NQ];
 #pragma unroll
@@ -82,7 +80,12 @@ __global__ __launch_bounds__(64 * W) void forward_kernel(AttnArgs a, AttnPlan pl
 #pragma unroll
                         for (int j = 0; j < 4; ++j) s[t][n][j] = term.dead(t, j) ? minus_inf() : s[t][n][j];
             }
-            Split8 w[NQ];
+            // The factor's exponent follows the maximum only where that has
+            // grown by more than kSlack since: sums and results of up to
+            // e^kSlack a key lose nothing in FP32, and most tiles leave the
+            // results as they are.
+            bool grown = false;
+            float next[NQ];
 #pragma unroll
             for (int n = 0; n < NQ; ++n) {
                 float top = s[0][n][0];
@@ -90,10 +93,24 @@ __global__ __launch_bounds__(64 * W) void forward_kernel(AttnArgs a, AttnPlan pl
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) top = __builtin_fmaxf(top, s[t][n][j]);
-                const float next = __builtin_fmaxf(most[n], column_max(top));
-                const float safe = next == minus_inf() ? 0.0f : next;   // (no key so far: all of e^(-inf - 0) = 0)
-                const float old = exp_of(most[n] - safe);
-                most[n] = next;
+                next[n] = column_max(top);
+                grown = grown || next[n] > most[n] + kSlack;
+            }
+            if (__any(grown)) {
+#pragma unroll
+                for (int n = 0; n < NQ; ++n) {
+                    next[n] = __builtin_fmaxf(most[n], next[n]);
+                    const float old = most[n] == next[n] ? 1.0f : exp_of(most[n] - next[n]);
+                    most[n] = next[n];
+                    sum[n] = sum[n] * old;
+#pragma unroll
+                    for (int t = 0; t < ND; ++t) acc[n][t] = acc[n][t] * old;
+                }
+            }
+            Split8 w[NQ];
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) {
+                const float safe = most[n] == minus_inf() ? 0.0f : most[n];   // (no key so far: all of e^(-inf - 0) = 0)
                 float here = 0.0f;
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
@@ -102,13 +119,11 @@ __global__ __launch_bounds__(64 * W) void forward_kernel(AttnArgs a, AttnPlan pl
                         s[t][n][j] = exp_of(s[t][n][j] - safe);
                         here = here + s[t][n][j];
                     }
-                sum[n] = __builtin_fmaf(sum[n], old, here);
-#pragma unroll
-                for (int t = 0; t < ND; ++t) acc[n][t] = acc[n][t] * old;
+                sum[n] = sum[n] + here;
                 w[n] = split8(s[0][n], s[1][n]);
             }
             results<ND, S::kPiece, NQ>(arrays + S::kArray, m, h, w, acc);
-        });
+        }, k, v);
 
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
@@ -204,23 +219,20 @@ int splits_for(int64_t waves, int64_t other, int64_t least)
     return s < 1 ? 1 : (int)s;
 }
 
-// `most`: tiles of 16 per wave that fit its registers.
-AttnPlan plan_for(const AttnArgs& a, int64_t own, int64_t other, int most)
+}  // namespace
+
+AttnPlan attn_plan(const AttnArgs& a, AttnPass pass)
 {
+    const bool keys = pass == AttnPass::keys || pass == AttnPass::second_keys;
+    const int64_t own = keys ? a.keys : a.rows, other = keys ? a.rows : a.keys;
     AttnPlan p{};
-    p.waves = own <= 32 ? 1 : 4;
-    p.tiles = most == 1 || own <= 16 || (own > 32 && own <= 64) ? 1 : 2;
-    if (p.waves == 1 && own > 16 * p.tiles) p.waves = 4;
+    p.waves = own <= 16 ? 1 : own <= 32 ? 2 : 4;
+    p.tiles = own <= 64 ? 1 : attn_tiles(pass, a.dim);
     const int64_t each = p.waves * p.tiles * 16;
     p.own = (own + each - 1) / each;
     p.splits = splits_for((int64_t)a.batch * a.kv_heads * p.own * p.waves, other, p.waves == 1 ? 128 : 256);
     return p;
 }
-
-}  // namespace
-
-AttnPlan attn_rows_plan(const AttnArgs& a, int order) { return plan_for(a, a.rows, a.keys, a.dim > 64 && order == 2 ? 1 : 2); }
-AttnPlan attn_keys_plan(const AttnArgs& a, int) { return plan_for(a, a.keys, a.rows, a.dim > 64 ? 1 : 2); }
 
 size_t attn_forward_partial(const AttnArgs& a, const AttnPlan& p)
 {
@@ -242,7 +254,7 @@ size_t attn_bias_partial(const AttnArgs& a, const AttnPlan& p)
 hipError_t launch_attn_forward(const AttnArgs& a, const AttnPlan& p, emu_heads_t q, emu_heads_t k, emu_heads_t v,
                                float* out, float* stats, float* partial, hipStream_t s)
 {
-    with_shape<2>(a.dim, p, [&]<int ND, int W, int NQ>() {
+    with_shape<AttnPass::forward>(a.dim, p, [&]<int ND, int W, int NQ>() {
         const int64_t n = (int64_t)a.batch * a.kv_heads * p.own * p.splits;
         forward_kernel<ND, W, NQ><<<Team<W>::grid(n), 64 * W, 0, s>>>(a, p, q, k, v, out, stats, partial);
     });

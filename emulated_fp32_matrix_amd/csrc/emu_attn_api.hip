@@ -92,14 +92,14 @@ size_t rows_of(const AttnArgs& a) { return (size_t)a.batch * a.queries * a.heads
 size_t forward_bytes(const AttnArgs& a)
 {
     if (!has_rows(a) || emu::attn_whole(a, 0)) return 0;
-    return round256(emu::attn_forward_partial(a, emu::attn_rows_plan(a, 0)) * sizeof(float));
+    return round256(emu::attn_forward_partial(a, emu::attn_plan(a, emu::AttnPass::forward)) * sizeof(float));
 }
 
 struct BackwardSpace {
     AttnPlan rows, keys;
     float *delta, *dq, *dk, *dv, *db;
     size_t bytes;
-    BackwardSpace(const AttnArgs& a, void* ws) : rows(emu::attn_rows_plan(a, 1)), keys(emu::attn_keys_plan(a, 1))
+    BackwardSpace(const AttnArgs& a, void* ws) : rows(emu::attn_plan(a, emu::AttnPass::rows)), keys(emu::attn_plan(a, emu::AttnPass::keys))
     {
         Layout l(ws);
         delta = dq = dk = dv = db = nullptr;
@@ -121,7 +121,7 @@ struct SecondSpace {
     AttnPlan rows, keys;
     float *delta, *sums, *go, *gq, *gk, *gv, *gb;
     size_t bytes;
-    SecondSpace(const AttnArgs& a, void* ws) : rows(emu::attn_rows_plan(a, 2)), keys(emu::attn_keys_plan(a, 2))
+    SecondSpace(const AttnArgs& a, void* ws) : rows(emu::attn_plan(a, emu::AttnPass::second_rows)), keys(emu::attn_plan(a, emu::AttnPass::second_keys))
     {
         Layout l(ws);
         delta = sums = go = gq = gk = gv = gb = nullptr;
@@ -186,7 +186,7 @@ emu_status_t emu_cross_attention(const emu_attention_t* in, emu_heads_t q, emu_h
     if (bad_workspace(workspace, workspace_bytes, forward_bytes(a))) return EMU_STATUS_INVALID_VALUE;
     if (!on_gfx950()) return EMU_STATUS_NOT_SUPPORTED;
     if (emu::attn_whole(a, 0)) return from_hip(emu::launch_whole_forward(a, q, k, v, out, stats, stream_of(stream)));
-    return from_hip(emu::launch_attn_forward(a, emu::attn_rows_plan(a, 0), q, k, v, out, stats, static_cast<float*>(workspace), stream_of(stream)));
+    return from_hip(emu::launch_attn_forward(a, emu::attn_plan(a, emu::AttnPass::forward), q, k, v, out, stats, static_cast<float*>(workspace), stream_of(stream)));
 }
 
 emu_status_t emu_cross_attention_backward_workspace(const emu_attention_t* in, size_t* bytes)

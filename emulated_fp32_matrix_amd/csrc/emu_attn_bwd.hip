@@ -12,14 +12,15 @@ namespace emu {
 namespace {
 
 template <int ND, int W, int NQ>
-__global__ __launch_bounds__(64 * W) void rows_kernel(AttnArgs a, AttnPlan plan, emu_heads_t dout, emu_heads_t q,
+__global__ __launch_bounds__(64 * W, attn_waves(AttnPass::rows, ND)) void rows_kernel(AttnArgs a, AttnPlan plan, emu_heads_t dout, emu_heads_t q,
                                                       emu_heads_t k, emu_heads_t v, const float* out, const float* stats,
                                                       float* delta, float* dq, float* partial)
 {
     using T = Team<W>;
-    using S = Stream<ND, W, 2, 1>;
+    using S = Stream<ND, W, 2, 1, true>;
     __shared__ __attribute__((aligned(16))) char lds[S::kBuffers * S::kBytes];
     S stream{lds};
+    stream.clear();
     const int lane = threadIdx.x & 63, m = lane & 15, h = lane >> 4;
 
     T::each_piece((int64_t)a.batch * a.kv_heads * plan.own * plan.splits, [&](int64_t piece) {
@@ -47,13 +48,9 @@ __global__ __launch_bounds__(64 * W) void rows_kernel(AttnArgs a, AttnPlan plan,
         }
         clear(acc);
 
-        const auto where = [&](int64_t first, int i, int row) {
-            return key_term(a, at.b, (int)first + row, limit) != minus_inf() ? key_ptr(i == 0 ? k : v, at.b, at.g, first + row)
-                                                                             : nullptr;
-        };
         const auto number = [&](int64_t first, float* to) { to[0] = key_term(a, at.b, (int)first + T::thread(), limit); };
-        stream.run(lo, dq != nullptr ? hi : lo, a.dim, where, number,
-                   [&](int64_t, const uint16_t* arrays, const float* numbers) {
+        stream.run_keys(a, at, lo, dq != nullptr ? hi : lo, number,
+                        [&](int64_t, const uint16_t* arrays, const float* numbers) {
             const Terms term(numbers, h);
             f32x4_t s[2][NQ], dp[2][NQ];
 #pragma unroll
@@ -82,7 +79,7 @@ __global__ __launch_bounds__(64 * W) void rows_kernel(AttnArgs a, AttnPlan plan,
 #pragma unroll
             for (int n = 0; n < NQ; ++n) w[n] = split8(s[0][n], s[1][n]);
             results<ND, S::kPiece, NQ>(arrays, m, h, w, acc);
-        });
+        }, k, v);
 
         if (dq == nullptr) return;
 #pragma unroll
@@ -97,14 +94,15 @@ __global__ __launch_bounds__(64 * W) void rows_kernel(AttnArgs a, AttnPlan plan,
 }
 
 template <int ND, int W, int NT>
-__global__ __launch_bounds__(64 * W) void keys_kernel(AttnArgs a, AttnPlan plan, emu_heads_t dout, emu_heads_t q,
+__global__ __launch_bounds__(64 * W, attn_waves(AttnPass::keys, ND)) void keys_kernel(AttnArgs a, AttnPlan plan, emu_heads_t dout, emu_heads_t q,
                                                       emu_heads_t k, emu_heads_t v, const float* stats,
                                                       const float* delta, float* dk, float* dv, float* db)
 {
     using T = Team<W>;
-    using S = Stream<ND, W, 2, 3>;
+    using S = Stream<ND, W, 2, 3, false>;
     __shared__ __attribute__((aligned(16))) char lds[S::kBuffers * S::kBytes];
     S stream{lds};
+    stream.clear();
     const int lane = threadIdx.x & 63, m = lane & 15, h = lane >> 4;
 
     T::each_piece((int64_t)a.batch * a.kv_heads * plan.own * plan.splits, [&](int64_t piece) {
@@ -131,9 +129,6 @@ __global__ __launch_bounds__(64 * W) void keys_kernel(AttnArgs a, AttnPlan plan,
         // (a team whose keys all take no part has zeros to write)
         if (at.own * W * 16 * NT >= limit) hi = lo;
 
-        const auto where = [&](int64_t first, int i, int row) {
-            return first + row < hi ? row_ptr(i == 0 ? q : dout, at.b, row_at(a, at.g, first + row)) : nullptr;
-        };
         // maxima, 1 / sums, deltas; behind the last row p = e^-inf 0
         const auto number = [&](int64_t first, float* to) {
             const bool valid = first + T::thread() < hi;
@@ -142,7 +137,7 @@ __global__ __launch_bounds__(64 * W) void keys_kernel(AttnArgs a, AttnPlan plan,
             to[1] = valid ? stats[2 * row + 1] : 0.0f;
             to[2] = valid ? delta[row] : 0.0f;
         };
-        stream.run(lo, hi, a.dim, where, number, [&](int64_t, const uint16_t* arrays, const float* numbers) {
+        stream.run_rows(a, at, lo, hi, number, [&](int64_t, const uint16_t* arrays, const float* numbers) {
             f32x4_t s[2][NT], dp[2][NT];
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
@@ -171,7 +166,7 @@ __global__ __launch_bounds__(64 * W) void keys_kernel(AttnArgs a, AttnPlan plan,
 #pragma unroll
             for (int n = 0; n < NT; ++n) w[n] = split8(dp[0][n], dp[1][n]);
             results<ND, S::kPiece, NT>(arrays, m, h, w, ak);
-        });
+        }, q, dout);
 
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -199,7 +194,7 @@ hipError_t launch_attn_backward_rows(const AttnArgs& a, const AttnPlan& p, emu_h
                                      emu_heads_t k, emu_heads_t v, const float* out, const float* stats,
                                      float* delta, float* dq, float* partial, hipStream_t s)
 {
-    with_shape<2>(a.dim, p, [&]<int ND, int W, int NQ>() {
+    with_shape<AttnPass::rows>(a.dim, p, [&]<int ND, int W, int NQ>() {
         const int64_t n = (int64_t)a.batch * a.kv_heads * p.own * p.splits;
         rows_kernel<ND, W, NQ><<<Team<W>::grid(n), 64 * W, 0, s>>>(a, p, dout, q, k, v, out, stats, delta, dq, partial);
     });
@@ -218,7 +213,7 @@ hipError_t launch_attn_backward_keys(const AttnArgs& a, const AttnPlan& p, emu_h
     float* const to_k = dk != nullptr && cut ? partial_k : dk;
     float* const to_v = dv != nullptr && cut ? partial_v : dv;
     float* const to_b = join_bias ? partial_b : dbias;
-    with_shape<1>(a.dim, p, [&]<int ND, int W, int NT>() {
+    with_shape<AttnPass::keys>(a.dim, p, [&]<int ND, int W, int NT>() {
         const int64_t n = (int64_t)a.batch * a.kv_heads * p.own * p.splits;
         keys_kernel<ND, W, NT><<<Team<W>::grid(n), 64 * W, 0, s>>>(a, p, dout, q, k, v, stats, delta, to_k, to_v, to_b);
     });

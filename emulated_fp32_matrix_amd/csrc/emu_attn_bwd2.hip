@@ -15,14 +15,15 @@ namespace emu {
 namespace {
 
 template <int ND, int W, int NQ, bool SUMS>
-__global__ __launch_bounds__(64 * W) void rows_kernel(AttnArgs a, AttnPlan plan, AttnSeconds x, float* delta, float* sums,
+__global__ __launch_bounds__(64 * W, attn_waves(AttnPass::second_rows, ND)) void rows_kernel(AttnArgs a, AttnPlan plan, AttnSeconds x, float* delta, float* sums,
                                                       float* go, float* gq)
 {
     using T = Team<W>;
-    using S = Stream<ND, W, 4, 2>;
+    using S = Stream<ND, W, 4, 2, true>;
     constexpr int KS = Heads<ND>::KS;
     __shared__ __attribute__((aligned(16))) char lds[S::kBuffers * S::kBytes];
     S stream{lds};
+    stream.clear();
     const int lane = threadIdx.x & 63, m = lane & 15, h = lane >> 4;
     const int64_t all_rows = (int64_t)a.batch * a.queries * a.heads;
 
@@ -63,18 +64,12 @@ __global__ __launch_bounds__(64 * W) void rows_kernel(AttnArgs a, AttnPlan plan,
         clear(ao);
         clear(aq);
 
-        const auto where = [&](int64_t first, int i, int row) {
-            const emu_heads_t& t = i == 0 ? x.k : i == 1 ? x.v : i == 2 ? x.vk : x.vv;
-            return t.data != nullptr && key_term(a, at.b, (int)first + row, limit) != minus_inf()
-                       ? key_ptr(t, at.b, at.g, first + row)
-                       : nullptr;
-        };
         const auto number = [&](int64_t first, float* to) {
             to[0] = key_term(a, at.b, (int)first + T::thread(), limit);
             to[1] = x.vbias != nullptr && to[0] != minus_inf() ? x.vbias[at.b * x.vbias_b + (first + T::thread()) * x.vbias_k]
                                                                : 0.0f;
         };
-        stream.run(lo, hi, a.dim, where, number, [&](int64_t, const uint16_t* arrays, const float* numbers) {
+        stream.run_keys(a, at, lo, hi, number, [&](int64_t, const uint16_t* arrays, const float* numbers) {
             const Terms term(numbers, h);
             const uint16_t *const tk = arrays, *const tv = tk + S::kArray, *const tvk = tv + S::kArray,
                            *const tvv = tvk + S::kArray;
@@ -123,7 +118,7 @@ __global__ __launch_bounds__(64 * W) void rows_kernel(AttnArgs a, AttnPlan plan,
                 add(ee, tk, aq);    // U k
                 add(dp, tvk, aq);   // ds vk
             }
-        });
+        }, x.k, x.v, x.vk, x.vv);
 
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
@@ -146,14 +141,15 @@ __global__ __launch_bounds__(64 * W) void rows_kernel(AttnArgs a, AttnPlan plan,
 }
 
 template <int ND, int W, int NT>
-__global__ __launch_bounds__(64 * W) void keys_kernel(AttnArgs a, AttnPlan plan, AttnSeconds x, const float* delta,
+__global__ __launch_bounds__(64 * W, attn_waves(AttnPass::second_keys, ND)) void keys_kernel(AttnArgs a, AttnPlan plan, AttnSeconds x, const float* delta,
                                                       const float* sums, int sum_splits, float* gk, float* gv, float* gb)
 {
     using T = Team<W>;
-    using S = Stream<ND, W, 3, 5>;
+    using S = Stream<ND, W, 3, 5, false>;
     constexpr int KS = Heads<ND>::KS;
     __shared__ __attribute__((aligned(16))) char lds[S::kBuffers * S::kBytes];
     S stream{lds};
+    stream.clear();
     const int lane = threadIdx.x & 63, m = lane & 15, h = lane >> 4;
     const int64_t all_rows = (int64_t)a.batch * a.queries * a.heads;
 
@@ -185,10 +181,6 @@ __global__ __launch_bounds__(64 * W) void keys_kernel(AttnArgs a, AttnPlan plan,
         // (a team whose keys all take no part has zeros to write)
         if (at.own * W * 16 * NT >= limit) hi = lo;
 
-        const auto where = [&](int64_t first, int i, int row) {
-            const emu_heads_t& t = i == 0 ? x.q : i == 1 ? x.dout : x.vq;
-            return t.data != nullptr && first + row < hi ? row_ptr(t, at.b, row_at(a, at.g, first + row)) : nullptr;
-        };
         // maxima, 1 / sums, deltas, g, t; behind the last row p = e^-inf 0
         const auto number = [&](int64_t first, float* to) {
             const bool valid = first + T::thread() < hi;
@@ -204,7 +196,7 @@ __global__ __launch_bounds__(64 * W) void keys_kernel(AttnArgs a, AttnPlan plan,
             to[3] = g;
             to[4] = __builtin_fmaf(-g, to[2], t);
         };
-        stream.run(lo, hi, a.dim, where, number, [&](int64_t, const uint16_t* arrays, const float* numbers) {
+        stream.run_rows(a, at, lo, hi, number, [&](int64_t, const uint16_t* arrays, const float* numbers) {
             const uint16_t *const tq = arrays, *const td = tq + S::kArray, *const ta = td + S::kArray;
             f32x4_t s[2][NT], dp[2][NT], gg[2][NT], ee[2][NT];
 #pragma unroll
@@ -247,7 +239,7 @@ __global__ __launch_bounds__(64 * W) void keys_kernel(AttnArgs a, AttnPlan plan,
             sum(gg, td, av);   // H dout
             sum(ee, tq, ak);   // U q
             sum(dp, ta, ak);   // ds vq
-        });
+        }, x.q, x.dout, x.vq);
 
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -275,7 +267,7 @@ int64_t pieces(const AttnArgs& a, const AttnPlan& p) { return (int64_t)a.batch *
 hipError_t launch_attn_second_sums(const AttnArgs& a, const AttnPlan& p, const AttnSeconds& x, float* delta,
                                    float* sums, hipStream_t s)
 {
-    with_shape<1>(a.dim, p, [&]<int ND, int W, int NQ>() {
+    with_shape<AttnPass::second_rows>(a.dim, p, [&]<int ND, int W, int NQ>() {
         rows_kernel<ND, W, NQ, true><<<Team<W>::grid(pieces(a, p)), 64 * W, 0, s>>>(a, p, x, delta, sums, nullptr, nullptr);
     });
     return hipGetLastError();
@@ -288,7 +280,7 @@ hipError_t launch_attn_second_rows(const AttnArgs& a, const AttnPlan& p, const A
     const bool cut = p.splits > 1;
     float* const to_o = gdout != nullptr && cut ? partial_o : gdout;
     float* const to_q = gq != nullptr && cut ? partial_q : gq;
-    with_shape<1>(a.dim, p, [&]<int ND, int W, int NQ>() {
+    with_shape<AttnPass::second_rows>(a.dim, p, [&]<int ND, int W, int NQ>() {
         rows_kernel<ND, W, NQ, false><<<Team<W>::grid(pieces(a, p)), 64 * W, 0, s>>>(
             a, p, x, const_cast<float*>(delta), const_cast<float*>(sums), to_o, to_q);
     });
@@ -307,7 +299,7 @@ hipError_t launch_attn_second_keys(const AttnArgs& a, const AttnPlan& p, const A
     float* const to_k = gk != nullptr && cut ? partial_k : gk;
     float* const to_v = gv != nullptr && cut ? partial_v : gv;
     float* const to_b = join_bias ? partial_b : gbias;
-    with_shape<1>(a.dim, p, [&]<int ND, int W, int NT>() {
+    with_shape<AttnPass::second_keys>(a.dim, p, [&]<int ND, int W, int NT>() {
         keys_kernel<ND, W, NT><<<Team<W>::grid(pieces(a, p)), 64 * W, 0, s>>>(a, p, x, delta, sums, sum_splits, to_k, to_v, to_b);
     });
     hipError_t e = hipGetLastError();

@@ -25,6 +25,23 @@ struct AttnArgs {
     int lengths_64;
 };
 
+// The passes of longer sequences: the forward pass, its backward pass over rows
+// and over keys, and that one's (its rows' sums and results share a plan).
+enum class AttnPass { forward, rows, keys, second_rows, second_keys };
+
+// Tiles of 16 of its own side that a wave's registers hold while two waves fit
+// a SIMD.
+constexpr int attn_tiles(AttnPass pass, int dim)
+{
+    return dim <= (pass == AttnPass::forward ? 96 : pass == AttnPass::rows || pass == AttnPass::keys ? 64 : 32) ? 2 : 1;
+}
+// Waves of a SIMD that the registers are divided among: one where even a tile
+// each of wide heads does not fit half of them.
+constexpr int attn_waves(AttnPass pass, int nd)
+{
+    return nd >= 5 && (pass == AttnPass::second_rows || pass == AttnPass::second_keys) ? 1 : nd >= 8 && pass == AttnPass::keys ? 1 : 2;
+}
+
 // How a pass is cut into pieces of work: a team of `waves` waves takes
 // `tiles` tiles of 16 (of its own side) per wave and one of `splits` ranges of
 // the other side.
@@ -32,12 +49,7 @@ struct AttnPlan {
     int waves, tiles, splits;
     int64_t own;             // pieces along the team's own side
 };
-
-// Pass over rows (the keys stream by) and pass over keys (the rows stream by)
-// of the forward pass (order 0, rows only), its backward pass (1) and that
-// one's (2).
-AttnPlan attn_rows_plan(const AttnArgs& a, int order);
-AttnPlan attn_keys_plan(const AttnArgs& a, int order);
+AttnPlan attn_plan(const AttnArgs& a, AttnPass pass);
 
 // The forward pass; partial: null unless plan.splits > 1.
 size_t attn_forward_partial(const AttnArgs& a, const AttnPlan& p);

@@ -192,11 +192,21 @@ __device__ __forceinline__ void clear(f32x4_t (&acc)[NT][ND])
 
 constexpr int kStreamRows = 32;
 
-template <int ND, int W, int N, int X>
+// An array as a thread reads it: a tile's rows begin at base + first row / 32
+// * tile floats, the thread's there at offset + e * step.
+struct StreamRows {
+    const float* base;       // null: zeros
+    int64_t tile, step;
+    int offset;
+};
+
+template <int ND, int W, int N, int X, bool KEYS>
 struct Stream {
     using T = Team<W>;
     static constexpr int RS = Heads<ND>::RS, kPiece = kStreamRows * RS, kArray = 3 * kPiece;
-    static constexpr int kQuads = 8 * Heads<ND>::KS, kAll = kStreamRows * kQuads, kEach = (kAll + T::kThreads - 1) / T::kThreads;
+    // threads along a row (a power of two), a thread's rows and the distance between them
+    static constexpr int kQuads = Heads<ND>::KS == 3 ? 32 : 8 * Heads<ND>::KS, kStep = T::kThreads / kQuads < kStreamRows ? T::kThreads / kQuads : kStreamRows;
+    static constexpr int kEach = kStreamRows / kStep;
     static constexpr int kBytes = N * kArray * 2 + X * kStreamRows * 4;
     static constexpr bool kAhead = N * kEach <= 16;
     static constexpr int kBuffers = W > 1 && kAhead && 2 * kBytes <= 80 * 1024 ? 2 : 1;
@@ -209,42 +219,53 @@ struct Stream {
         f32x4_t v[kEach];
     };
 
-    // where(i, row): array i's row, null for a row of zeros
-    template <class F>
-    __device__ __forceinline__ void fetch(Tile& t, int i, int dim, F&& where)
+    // Once: what lies past the heads' width is zero and stays so.
+    __device__ __forceinline__ void clear()
     {
-#pragma unroll
-        for (int e = 0; e < kEach; ++e) {
-            const int at = T::thread() + e * T::kThreads, row = at / kQuads, col = at % kQuads * 4;
-            const float* p = kAll % T::kThreads != 0 && at >= kAll ? nullptr : where(i, row);
-            t.v[e] = p != nullptr ? load4(p, col, dim) : f32x4_t{};
-        }
-    }
-    __device__ __forceinline__ void put(const Tile& t, uint16_t* array)
-    {
-#pragma unroll
-        for (int e = 0; e < kEach; ++e) {
-            const int at = T::thread() + e * T::kThreads, row = at / kQuads, col = at % kQuads * 4;
-            const Split4 s = split4(t.v[e]);
-            if (kAll % T::kThreads != 0 && at >= kAll) continue;
-#pragma unroll
-            for (int i = 0; i < 3; ++i) *reinterpret_cast<u32x2_t*>(array + i * kPiece + row * RS + col) = s.p[i];
-        }
+        for (int i = T::thread(); i < kBuffers * kBytes / 16; i += T::kThreads) reinterpret_cast<u32x4_t*>(base)[i] = u32x4_t{};
+        T::sync();
     }
 
-    // f(first row, arrays, numbers) for the tiles of lo .. hi: array i at
-    // arrays + i kArray, its number x of row r at numbers + x kStreamRows + r.
-    // where(first, i, row) as above; number(first, numbers): those of row
-    // first + thread.
-    template <class P, class Q, class F>
-    __device__ __forceinline__ void run(int64_t lo, int64_t hi, int dim, P&& where, Q&& number, F&& f)
+    static_assert(kStep * kEach == kStreamRows && T::kThreads <= kQuads * kStreamRows, "every thread has whole quads of rows");
+    static __device__ __forceinline__ int row() { return T::thread() / kQuads; }
+    static __device__ __forceinline__ int col() { return T::thread() % kQuads * 4; }
+
+    // f(first row, arrays, numbers) for the tiles of lo .. hi (lo a multiple of
+    // 32): array i at arrays + i kArray, its number x of row r at numbers + x
+    // kStreamRows + r.
+    // rows(i): array i's StreamRows; even: they hold for whole tiles (else,
+    // and in the last, cut tile, where(i, row) is the row's address).
+    // number(first, numbers): those of row first + thread, < 32.
+    // KEYS: number 0 is a key's term; what is loaded of keys that take no part
+    // is dropped again.
+    template <class R, class P, class Q, class F>
+    __device__ __forceinline__ void run(int64_t lo, int64_t hi, int dim, bool even, R&& rows, P&& where, Q&& number, F&& f)
     {
         Tile tiles[kAhead ? N : 1];
         float numbers[X];
+        even = even && dim % 4 == 0;
+        const bool has = col() < dim;
+        const auto fetch = [&](int i, int64_t first) {
+            Tile& t = tiles[kAhead ? i : 0];
+            const StreamRows r = rows(i);
+            if (even && first + kStreamRows <= hi) {
+                if (r.base == nullptr || !has) return;   // (zeros since clear())
+                const char* from = reinterpret_cast<const char*>(r.base + (first >> 5) * r.tile);
+                const uint32_t at = (uint32_t)(r.offset + col()) * 4u;
+#pragma unroll
+                for (int e = 0; e < kEach; ++e) t.v[e] = *reinterpret_cast<const f32x4u_t*>(from + e * r.step * 4 + at);
+            } else {
+#pragma unroll
+                for (int e = 0; e < kEach; ++e) {
+                    const int64_t at = first + row() + e * kStep;
+                    t.v[e] = has && at < hi && r.base != nullptr ? load4(where(i, at), col(), dim) : f32x4_t{};
+                }
+            }
+        };
         const auto request = [&](int64_t first) {
             if constexpr (kAhead) {
 #pragma unroll
-                for (int i = 0; i < N; ++i) fetch(tiles[i], i, dim, [&](int a, int row) { return where(first, a, row); });
+                for (int i = 0; i < N; ++i) fetch(i, first);
             }
             if (T::thread() < kStreamRows) number(first, numbers);
         };
@@ -256,18 +277,78 @@ struct Stream {
             float* const nums = reinterpret_cast<float*>(buffer + N * kArray * 2);
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                if constexpr (!kAhead) fetch(tiles[0], i, dim, [&](int a, int row) { return where(first, a, row); });
-                put(tiles[kAhead ? i : 0], arrays + i * kArray);
+                if constexpr (!kAhead) fetch(i, first);
+                if (!has || rows(i).base == nullptr) continue;
+#pragma unroll
+                for (int e = 0; e < kEach; ++e) {
+                    const Split4 s = split4(tiles[kAhead ? i : 0].v[e]);
+#pragma unroll
+                    for (int p = 0; p < 3; ++p)
+                        *reinterpret_cast<u32x2_t*>(arrays + i * kArray + p * kPiece + (row() + e * kStep) * RS + col()) = s.p[p];
+                }
             }
             if (T::thread() < kStreamRows) {
 #pragma unroll
                 for (int i = 0; i < X; ++i) nums[i * kStreamRows + T::thread()] = numbers[i];
             }
             T::sync();
+            if constexpr (KEYS) {
+                if (__any(nums[threadIdx.x & 31] == minus_inf())) {
+                    for (int i = T::thread(); i < 3 * N * kStreamRows * (RS / 4); i += T::kThreads) {
+                        const int r = i / (RS / 4) % kStreamRows;
+                        if (nums[r] == minus_inf()) reinterpret_cast<u32x2_t*>(arrays)[i] = u32x2_t{};
+                    }
+                    T::sync();
+                }
+            }
             if (first + kStreamRows < hi) request(first + kStreamRows);
             f(first, (const uint16_t*)arrays, (const float*)nums);
         }
     }
+
+    // The keys' side: arrays of the keys' shape.
+    template <class Q, class F, class... A>
+    __device__ __forceinline__ void run_keys(const AttnArgs& a, const Piece& at, int64_t lo, int64_t hi, Q&& number, F&& f,
+                                             const A&... arrays)
+    {
+        const emu_heads_t of[N] = {arrays...};
+        bool even = true;
+#pragma unroll
+        for (int i = 0; i < N; ++i) even = even && fits(of[i].token);
+        run(
+            lo, hi, a.dim, even,
+            [&](int i) {
+                const emu_heads_t& t = of[i];
+                return StreamRows{t.data != nullptr ? key_ptr(t, at.b, at.g, 0) : nullptr, kStreamRows * t.token, kStep * t.token,
+                                  row() * (int)t.token};
+            },
+            [&](int i, int64_t row) { return key_ptr(of[i], at.b, at.g, row); }, number, f);
+    }
+
+    // The rows' side: arrays of the queries' shape.
+    template <class Q, class F, class... A>
+    __device__ __forceinline__ void run_rows(const AttnArgs& a, const Piece& at, int64_t lo, int64_t hi, Q&& number, F&& f,
+                                             const A&... arrays)
+    {
+        const emu_heads_t of[N] = {arrays...};
+        // (a thread's rows are a whole number of queries apart)
+        bool even = a.share <= kStep && kStep % a.share == 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) even = even && fits(of[i].token) && fits(of[i].head);
+        const RowAt mine = row_at(a, 0, row());   // (query and head of a tile's row)
+        run(
+            lo, hi, a.dim, even,
+            [&](int i) {
+                const emu_heads_t& t = of[i];
+                return StreamRows{t.data != nullptr ? row_ptr(t, at.b, RowAt{0, at.g * a.share}) : nullptr,
+                                  kStreamRows / a.share * t.token, kStep / a.share * t.token,
+                                  mine.query * (int)t.token + mine.head * (int)t.head};
+            },
+            [&](int i, int64_t row) { return row_ptr(of[i], at.b, row_at(a, at.g, row)); }, number, f);
+    }
+
+    // 32 strides of tokens and of heads in 32 bits of bytes, none backwards
+    static __device__ __forceinline__ bool fits(int64_t stride) { return stride >= 0 && stride < ((int64_t)1 << 24); }
 };
 
 // Whether any key of a tile of 32 takes no part, and the terms of a lane's keys.
@@ -288,19 +369,16 @@ struct Terms {
     __device__ __forceinline__ bool dead(int t, int j) const { return of[t][j] == minus_inf(); }
 };
 
-// f.template operator()<ND, W, NT>() for a head and plan; WIDE: tiles of 16
-// per wave that the registers hold of heads above 64, as the plan has it.
-template <int WIDE, class F>
+// f.template operator()<ND, W, NT>() for a head and plan.
+template <AttnPass PASS, class F>
 inline void with_shape(int dim, const AttnPlan& p, F&& f)
 {
     const auto tiles = [&]<int ND>() {
-        if constexpr (ND <= 4 || WIDE == 2) {
-            if (p.tiles == 2) {
-                if (p.waves == 1) return f.template operator()<ND, 1, 2>();
-                return f.template operator()<ND, 4, 2>();
-            }
-        }
         if (p.waves == 1) return f.template operator()<ND, 1, 1>();
+        if (p.waves == 2) return f.template operator()<ND, 2, 1>();
+        if constexpr (attn_tiles(PASS, 16 * ND) == 2) {
+            if (p.tiles == 2) return f.template operator()<ND, 4, 2>();
+        }
         return f.template operator()<ND, 4, 1>();
     };
     if (dim <= 16)
