@@ -63,23 +63,14 @@ __global__ __launch_bounds__(64 * W, attn_waves(AttnPass::forward, ND)) void for
             const Terms term(numbers, h);
             f32x4_t s[2][NQ];
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
+            for (int n = 0; n < NQ; ++n) s[0][n] = s[1][n] = f32x4_t{};
+            scores<ND, S::kPiece, NQ>(arrays, m, h, own, s);
 #pragma unroll
-                for (int n = 0; n < NQ; ++n) s[t][n] = f32x4_t{};
-                scores<ND, S::kPiece, NQ>(arrays + 16 * t * S::RS, m, h, own, s[t]);
+            for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int n = 0; n < NQ; ++n)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) s[t][n][j] = __builtin_fmaf(s[t][n][j], a.scale, term.of[t][j]);
-            }
-            if (term.some) {
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int n = 0; n < NQ; ++n)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) s[t][n][j] = term.dead(t, j) ? minus_inf() : s[t][n][j];
-            }
             // The factor's exponent follows the maximum only where that has
             // grown by more than kSlack since: sums and results of up to
             // e^kSlack a key lose nothing in FP32, and most tiles leave the

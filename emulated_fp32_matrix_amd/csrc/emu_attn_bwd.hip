@@ -54,11 +54,11 @@ __global__ __launch_bounds__(64 * W, attn_waves(AttnPass::rows, ND)) void rows_k
             const Terms term(numbers, h);
             f32x4_t s[2][NQ], dp[2][NQ];
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
+            for (int n = 0; n < NQ; ++n) s[0][n] = s[1][n] = dp[0][n] = dp[1][n] = f32x4_t{};
+            scores<ND, S::kPiece, NQ>(arrays, m, h, oq, s);
+            scores<ND, S::kPiece, NQ>(arrays + S::kArray, m, h, od, dp);
 #pragma unroll
-                for (int n = 0; n < NQ; ++n) s[t][n] = dp[t][n] = f32x4_t{};
-                scores<ND, S::kPiece, NQ>(arrays + 16 * t * S::RS, m, h, oq, s[t]);
-                scores<ND, S::kPiece, NQ>(arrays + S::kArray + 16 * t * S::RS, m, h, od, dp[t]);
+            for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int n = 0; n < NQ; ++n)
 #pragma unroll
@@ -66,15 +66,6 @@ __global__ __launch_bounds__(64 * W, attn_waves(AttnPass::rows, ND)) void rows_k
                         const float p = exp_of(__builtin_fmaf(s[t][n][j], a.scale, term.of[t][j]) - top[n]) * over[n];
                         s[t][n][j] = p * (dp[t][n][j] - del[n]);
                     }
-            }
-            if (term.some) {
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int n = 0; n < NQ; ++n)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) s[t][n][j] = term.dead(t, j) ? 0.0f : s[t][n][j];
-            }
             Split8 w[NQ];
 #pragma unroll
             for (int n = 0; n < NQ; ++n) w[n] = split8(s[0][n], s[1][n]);
@@ -140,11 +131,11 @@ __global__ __launch_bounds__(64 * W, attn_waves(AttnPass::keys, ND)) void keys_k
         stream.run_rows(a, at, lo, hi, number, [&](int64_t, const uint16_t* arrays, const float* numbers) {
             f32x4_t s[2][NT], dp[2][NT];
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
+            for (int n = 0; n < NT; ++n) s[0][n] = s[1][n] = dp[0][n] = dp[1][n] = f32x4_t{};
+            scores<ND, S::kPiece, NT>(arrays, m, h, ok, s);
+            scores<ND, S::kPiece, NT>(arrays + S::kArray, m, h, ov, dp);
 #pragma unroll
-                for (int n = 0; n < NT; ++n) s[t][n] = dp[t][n] = f32x4_t{};
-                scores<ND, S::kPiece, NT>(arrays + 16 * t * S::RS, m, h, ok, s[t]);
-                scores<ND, S::kPiece, NT>(arrays + S::kArray + 16 * t * S::RS, m, h, ov, dp[t]);
+            for (int t = 0; t < 2; ++t) {
                 const float* const row = numbers + 16 * t + 4 * h;
                 const f32x4_t top = *reinterpret_cast<const f32x4_t*>(row);
                 const f32x4_t over = *reinterpret_cast<const f32x4_t*>(row + kStreamRows);

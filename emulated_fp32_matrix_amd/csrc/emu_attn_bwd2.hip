@@ -75,34 +75,33 @@ __global__ __launch_bounds__(64 * W, attn_waves(AttnPass::second_rows, ND)) void
                            *const tvv = tvk + S::kArray;
             f32x4_t s[2][NQ], dp[2][NQ], gg[2][NQ], ee[2][NQ];
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const int row = 16 * t * S::RS;
+            for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int n = 0; n < NQ; ++n) s[t][n] = dp[t][n] = gg[t][n] = ee[t][n] = f32x4_t{};
-                scores<ND, S::kPiece, NQ>(tk + row, m, h, oq, s[t]);
-                scores<ND, S::kPiece, NQ>(tk + row, m, h, oa, gg[t]);
-                scores<ND, S::kPiece, NQ>(tvk + row, m, h, oq, gg[t]);
-                scores<ND, S::kPiece, NQ>(tv + row, m, h, od, dp[t]);
-                scores<ND, S::kPiece, NQ>(tvv + row, m, h, od, ee[t]);
+            scores<ND, S::kPiece, NQ>(tk, m, h, oq, s);
+            scores<ND, S::kPiece, NQ>(tk, m, h, oa, gg);
+            scores<ND, S::kPiece, NQ>(tvk, m, h, oq, gg);
+            scores<ND, S::kPiece, NQ>(tv, m, h, od, dp);
+            scores<ND, S::kPiece, NQ>(tvv, m, h, od, ee);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
                 const f32x4_t vadd = *reinterpret_cast<const f32x4_t*>(numbers + kStreamRows + 16 * t + 4 * h);
 #pragma unroll
                 for (int n = 0; n < NQ; ++n)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        float p = exp_of(__builtin_fmaf(s[t][n][j], a.scale, term.of[t][j]) - top[n]) * over[n];
-                        float g = __builtin_fmaf(gg[t][n][j], a.scale, vadd[j]);
-                        float e = ee[t][n][j], dpj = dp[t][n][j];
-                        if (term.some && term.dead(t, j)) p = g = e = dpj = 0.0f;
-                        const float d = dpj - del[n];
-                        const float v = __builtin_fmaf(g, d, e);
+                        const float p = exp_of(__builtin_fmaf(s[t][n][j], a.scale, term.of[t][j]) - top[n]) * over[n];
+                        const float g = __builtin_fmaf(gg[t][n][j], a.scale, vadd[j]);
+                        const float d = dp[t][n][j] - del[n];
+                        const float v = __builtin_fmaf(g, d, ee[t][n][j]);
                         if constexpr (SUMS) {
                             mean[n] = __builtin_fmaf(p, g, mean[n]);
                             tmean[n] = __builtin_fmaf(p, v, tmean[n]);
                         } else {
                             s[t][n][j] = p;
                             gg[t][n][j] = p * (g - mean[n]);
+                            ee[t][n][j] = p * (__builtin_fmaf(-mean[n], dp[t][n][j], v) - tmean[n]);
                             dp[t][n][j] = p * d;
-                            ee[t][n][j] = p * (__builtin_fmaf(-mean[n], dpj, v) - tmean[n]);
                         }
                     }
             }
@@ -200,15 +199,16 @@ __global__ __launch_bounds__(64 * W, attn_waves(AttnPass::second_keys, ND)) void
             const uint16_t *const tq = arrays, *const td = tq + S::kArray, *const ta = td + S::kArray;
             f32x4_t s[2][NT], dp[2][NT], gg[2][NT], ee[2][NT];
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const int row = 16 * t * S::RS;
+            for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int n = 0; n < NT; ++n) s[t][n] = dp[t][n] = gg[t][n] = ee[t][n] = f32x4_t{};
-                scores<ND, S::kPiece, NT>(tq + row, m, h, ok, s[t]);
-                scores<ND, S::kPiece, NT>(ta + row, m, h, ok, gg[t]);
-                scores<ND, S::kPiece, NT>(tq + row, m, h, ovk, gg[t]);
-                scores<ND, S::kPiece, NT>(td + row, m, h, ov, dp[t]);
-                scores<ND, S::kPiece, NT>(td + row, m, h, ovv, ee[t]);
+            scores<ND, S::kPiece, NT>(tq, m, h, ok, s);
+            scores<ND, S::kPiece, NT>(ta, m, h, ok, gg);
+            scores<ND, S::kPiece, NT>(tq, m, h, ovk, gg);
+            scores<ND, S::kPiece, NT>(td, m, h, ov, dp);
+            scores<ND, S::kPiece, NT>(td, m, h, ovv, ee);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
                 const float* const nums = numbers + 16 * t + 4 * h;
                 const f32x4_t top = *reinterpret_cast<const f32x4_t*>(nums);
                 const f32x4_t over = *reinterpret_cast<const f32x4_t*>(nums + kStreamRows);

@@ -39,7 +39,7 @@ constexpr int attn_tiles(AttnPass pass, int dim)
 // each of wide heads does not fit half of them.
 constexpr int attn_waves(AttnPass pass, int nd)
 {
-    return nd >= 5 && (pass == AttnPass::second_rows || pass == AttnPass::second_keys) ? 1 : nd >= 8 && pass == AttnPass::keys ? 1 : 2;
+    return nd >= 8 && (pass == AttnPass::second_rows || pass == AttnPass::second_keys) ? 1 : nd >= 8 && pass == AttnPass::keys ? 1 : 2;
 }
 
 // How a pass is cut into pieces of work: a team of `waves` waves takes

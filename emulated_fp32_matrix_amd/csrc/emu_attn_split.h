@@ -76,15 +76,18 @@ __device__ __forceinline__ f32x4_t mfma32(bf16x8_t a, bf16x8_t b, f32x4_t c)
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
-// acc[n] += a . b[n], the smallest products first.
-template <int NT>
-__device__ __forceinline__ void product6(const bf16x8_t (&a)[3], const Split8* const (&b)[NT], f32x4_t* const (&acc)[NT])
+// acc[k][n] += a[k] . b[n], the smallest products first. K and N together are
+// the independent chains that follow each other on the matrix unit.
+template <int K, int N>
+__device__ __forceinline__ void product6(const bf16x8_t (&a)[K][3], const Split8* const (&b)[N], f32x4_t* const (&acc)[K][N])
 {
     constexpr int ia[6] = {2, 0, 1, 1, 0, 0}, ib[6] = {0, 2, 1, 0, 1, 0};
 #pragma unroll
     for (int i = 0; i < 6; ++i)
 #pragma unroll
-        for (int n = 0; n < NT; ++n) *acc[n] = mfma32(a[ia[i]], b[n]->p[ib[i]], *acc[n]);
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int n = 0; n < N; ++n) *acc[k][n] = mfma32(a[k][ia[i]], b[n]->p[ib[i]], *acc[k][n]);
 }
 
 // ND tiles of 16 cover a head; scores take KS steps of 32 of it. A tile in LDS
@@ -105,24 +108,30 @@ __device__ __forceinline__ void load_own(Split8 (&f)[Heads<ND>::KS], const float
                      : split8(f32x4_t{}, f32x4_t{});
 }
 
-// acc[n] += (the 16 streamed rows at `tile`) . own[n]; PS: elements of a piece
+// acc[t][n] += (streamed rows 16 t .. of `tile`) . own[n]; PS: elements of a
+// piece
 template <int ND, int PS, int NT>
 __device__ __forceinline__ void scores(const uint16_t* tile, int m, int h, const Split8 (&own)[NT][Heads<ND>::KS],
-                                       f32x4_t (&acc)[NT])
+                                       f32x4_t (&acc)[2][NT])
 {
-    const uint16_t* const at = tile + m * Heads<ND>::RS + 8 * h;
-    f32x4_t* to[NT];
+    constexpr int RS = Heads<ND>::RS;
+    const uint16_t* const at = tile + m * RS + 8 * h;
+    f32x4_t* to[2][NT];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) to[n] = &acc[n];
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) to[t][n] = &acc[t][n];
 #pragma unroll
     for (int c = 0; c < Heads<ND>::KS; ++c) {
-        bf16x8_t a[3];
+        bf16x8_t a[2][3];
         const Split8* b[NT];
 #pragma unroll
-        for (int i = 0; i < 3; ++i) a[i] = *reinterpret_cast<const bf16x8_t*>(at + i * PS + 32 * c);
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int i = 0; i < 3; ++i) a[t][i] = *reinterpret_cast<const bf16x8_t*>(at + i * PS + 16 * t * RS + 32 * c);
 #pragma unroll
         for (int n = 0; n < NT; ++n) b[n] = &own[n][c];
-        product6<NT>(a, b, to);
+        product6<2, NT>(a, b, to);
     }
 }
 
@@ -131,24 +140,38 @@ template <int ND, int PS, int NT>
 __device__ __forceinline__ void results(const uint16_t* tile, int m, int h, const Split8 (&w)[NT], f32x4_t (&acc)[NT][ND])
 {
     typedef __attribute__((address_space(3))) i16x4_t lds_t;
-    constexpr int RS = Heads<ND>::RS;
+    constexpr int RS = Heads<ND>::RS, PAIRS = ND / 2;
     const uint16_t* const at = tile + (4 * h + (m >> 2)) * RS + 4 * (m & 3);
     const Split8* b[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) b[n] = &w[n];
-#pragma unroll
-    for (int t = 0; t < ND; ++t) {
-        bf16x8_t a[3];
-        f32x4_t* to[NT];
+    const auto load = [&](int t, bf16x8_t (&a)[3]) {
 #pragma unroll
         for (int i = 0; i < 3; ++i) {
             const i16x4_t u = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t*)(at + i * PS + 16 * t));
             const i16x4_t v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t*)(at + i * PS + 16 * RS + 16 * t));
             a[i] = __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(u, v, 0, 1, 2, 3, 4, 5, 6, 7));
         }
+    };
 #pragma unroll
-        for (int n = 0; n < NT; ++n) to[n] = &acc[n][t];
-        product6<NT>(a, b, to);
+    for (int p = 0; p < PAIRS; ++p) {
+        bf16x8_t a[2][3];
+        f32x4_t* to[2][NT];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            load(2 * p + t, a[t]);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) to[t][n] = &acc[n][2 * p + t];
+        }
+        product6<2, NT>(a, b, to);
+    }
+    if constexpr (ND % 2 == 1) {
+        bf16x8_t a[1][3];
+        f32x4_t* to[1][NT];
+        load(ND - 1, a[0]);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) to[0][n] = &acc[n][ND - 1];
+        product6<1, NT>(a, b, to);
     }
 }
 
@@ -208,7 +231,7 @@ struct Stream {
     static constexpr int kQuads = Heads<ND>::KS == 3 ? 32 : 8 * Heads<ND>::KS, kStep = T::kThreads / kQuads < kStreamRows ? T::kThreads / kQuads : kStreamRows;
     static constexpr int kEach = kStreamRows / kStep;
     static constexpr int kBytes = N * kArray * 2 + X * kStreamRows * 4;
-    static constexpr bool kAhead = N * kEach <= 16;
+    static constexpr bool kAhead = N * kEach <= 8;
     static constexpr int kBuffers = W > 1 && kAhead && 2 * kBytes <= 80 * 1024 ? 2 : 1;
     static_assert(kBytes % 16 == 0, "buffers stay aligned");
 
@@ -236,17 +259,21 @@ struct Stream {
     // rows(i): array i's StreamRows; even: they hold for whole tiles (else,
     // and in the last, cut tile, where(i, row) is the row's address).
     // number(first, numbers): those of row first + thread, < 32.
-    // KEYS: number 0 is a key's term; what is loaded of keys that take no part
-    // is dropped again.
-    template <class R, class P, class Q, class F>
-    __device__ __forceinline__ void run(int64_t lo, int64_t hi, int dim, bool even, R&& rows, P&& where, Q&& number, F&& f)
+    // KEYS: number 0 is a key's term; keys that take no part (dropped(row), if
+    // some are) are zeros, and a tile of such keys alone is left out. (The
+    // others' scores of a row are then finite plus -infinity, or as little as
+    // the row's own infinities leave of any score.)
+    template <class R, class P, class D, class Q, class F>
+    __device__ __forceinline__ void run(int64_t lo, int64_t hi, int dim, bool even, R&& rows, P&& where, bool some,
+                                        D&& dropped, Q&& number, F&& f)
     {
-        Tile tiles[kAhead ? N : 1];
+        Tile tiles[N];
         float numbers[X];
+        uint32_t drop = 0;   // bit e: the thread's row e
         even = even && dim % 4 == 0;
         const bool has = col() < dim;
         const auto fetch = [&](int i, int64_t first) {
-            Tile& t = tiles[kAhead ? i : 0];
+            Tile& t = tiles[i];
             const StreamRows r = rows(i);
             if (even && first + kStreamRows <= hi) {
                 if (r.base == nullptr || !has) return;   // (zeros since clear())
@@ -254,11 +281,18 @@ struct Stream {
                 const uint32_t at = (uint32_t)(r.offset + col()) * 4u;
 #pragma unroll
                 for (int e = 0; e < kEach; ++e) t.v[e] = *reinterpret_cast<const f32x4u_t*>(from + e * r.step * 4 + at);
-            } else {
+            } else if (r.base != nullptr) {
+                // (float by float, clamped to what is there)
 #pragma unroll
                 for (int e = 0; e < kEach; ++e) {
                     const int64_t at = first + row() + e * kStep;
-                    t.v[e] = has && at < hi && r.base != nullptr ? load4(where(i, at), col(), dim) : f32x4_t{};
+                    const float* const p = where(i, at < hi ? at : hi - 1);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const bool there = at < hi && col() + x < dim;
+                        const float y = p[col() + x < dim ? col() + x : dim - 1];
+                        t.v[e][x] = there ? y : 0.0f;
+                    }
                 }
             }
         };
@@ -268,41 +302,52 @@ struct Stream {
                 for (int i = 0; i < N; ++i) fetch(i, first);
             }
             if (T::thread() < kStreamRows) number(first, numbers);
+            if (KEYS && some) {
+                drop = 0;
+#pragma unroll
+                for (int e = 0; e < kEach; ++e) drop |= dropped(first + row() + e * kStep) ? 1u << e : 0u;
+            }
         };
-        if (lo < hi) request(lo);
-        for (int64_t first = lo; first < hi; first += kStreamRows) {
-            if (kBuffers == 1) T::sync();   // the previous tile has been read
-            char* const buffer = base + (kBuffers == 2 ? (turn ^= 1) * kBytes : 0);
-            uint16_t* const arrays = reinterpret_cast<uint16_t*>(buffer);
-            float* const nums = reinterpret_cast<float*>(buffer + N * kArray * 2);
+        // (the first turn only requests)
+        for (int64_t first = lo - kStreamRows; first < hi; first += kStreamRows) {
+            const bool here = first >= lo;
+            char* buffer = base;
+            if (here) {
+                if (kBuffers == 1) T::sync();   // the previous tile has been read
+                if (kBuffers == 2) buffer += (turn ^= 1) * kBytes;
+                uint16_t* const arrays = reinterpret_cast<uint16_t*>(buffer);
+                if constexpr (!kAhead) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                if constexpr (!kAhead) fetch(i, first);
-                if (!has || rows(i).base == nullptr) continue;
-#pragma unroll
-                for (int e = 0; e < kEach; ++e) {
-                    const Split4 s = split4(tiles[kAhead ? i : 0].v[e]);
-#pragma unroll
-                    for (int p = 0; p < 3; ++p)
-                        *reinterpret_cast<u32x2_t*>(arrays + i * kArray + p * kPiece + (row() + e * kStep) * RS + col()) = s.p[p];
+                    for (int i = 0; i < N; ++i) fetch(i, first);
                 }
-            }
-            if (T::thread() < kStreamRows) {
 #pragma unroll
-                for (int i = 0; i < X; ++i) nums[i * kStreamRows + T::thread()] = numbers[i];
-            }
-            T::sync();
-            if constexpr (KEYS) {
-                if (__any(nums[threadIdx.x & 31] == minus_inf())) {
-                    for (int i = T::thread(); i < 3 * N * kStreamRows * (RS / 4); i += T::kThreads) {
-                        const int r = i / (RS / 4) % kStreamRows;
-                        if (nums[r] == minus_inf()) reinterpret_cast<u32x2_t*>(arrays)[i] = u32x2_t{};
+                for (int i = 0; i < N; ++i) {
+                    if (!has || rows(i).base == nullptr) continue;
+                    if (KEYS && some && __any(drop != 0)) {
+#pragma unroll
+                        for (int e = 0; e < kEach; ++e)
+                            if (drop >> e & 1) tiles[i].v[e] = f32x4_t{};
                     }
-                    T::sync();
+#pragma unroll
+                    for (int e = 0; e < kEach; ++e) {
+                        const Split4 s = split4(tiles[i].v[e]);
+#pragma unroll
+                        for (int p = 0; p < 3; ++p)
+                            *reinterpret_cast<u32x2_t*>(arrays + i * kArray + p * kPiece + (row() + e * kStep) * RS + col()) = s.p[p];
+                    }
                 }
+                if (T::thread() < kStreamRows) {
+                    float* const nums = reinterpret_cast<float*>(buffer + N * kArray * 2);
+#pragma unroll
+                    for (int i = 0; i < X; ++i) nums[i * kStreamRows + T::thread()] = numbers[i];
+                }
+                T::sync();
             }
             if (first + kStreamRows < hi) request(first + kStreamRows);
-            f(first, (const uint16_t*)arrays, (const float*)nums);
+            const float* const nums = reinterpret_cast<const float*>(buffer + N * kArray * 2);
+            // (a tile of keys that take no part adds nothing, whatever the rows hold)
+            if (here && !(KEYS && some && __all(nums[threadIdx.x & 31] == minus_inf())))
+                f(first, reinterpret_cast<const uint16_t*>(buffer), nums);
         }
     }
 
@@ -322,7 +367,8 @@ struct Stream {
                 return StreamRows{t.data != nullptr ? key_ptr(t, at.b, at.g, 0) : nullptr, kStreamRows * t.token, kStep * t.token,
                                   row() * (int)t.token};
             },
-            [&](int i, int64_t row) { return key_ptr(of[i], at.b, at.g, row); }, number, f);
+            [&](int i, int64_t row) { return key_ptr(of[i], at.b, at.g, row); }, a.bias != nullptr || a.mask != nullptr,
+            [&](int64_t row) { return key_term(a, at.b, (int)row, (int)hi) == minus_inf(); }, number, f);
     }
 
     // The rows' side: arrays of the queries' shape.
@@ -344,29 +390,23 @@ struct Stream {
                                   kStreamRows / a.share * t.token, kStep / a.share * t.token,
                                   mine.query * (int)t.token + mine.head * (int)t.head};
             },
-            [&](int i, int64_t row) { return row_ptr(of[i], at.b, row_at(a, at.g, row)); }, number, f);
+            [&](int i, int64_t row) { return row_ptr(of[i], at.b, row_at(a, at.g, row)); }, false,
+            [](int64_t) { return false; }, number, f);
     }
 
     // 32 strides of tokens and of heads in 32 bits of bytes, none backwards
     static __device__ __forceinline__ bool fits(int64_t stride) { return stride >= 0 && stride < ((int64_t)1 << 24); }
 };
 
-// Whether any key of a tile of 32 takes no part, and the terms of a lane's keys.
+// The terms of a lane's keys: 0 .. 3 of the first 16 at its group, then of the
+// second.
 struct Terms {
     f32x4_t of[2];
-    bool some;
     __device__ __forceinline__ Terms(const float* term, int h)
     {
         of[0] = *reinterpret_cast<const f32x4_t*>(term + 4 * h);
         of[1] = *reinterpret_cast<const f32x4_t*>(term + 16 + 4 * h);
-        bool any = false;
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) any = any || of[t][j] == minus_inf();
-        some = __any(any) != 0;
     }
-    __device__ __forceinline__ bool dead(int t, int j) const { return of[t][j] == minus_inf(); }
 };
 
 // f.template operator()<ND, W, NT>() for a head and plan.
