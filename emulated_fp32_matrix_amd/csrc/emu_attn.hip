@@ -14,6 +14,7 @@ namespace emu {
 namespace {
 
 constexpr int kMostSplits = 64;
+constexpr int kImageTeams = 2;   // teams that stream the same side, from which on it is split beforehand
 constexpr float kSlack = 4.0f;
 
 // Partial results of a split: rows' results, then their maxima and sums.
@@ -27,12 +28,13 @@ __host__ __device__ __forceinline__ ForwardPartial forward_partial(const AttnArg
     return {at + 2 * p.splits * n, at};
 }
 
-template <int ND, int W, int NQ>
+template <int ND, int W, int NQ, bool IMAGES>
 __global__ __launch_bounds__(64 * W, attn_waves(AttnPass::forward, ND)) void forward_kernel(AttnArgs a, AttnPlan plan, emu_heads_t q, emu_heads_t k,
-                                                         emu_heads_t v, float* out, float* stats, float* partial)
+                                                         emu_heads_t v, const char* images, float* out, float* stats,
+                                                         float* partial)
 {
     using T = Team<W>;
-    using S = Stream<ND, W, 2, 1, true>;
+    using S = Stream<ND, W, 2, 1, true, IMAGES>;
     __shared__ __attribute__((aligned(16))) char lds[S::kBuffers * S::kBytes];
     S stream{lds};
     stream.clear();
@@ -59,7 +61,7 @@ __global__ __launch_bounds__(64 * W, attn_waves(AttnPass::forward, ND)) void for
         clear(acc);
 
         const auto number = [&](int64_t first, float* to) { to[0] = key_term(a, at.b, (int)first + T::thread(), limit); };
-        stream.run_keys(a, at, lo, hi, number, [&](int64_t, const uint16_t* arrays, const float* numbers) {
+        stream.run_keys(a, at, images, lo, hi, number, [&](int64_t, const uint16_t* arrays, const float* numbers) {
             const Terms term(numbers, h);
             f32x4_t s[2][NQ];
 #pragma unroll
@@ -221,6 +223,7 @@ AttnPlan attn_plan(const AttnArgs& a, AttnPass pass)
     p.tiles = own <= 64 ? 1 : attn_tiles(pass, a.dim);
     const int64_t each = p.waves * p.tiles * 16;
     p.own = (own + each - 1) / each;
+    p.images = p.waves == 4 && p.own >= kImageTeams;
     p.splits = splits_for((int64_t)a.batch * a.kv_heads * p.own * p.waves, other, p.waves == 1 ? 128 : 256);
     return p;
 }
@@ -243,11 +246,12 @@ size_t attn_bias_partial(const AttnArgs& a, const AttnPlan& p)
 }
 
 hipError_t launch_attn_forward(const AttnArgs& a, const AttnPlan& p, emu_heads_t q, emu_heads_t k, emu_heads_t v,
-                               float* out, float* stats, float* partial, hipStream_t s)
+                               const void* images, float* out, float* stats, float* partial, hipStream_t s)
 {
-    with_shape<AttnPass::forward>(a.dim, p, [&]<int ND, int W, int NQ>() {
+    with_shape<AttnPass::forward>(a.dim, p, [&]<int ND, int W, int NQ, bool IMAGES>() {
         const int64_t n = (int64_t)a.batch * a.kv_heads * p.own * p.splits;
-        forward_kernel<ND, W, NQ><<<Team<W>::grid(n), 64 * W, 0, s>>>(a, p, q, k, v, out, stats, partial);
+        forward_kernel<ND, W, NQ, IMAGES><<<Team<W>::grid(n), 64 * W, 0, s>>>(a, p, q, k, v, static_cast<const char*>(images), out,
+                                                                                stats, partial);
     });
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1) return e;

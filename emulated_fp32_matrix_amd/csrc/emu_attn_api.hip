@@ -89,20 +89,34 @@ struct Layout {
 
 size_t rows_of(const AttnArgs& a) { return (size_t)a.batch * a.queries * a.heads; }
 
+struct ForwardSpace {
+    AttnPlan plan;
+    float* partial;
+    void* images;
+    size_t bytes;
+    ForwardSpace(const AttnArgs& a, void* ws) : plan(emu::attn_plan(a, emu::AttnPass::forward))
+    {
+        Layout l(ws);
+        partial = l.take(emu::attn_forward_partial(a, plan));
+        images = plan.images ? l.take(emu::attn_key_images(a, 2) / sizeof(float)) : nullptr;
+        bytes = l.bytes;
+    }
+};
 size_t forward_bytes(const AttnArgs& a)
 {
-    if (!has_rows(a) || emu::attn_whole(a, 0)) return 0;
-    return round256(emu::attn_forward_partial(a, emu::attn_plan(a, emu::AttnPass::forward)) * sizeof(float));
+    return !has_rows(a) || emu::attn_whole(a, 0) ? 0 : ForwardSpace(a, nullptr).bytes;
 }
 
 struct BackwardSpace {
     AttnPlan rows, keys;
     float *delta, *dq, *dk, *dv, *db;
+    void *key_images, *row_images;
     size_t bytes;
     BackwardSpace(const AttnArgs& a, void* ws) : rows(emu::attn_plan(a, emu::AttnPass::rows)), keys(emu::attn_plan(a, emu::AttnPass::keys))
     {
         Layout l(ws);
         delta = dq = dk = dv = db = nullptr;
+        key_images = row_images = nullptr;
         if (emu::attn_whole(a, 1)) {
             db = l.take(emu::attn_whole_partial(a));
             bytes = l.bytes;
@@ -113,6 +127,8 @@ struct BackwardSpace {
         dk = l.take(emu::attn_keys_partial(a, keys));
         dv = l.take(emu::attn_keys_partial(a, keys));
         db = l.take(emu::attn_bias_partial(a, keys));
+        if (rows.images) key_images = l.take(emu::attn_key_images(a, 2) / sizeof(float));
+        if (keys.images) row_images = l.take(emu::attn_row_images(a, 2) / sizeof(float));
         bytes = l.bytes;
     }
 };
@@ -120,11 +136,13 @@ struct BackwardSpace {
 struct SecondSpace {
     AttnPlan rows, keys;
     float *delta, *sums, *go, *gq, *gk, *gv, *gb;
+    void *key_images, *row_images;
     size_t bytes;
     SecondSpace(const AttnArgs& a, void* ws) : rows(emu::attn_plan(a, emu::AttnPass::second_rows)), keys(emu::attn_plan(a, emu::AttnPass::second_keys))
     {
         Layout l(ws);
         delta = sums = go = gq = gk = gv = gb = nullptr;
+        key_images = row_images = nullptr;
         if (emu::attn_whole(a, 2)) {
             gb = l.take(emu::attn_whole_partial(a));
             bytes = l.bytes;
@@ -137,6 +155,8 @@ struct SecondSpace {
         gk = l.take(emu::attn_keys_partial(a, keys));
         gv = l.take(emu::attn_keys_partial(a, keys));
         gb = l.take(emu::attn_bias_partial(a, keys));
+        if (rows.images) key_images = l.take(emu::attn_key_images(a, 4) / sizeof(float));
+        if (keys.images) row_images = l.take(emu::attn_row_images(a, 3) / sizeof(float));
         bytes = l.bytes;
     }
 };
@@ -186,7 +206,11 @@ emu_status_t emu_cross_attention(const emu_attention_t* in, emu_heads_t q, emu_h
     if (bad_workspace(workspace, workspace_bytes, forward_bytes(a))) return EMU_STATUS_INVALID_VALUE;
     if (!on_gfx950()) return EMU_STATUS_NOT_SUPPORTED;
     if (emu::attn_whole(a, 0)) return from_hip(emu::launch_whole_forward(a, q, k, v, out, stats, stream_of(stream)));
-    return from_hip(emu::launch_attn_forward(a, emu::attn_plan(a, emu::AttnPass::forward), q, k, v, out, stats, static_cast<float*>(workspace), stream_of(stream)));
+    const ForwardSpace w(a, workspace);
+    const emu_heads_t keys[] = {k, v};
+    hipError_t e = w.plan.images ? emu::launch_attn_images(a, 2, keys, w.images, 0, nullptr, nullptr, stream_of(stream)) : hipSuccess;
+    if (e == hipSuccess) e = emu::launch_attn_forward(a, w.plan, q, k, v, w.images, out, stats, w.partial, stream_of(stream));
+    return from_hip(e);
 }
 
 emu_status_t emu_cross_attention_backward_workspace(const emu_attention_t* in, size_t* bytes)
@@ -220,9 +244,13 @@ emu_status_t emu_cross_attention_backward(const emu_attention_t* in, emu_heads_t
     const BackwardSpace w(a, workspace);
     if (emu::attn_whole(a, 1))
         return from_hip(emu::launch_whole_backward(a, dout, q, k, v, stats, dq, dk, dv, dbias, w.db, s));
-    hipError_t e = emu::launch_attn_backward_rows(a, w.rows, dout, q, k, v, out, stats, w.delta, dq, w.dq, s);
+    const emu_heads_t key_side[] = {k, v}, row_side[] = {q, dout};
+    hipError_t e = emu::launch_attn_images(a, w.rows.images && dq != nullptr ? 2 : 0, key_side, w.key_images,
+                                           w.keys.images && keys_wanted ? 2 : 0, row_side, w.row_images, s);
+    if (e == hipSuccess)
+        e = emu::launch_attn_backward_rows(a, w.rows, dout, q, k, v, out, stats, w.key_images, w.delta, dq, w.dq, s);
     if (e == hipSuccess && keys_wanted)
-        e = emu::launch_attn_backward_keys(a, w.keys, dout, q, k, v, stats, w.delta, dk, dv, dbias, w.dk, w.dv, w.db, s);
+        e = emu::launch_attn_backward_keys(a, w.keys, dout, q, k, v, w.row_images, stats, w.delta, dk, dv, dbias, w.dk, w.dv, w.db, s);
     return from_hip(e);
 }
 
@@ -260,11 +288,14 @@ emu_status_t emu_cross_attention_backward2(const emu_attention_t* in, emu_heads_
     const SecondSpace w(a, workspace);
     const emu::AttnSeconds x{vq, vk, vv, vbias, vbias_batch, vbias_key, dout, q, k, v, out, stats};
     if (emu::attn_whole(a, 2)) return from_hip(emu::launch_whole_second(a, x, gdout, gq, gk, gv, gbias, w.gb, s));
-    hipError_t e = emu::launch_attn_second_sums(a, w.rows, x, w.delta, w.sums, s);
+    const emu_heads_t key_side[] = {k, v, vk, vv}, row_side[] = {q, dout, vq};
+    hipError_t e = emu::launch_attn_images(a, w.rows.images ? 4 : 0, key_side, w.key_images,
+                                           w.keys.images && keys_wanted ? 3 : 0, row_side, w.row_images, s);
+    if (e == hipSuccess) e = emu::launch_attn_second_sums(a, w.rows, x, w.key_images, w.delta, w.sums, s);
     if (e == hipSuccess && rows_wanted)
-        e = emu::launch_attn_second_rows(a, w.rows, x, w.delta, w.sums, gdout, gq, w.go, w.gq, s);
+        e = emu::launch_attn_second_rows(a, w.rows, x, w.key_images, w.delta, w.sums, gdout, gq, w.go, w.gq, s);
     if (e == hipSuccess && keys_wanted)
-        e = emu::launch_attn_second_keys(a, w.keys, x, w.delta, w.sums, w.rows.splits, gk, gv, gbias, w.gk, w.gv, w.gb, s);
+        e = emu::launch_attn_second_keys(a, w.keys, x, w.row_images, w.delta, w.sums, w.rows.splits, gk, gv, gbias, w.gk, w.gv, w.gb, s);
     return from_hip(e);
 }
 

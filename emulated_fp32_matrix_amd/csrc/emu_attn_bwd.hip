@@ -11,13 +11,13 @@
 namespace emu {
 namespace {
 
-template <int ND, int W, int NQ>
+template <int ND, int W, int NQ, bool IMAGES>
 __global__ __launch_bounds__(64 * W, attn_waves(AttnPass::rows, ND)) void rows_kernel(AttnArgs a, AttnPlan plan, emu_heads_t dout, emu_heads_t q,
-                                                      emu_heads_t k, emu_heads_t v, const float* out, const float* stats,
-                                                      float* delta, float* dq, float* partial)
+                                                      emu_heads_t k, emu_heads_t v, const char* images, const float* out,
+                                                      const float* stats, float* delta, float* dq, float* partial)
 {
     using T = Team<W>;
-    using S = Stream<ND, W, 2, 1, true>;
+    using S = Stream<ND, W, 2, 1, true, IMAGES>;
     __shared__ __attribute__((aligned(16))) char lds[S::kBuffers * S::kBytes];
     S stream{lds};
     stream.clear();
@@ -49,7 +49,7 @@ __global__ __launch_bounds__(64 * W, attn_waves(AttnPass::rows, ND)) void rows_k
         clear(acc);
 
         const auto number = [&](int64_t first, float* to) { to[0] = key_term(a, at.b, (int)first + T::thread(), limit); };
-        stream.run_keys(a, at, lo, dq != nullptr ? hi : lo, number,
+        stream.run_keys(a, at, images, lo, dq != nullptr ? hi : lo, number,
                         [&](int64_t, const uint16_t* arrays, const float* numbers) {
             const Terms term(numbers, h);
             f32x4_t s[2][NQ], dp[2][NQ];
@@ -84,13 +84,13 @@ __global__ __launch_bounds__(64 * W, attn_waves(AttnPass::rows, ND)) void rows_k
     });
 }
 
-template <int ND, int W, int NT>
+template <int ND, int W, int NT, bool IMAGES>
 __global__ __launch_bounds__(64 * W, attn_waves(AttnPass::keys, ND)) void keys_kernel(AttnArgs a, AttnPlan plan, emu_heads_t dout, emu_heads_t q,
-                                                      emu_heads_t k, emu_heads_t v, const float* stats,
-                                                      const float* delta, float* dk, float* dv, float* db)
+                                                      emu_heads_t k, emu_heads_t v, const char* images,
+                                                      const float* stats, const float* delta, float* dk, float* dv, float* db)
 {
     using T = Team<W>;
-    using S = Stream<ND, W, 2, 3, false>;
+    using S = Stream<ND, W, 2, 3, false, IMAGES>;
     __shared__ __attribute__((aligned(16))) char lds[S::kBuffers * S::kBytes];
     S stream{lds};
     stream.clear();
@@ -128,7 +128,7 @@ __global__ __launch_bounds__(64 * W, attn_waves(AttnPass::keys, ND)) void keys_k
             to[1] = valid ? stats[2 * row + 1] : 0.0f;
             to[2] = valid ? delta[row] : 0.0f;
         };
-        stream.run_rows(a, at, lo, hi, number, [&](int64_t, const uint16_t* arrays, const float* numbers) {
+        stream.run_rows(a, at, images, lo, hi, number, [&](int64_t, const uint16_t* arrays, const float* numbers) {
             f32x4_t s[2][NT], dp[2][NT];
 #pragma unroll
             for (int n = 0; n < NT; ++n) s[0][n] = s[1][n] = dp[0][n] = dp[1][n] = f32x4_t{};
@@ -183,11 +183,11 @@ __global__ __launch_bounds__(64 * W, attn_waves(AttnPass::keys, ND)) void keys_k
 
 hipError_t launch_attn_backward_rows(const AttnArgs& a, const AttnPlan& p, emu_heads_t dout, emu_heads_t q,
                                      emu_heads_t k, emu_heads_t v, const float* out, const float* stats,
-                                     float* delta, float* dq, float* partial, hipStream_t s)
+                                     const void* images, float* delta, float* dq, float* partial, hipStream_t s)
 {
-    with_shape<AttnPass::rows>(a.dim, p, [&]<int ND, int W, int NQ>() {
+    with_shape<AttnPass::rows>(a.dim, p, [&]<int ND, int W, int NQ, bool IMAGES>() {
         const int64_t n = (int64_t)a.batch * a.kv_heads * p.own * p.splits;
-        rows_kernel<ND, W, NQ><<<Team<W>::grid(n), 64 * W, 0, s>>>(a, p, dout, q, k, v, out, stats, delta, dq, partial);
+        rows_kernel<ND, W, NQ, IMAGES><<<Team<W>::grid(n), 64 * W, 0, s>>>(a, p, dout, q, k, v, static_cast<const char*>(images), out, stats, delta, dq, partial);
     });
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && p.splits > 1 && dq != nullptr)
@@ -196,17 +196,17 @@ hipError_t launch_attn_backward_rows(const AttnArgs& a, const AttnPlan& p, emu_h
 }
 
 hipError_t launch_attn_backward_keys(const AttnArgs& a, const AttnPlan& p, emu_heads_t dout, emu_heads_t q,
-                                     emu_heads_t k, emu_heads_t v, const float* stats, const float* delta,
-                                     float* dk, float* dv, float* dbias, float* partial_k, float* partial_v,
+                                     emu_heads_t k, emu_heads_t v, const void* images, const float* stats,
+                                     const float* delta, float* dk, float* dv, float* dbias, float* partial_k, float* partial_v,
                                      float* partial_b, hipStream_t s)
 {
     const bool cut = p.splits > 1, join_bias = dbias != nullptr && (cut || a.kv_heads > 1);
     float* const to_k = dk != nullptr && cut ? partial_k : dk;
     float* const to_v = dv != nullptr && cut ? partial_v : dv;
     float* const to_b = join_bias ? partial_b : dbias;
-    with_shape<AttnPass::keys>(a.dim, p, [&]<int ND, int W, int NT>() {
+    with_shape<AttnPass::keys>(a.dim, p, [&]<int ND, int W, int NT, bool IMAGES>() {
         const int64_t n = (int64_t)a.batch * a.kv_heads * p.own * p.splits;
-        keys_kernel<ND, W, NT><<<Team<W>::grid(n), 64 * W, 0, s>>>(a, p, dout, q, k, v, stats, delta, to_k, to_v, to_b);
+        keys_kernel<ND, W, NT, IMAGES><<<Team<W>::grid(n), 64 * W, 0, s>>>(a, p, dout, q, k, v, static_cast<const char*>(images), stats, delta, to_k, to_v, to_b);
     });
     hipError_t e = hipGetLastError();
     const int64_t n = (int64_t)a.batch * a.keys * a.kv_heads * a.dim;

@@ -14,12 +14,12 @@
 namespace emu {
 namespace {
 
-template <int ND, int W, int NQ, bool SUMS>
-__global__ __launch_bounds__(64 * W, attn_waves(AttnPass::second_rows, ND)) void rows_kernel(AttnArgs a, AttnPlan plan, AttnSeconds x, float* delta, float* sums,
+template <int ND, int W, int NQ, bool IMAGES, bool SUMS>
+__global__ __launch_bounds__(64 * W, attn_waves(AttnPass::second_rows, ND)) void rows_kernel(AttnArgs a, AttnPlan plan, AttnSeconds x, const char* images, float* delta, float* sums,
                                                       float* go, float* gq)
 {
     using T = Team<W>;
-    using S = Stream<ND, W, 4, 2, true>;
+    using S = Stream<ND, W, 4, 2, true, IMAGES>;
     constexpr int KS = Heads<ND>::KS;
     __shared__ __attribute__((aligned(16))) char lds[S::kBuffers * S::kBytes];
     S stream{lds};
@@ -69,7 +69,7 @@ __global__ __launch_bounds__(64 * W, attn_waves(AttnPass::second_rows, ND)) void
             to[1] = x.vbias != nullptr && to[0] != minus_inf() ? x.vbias[at.b * x.vbias_b + (first + T::thread()) * x.vbias_k]
                                                                : 0.0f;
         };
-        stream.run_keys(a, at, lo, hi, number, [&](int64_t, const uint16_t* arrays, const float* numbers) {
+        stream.run_keys(a, at, images, lo, hi, number, [&](int64_t, const uint16_t* arrays, const float* numbers) {
             const Terms term(numbers, h);
             const uint16_t *const tk = arrays, *const tv = tk + S::kArray, *const tvk = tv + S::kArray,
                            *const tvv = tvk + S::kArray;
@@ -139,12 +139,12 @@ __global__ __launch_bounds__(64 * W, attn_waves(AttnPass::second_rows, ND)) void
     });
 }
 
-template <int ND, int W, int NT>
-__global__ __launch_bounds__(64 * W, attn_waves(AttnPass::second_keys, ND)) void keys_kernel(AttnArgs a, AttnPlan plan, AttnSeconds x, const float* delta,
+template <int ND, int W, int NT, bool IMAGES>
+__global__ __launch_bounds__(64 * W, attn_waves(AttnPass::second_keys, ND)) void keys_kernel(AttnArgs a, AttnPlan plan, AttnSeconds x, const char* images, const float* delta,
                                                       const float* sums, int sum_splits, float* gk, float* gv, float* gb)
 {
     using T = Team<W>;
-    using S = Stream<ND, W, 3, 5, false>;
+    using S = Stream<ND, W, 3, 5, false, IMAGES>;
     constexpr int KS = Heads<ND>::KS;
     __shared__ __attribute__((aligned(16))) char lds[S::kBuffers * S::kBytes];
     S stream{lds};
@@ -195,7 +195,7 @@ __global__ __launch_bounds__(64 * W, attn_waves(AttnPass::second_keys, ND)) void
             to[3] = g;
             to[4] = __builtin_fmaf(-g, to[2], t);
         };
-        stream.run_rows(a, at, lo, hi, number, [&](int64_t, const uint16_t* arrays, const float* numbers) {
+        stream.run_rows(a, at, images, lo, hi, number, [&](int64_t, const uint16_t* arrays, const float* numbers) {
             const uint16_t *const tq = arrays, *const td = tq + S::kArray, *const ta = td + S::kArray;
             f32x4_t s[2][NT], dp[2][NT], gg[2][NT], ee[2][NT];
 #pragma unroll
@@ -264,25 +264,25 @@ int64_t pieces(const AttnArgs& a, const AttnPlan& p) { return (int64_t)a.batch *
 
 }  // namespace
 
-hipError_t launch_attn_second_sums(const AttnArgs& a, const AttnPlan& p, const AttnSeconds& x, float* delta,
-                                   float* sums, hipStream_t s)
+hipError_t launch_attn_second_sums(const AttnArgs& a, const AttnPlan& p, const AttnSeconds& x, const void* images,
+                                   float* delta, float* sums, hipStream_t s)
 {
-    with_shape<AttnPass::second_rows>(a.dim, p, [&]<int ND, int W, int NQ>() {
-        rows_kernel<ND, W, NQ, true><<<Team<W>::grid(pieces(a, p)), 64 * W, 0, s>>>(a, p, x, delta, sums, nullptr, nullptr);
+    with_shape<AttnPass::second_rows>(a.dim, p, [&]<int ND, int W, int NQ, bool IMAGES>() {
+        rows_kernel<ND, W, NQ, IMAGES, true><<<Team<W>::grid(pieces(a, p)), 64 * W, 0, s>>>(a, p, x, static_cast<const char*>(images), delta, sums, nullptr, nullptr);
     });
     return hipGetLastError();
 }
 
-hipError_t launch_attn_second_rows(const AttnArgs& a, const AttnPlan& p, const AttnSeconds& x, const float* delta,
+hipError_t launch_attn_second_rows(const AttnArgs& a, const AttnPlan& p, const AttnSeconds& x, const void* images, const float* delta,
                                    const float* sums, float* gdout, float* gq, float* partial_o, float* partial_q,
                                    hipStream_t s)
 {
     const bool cut = p.splits > 1;
     float* const to_o = gdout != nullptr && cut ? partial_o : gdout;
     float* const to_q = gq != nullptr && cut ? partial_q : gq;
-    with_shape<AttnPass::second_rows>(a.dim, p, [&]<int ND, int W, int NQ>() {
-        rows_kernel<ND, W, NQ, false><<<Team<W>::grid(pieces(a, p)), 64 * W, 0, s>>>(
-            a, p, x, const_cast<float*>(delta), const_cast<float*>(sums), to_o, to_q);
+    with_shape<AttnPass::second_rows>(a.dim, p, [&]<int ND, int W, int NQ, bool IMAGES>() {
+        rows_kernel<ND, W, NQ, IMAGES, false><<<Team<W>::grid(pieces(a, p)), 64 * W, 0, s>>>(
+            a, p, x, static_cast<const char*>(images), const_cast<float*>(delta), const_cast<float*>(sums), to_o, to_q);
     });
     hipError_t e = hipGetLastError();
     const int64_t n = (int64_t)a.batch * a.queries * a.heads * a.dim;
@@ -291,7 +291,7 @@ hipError_t launch_attn_second_rows(const AttnArgs& a, const AttnPlan& p, const A
     return e;
 }
 
-hipError_t launch_attn_second_keys(const AttnArgs& a, const AttnPlan& p, const AttnSeconds& x, const float* delta,
+hipError_t launch_attn_second_keys(const AttnArgs& a, const AttnPlan& p, const AttnSeconds& x, const void* images, const float* delta,
                                    const float* sums, int sum_splits, float* gk, float* gv, float* gbias,
                                    float* partial_k, float* partial_v, float* partial_b, hipStream_t s)
 {
@@ -299,8 +299,8 @@ hipError_t launch_attn_second_keys(const AttnArgs& a, const AttnPlan& p, const A
     float* const to_k = gk != nullptr && cut ? partial_k : gk;
     float* const to_v = gv != nullptr && cut ? partial_v : gv;
     float* const to_b = join_bias ? partial_b : gbias;
-    with_shape<AttnPass::second_keys>(a.dim, p, [&]<int ND, int W, int NT>() {
-        keys_kernel<ND, W, NT><<<Team<W>::grid(pieces(a, p)), 64 * W, 0, s>>>(a, p, x, delta, sums, sum_splits, to_k, to_v, to_b);
+    with_shape<AttnPass::second_keys>(a.dim, p, [&]<int ND, int W, int NT, bool IMAGES>() {
+        keys_kernel<ND, W, NT, IMAGES><<<Team<W>::grid(pieces(a, p)), 64 * W, 0, s>>>(a, p, x, static_cast<const char*>(images), delta, sums, sum_splits, to_k, to_v, to_b);
     });
     hipError_t e = hipGetLastError();
     const int64_t n = (int64_t)a.batch * a.keys * a.kv_heads * a.dim;

@@ -45,16 +45,35 @@ constexpr int attn_waves(AttnPass pass, int nd)
 // How a pass is cut into pieces of work: a team of `waves` waves takes
 // `tiles` tiles of 16 (of its own side) per wave and one of `splits` ranges of
 // the other side.
+// images: the other side is split beforehand (attn_images).
 struct AttnPlan {
-    int waves, tiles, splits;
+    int waves, tiles, splits, images;
     int64_t own;             // pieces along the team's own side
 };
 AttnPlan attn_plan(const AttnArgs& a, AttnPass pass);
 
+// Tiles of 32 streamed rows of n arrays as they lie in LDS, split into three
+// BF16 pieces: [array][piece][row][attn_image_row], in whole KB.
+constexpr int kAttnTile = 32;
+constexpr int attn_image_row(int dim) { return (dim + 31) / 32 * 32 + 8; }
+constexpr int64_t attn_image_bytes(int dim, int n)
+{
+    return ((int64_t)n * 3 * kAttnTile * attn_image_row(dim) * 2 + 1023) / 1024 * 1024;
+}
+// Bytes of all tiles of a side, and the launch that makes them: `n` arrays of
+// the keys' shape (keys that take no part: zeros) and `m` of the rows' (either
+// may be 0; data null: zeros).
+size_t attn_key_images(const AttnArgs& a, int n);
+size_t attn_row_images(const AttnArgs& a, int m);
+hipError_t launch_attn_images(const AttnArgs& a, int n, const emu_heads_t* keys, void* key_images, int m,
+                              const emu_heads_t* rows, void* row_images, hipStream_t s);
+
 // The forward pass; partial: null unless plan.splits > 1.
 size_t attn_forward_partial(const AttnArgs& a, const AttnPlan& p);
+// images: of k and v, where the plan has them (so below: of the other side's
+// arrays, in the order k, v, vk, vv or q, dout, vq).
 hipError_t launch_attn_forward(const AttnArgs& a, const AttnPlan& p, emu_heads_t q, emu_heads_t k, emu_heads_t v,
-                               float* out, float* stats, float* partial, hipStream_t s);
+                               const void* images, float* out, float* stats, float* partial, hipStream_t s);
 
 // Floats of partial sums (0 for one split): of a result with the queries'
 // shape, of one with the keys' shape, of the bias gradient.
@@ -66,10 +85,10 @@ size_t attn_bias_partial(const AttnArgs& a, const AttnPlan& p);
 // over keys.  dq may be null (then only delta is written).
 hipError_t launch_attn_backward_rows(const AttnArgs& a, const AttnPlan& p, emu_heads_t dout, emu_heads_t q,
                                      emu_heads_t k, emu_heads_t v, const float* out, const float* stats,
-                                     float* delta, float* dq, float* partial, hipStream_t s);
+                                     const void* images, float* delta, float* dq, float* partial, hipStream_t s);
 hipError_t launch_attn_backward_keys(const AttnArgs& a, const AttnPlan& p, emu_heads_t dout, emu_heads_t q,
-                                     emu_heads_t k, emu_heads_t v, const float* stats, const float* delta,
-                                     float* dk, float* dv, float* dbias, float* partial_k, float* partial_v,
+                                     emu_heads_t k, emu_heads_t v, const void* images, const float* stats,
+                                     const float* delta, float* dk, float* dv, float* dbias, float* partial_k, float* partial_v,
                                      float* partial_b, hipStream_t s);
 
 // The backward pass's backward pass.
@@ -82,12 +101,12 @@ struct AttnSeconds {
     const float* stats;
 };
 // sums: [splits][rows of the call][2] partial sums over keys; delta as above.
-hipError_t launch_attn_second_sums(const AttnArgs& a, const AttnPlan& p, const AttnSeconds& t, float* delta,
-                                   float* sums, hipStream_t s);
-hipError_t launch_attn_second_rows(const AttnArgs& a, const AttnPlan& p, const AttnSeconds& t, const float* delta,
+hipError_t launch_attn_second_sums(const AttnArgs& a, const AttnPlan& p, const AttnSeconds& t, const void* images,
+                                   float* delta, float* sums, hipStream_t s);
+hipError_t launch_attn_second_rows(const AttnArgs& a, const AttnPlan& p, const AttnSeconds& t, const void* images, const float* delta,
                                    const float* sums, float* gdout, float* gq, float* partial_o, float* partial_q,
                                    hipStream_t s);
-hipError_t launch_attn_second_keys(const AttnArgs& a, const AttnPlan& p, const AttnSeconds& t, const float* delta,
+hipError_t launch_attn_second_keys(const AttnArgs& a, const AttnPlan& p, const AttnSeconds& t, const void* images, const float* delta,
                                    const float* sums, int sum_splits, float* gk, float* gv, float* gbias,
                                    float* partial_k, float* partial_v, float* partial_b, hipStream_t s);
 

@@ -22,6 +22,7 @@
 #pragma once
 
 #include "emu_attn_device.h"
+#include "emu_tile.h"
 
 namespace emu {
 
@@ -208,12 +209,16 @@ __device__ __forceinline__ void clear(f32x4_t (&acc)[NT][ND])
 
 // ---- the streamed side ------------------------------------------------------------
 //
-// N arrays of rows and X numbers per row, 32 at a time. Where registers allow,
-// the next tile is requested before the present one is used; a team of more
-// than one wave has two buffers in LDS where they leave room for two
-// workgroups, so that one barrier a tile does.
+// N arrays of rows and X numbers per row, 32 at a time, from one of two
+// sources. Where several teams stream the same side, it is split beforehand
+// into images of the tiles in LDS (emu_attn_planes.hip), which are copied there
+// directly, the next one while the present one is used. Otherwise the team
+// reads the arrays themselves and splits them on the way; where registers
+// allow, the next tile is requested before the present one is used.
+// Two buffers in LDS, so that one barrier a tile does, where they leave room
+// for two workgroups, or one buffer alone does not.
 
-constexpr int kStreamRows = 32;
+constexpr int kStreamRows = kAttnTile;
 
 // An array as a thread reads it: a tile's rows begin at base + first row / 32
 // * tile floats, the thread's there at offset + e * step.
@@ -223,20 +228,65 @@ struct StreamRows {
     int offset;
 };
 
-template <int ND, int W, int N, int X, bool KEYS>
+template <int ND, int W, int N, int X, bool KEYS, bool IMAGES>
 struct Stream {
     using T = Team<W>;
     static constexpr int RS = Heads<ND>::RS, kPiece = kStreamRows * RS, kArray = 3 * kPiece;
     // threads along a row (a power of two), a thread's rows and the distance between them
     static constexpr int kQuads = Heads<ND>::KS == 3 ? 32 : 8 * Heads<ND>::KS, kStep = T::kThreads / kQuads < kStreamRows ? T::kThreads / kQuads : kStreamRows;
     static constexpr int kEach = kStreamRows / kStep;
-    static constexpr int kBytes = N * kArray * 2 + X * kStreamRows * 4;
+    static constexpr int kArrays = IMAGES ? (int)attn_image_bytes(16 * ND, N) : N * kArray * 2;
+    static constexpr int kBytes = kArrays + X * kStreamRows * 4;
     static constexpr bool kAhead = N * kEach <= 8;
-    static constexpr int kBuffers = W > 1 && kAhead && 2 * kBytes <= 80 * 1024 ? 2 : 1;
+    static constexpr int kHalf = 80 * 1024;   // of a compute unit's LDS
+    static constexpr bool kTwo = IMAGES ? 2 * kBytes <= kHalf || (kBytes > kHalf && 2 * kBytes <= 2 * kHalf) : W > 1 && kAhead && 2 * kBytes <= kHalf;
+    static constexpr int kBuffers = kTwo ? 2 : 1;
     static_assert(kBytes % 16 == 0, "buffers stay aligned");
+    static_assert(RS == attn_image_row(16 * ND), "images are tiles as they lie in LDS");
 
     char* base;
     int turn = 0;
+
+    // The tiles lo .. hi of `images`, which hold the side's tiles in order.
+    template <class Q, class F>
+    __device__ __forceinline__ void run_images(const char* images, int64_t lo, int64_t hi, Q&& number, F&& f)
+    {
+        float numbers[X];
+        const auto request = [&](int64_t first) {
+            // (before the copies, which are waited for together with them)
+            if (T::thread() < kStreamRows) number(first, numbers);
+            char* const buffer = base + (kBuffers == 2 ? (turn ^ 1) * kBytes : 0);
+            const uint32_t to = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)buffer;
+            const char* const from = images + (first / kStreamRows) * kArrays;
+#pragma unroll
+            for (int c = 0; c < (kArrays / 1024 + W - 1) / W; ++c) {
+                const int chunk = c * W + T::wave();
+                if (chunk < kArrays / 1024) copy16_to_lds(to + chunk * 1024, from, (uint32_t)(chunk * 1024 + (threadIdx.x & 63) * 16));
+            }
+        };
+        if (kBuffers == 2 && lo < hi) {
+            T::sync();   // (a previous piece's last tile has been read)
+            request(lo);
+        }
+        for (int64_t first = lo; first < hi; first += kStreamRows) {
+            if (kBuffers == 1) {
+                T::sync();   // the previous tile has been read
+                request(first);
+            }
+            wait_vmcnt<0>();
+            if (kBuffers == 2) turn ^= 1;
+            char* const buffer = base + (kBuffers == 2 ? turn * kBytes : 0);
+            float* const nums = reinterpret_cast<float*>(buffer + kArrays);
+            if (T::thread() < kStreamRows) {
+#pragma unroll
+                for (int i = 0; i < X; ++i) nums[i * kStreamRows + T::thread()] = numbers[i];
+            }
+            T::sync();
+            if (kBuffers == 2 && first + kStreamRows < hi) request(first + kStreamRows);
+            if (!(KEYS && __all(nums[threadIdx.x & 31] == minus_inf())))
+                f(first, reinterpret_cast<const uint16_t*>(buffer), const_cast<const float*>(nums));
+        }
+    }
 
     struct Tile {
         f32x4_t v[kEach];
@@ -245,6 +295,7 @@ struct Stream {
     // Once: what lies past the heads' width is zero and stays so.
     __device__ __forceinline__ void clear()
     {
+        if (IMAGES) return;
         for (int i = T::thread(); i < kBuffers * kBytes / 16; i += T::kThreads) reinterpret_cast<u32x4_t*>(base)[i] = u32x4_t{};
         T::sync();
     }
@@ -353,9 +404,13 @@ struct Stream {
 
     // The keys' side: arrays of the keys' shape.
     template <class Q, class F, class... A>
-    __device__ __forceinline__ void run_keys(const AttnArgs& a, const Piece& at, int64_t lo, int64_t hi, Q&& number, F&& f,
-                                             const A&... arrays)
+    __device__ __forceinline__ void run_keys(const AttnArgs& a, const Piece& at, const char* images, int64_t lo, int64_t hi,
+                                             Q&& number, F&& f, const A&... arrays)
     {
+        if constexpr (IMAGES) {
+            const int64_t tiles = (a.keys + kStreamRows - 1) / kStreamRows;
+            return run_images(images + ((int64_t)at.b * a.kv_heads + at.g) * tiles * kArrays, lo, hi, number, f);
+        }
         const emu_heads_t of[N] = {arrays...};
         bool even = true;
 #pragma unroll
@@ -373,9 +428,13 @@ struct Stream {
 
     // The rows' side: arrays of the queries' shape.
     template <class Q, class F, class... A>
-    __device__ __forceinline__ void run_rows(const AttnArgs& a, const Piece& at, int64_t lo, int64_t hi, Q&& number, F&& f,
-                                             const A&... arrays)
+    __device__ __forceinline__ void run_rows(const AttnArgs& a, const Piece& at, const char* images, int64_t lo, int64_t hi,
+                                             Q&& number, F&& f, const A&... arrays)
     {
+        if constexpr (IMAGES) {
+            const int64_t tiles = (a.rows + kStreamRows - 1) / kStreamRows;
+            return run_images(images + ((int64_t)at.b * a.kv_heads + at.g) * tiles * kArrays, lo, hi, number, f);
+        }
         const emu_heads_t of[N] = {arrays...};
         // (a thread's rows are a whole number of queries apart)
         bool even = a.share <= kStep && kStep % a.share == 0;
@@ -409,17 +468,19 @@ struct Terms {
     }
 };
 
-// f.template operator()<ND, W, NT>() for a head and plan.
+// f.template operator()<ND, W, NT, IMAGES>() for a head and plan.
 template <AttnPass PASS, class F>
 inline void with_shape(int dim, const AttnPlan& p, F&& f)
 {
     const auto tiles = [&]<int ND>() {
-        if (p.waves == 1) return f.template operator()<ND, 1, 1>();
-        if (p.waves == 2) return f.template operator()<ND, 2, 1>();
-        if constexpr (attn_tiles(PASS, 16 * ND) == 2) {
-            if (p.tiles == 2) return f.template operator()<ND, 4, 2>();
+        constexpr int NT = attn_tiles(PASS, 16 * ND);
+        if (p.images) return f.template operator()<ND, 4, NT, true>();
+        if (p.waves == 1) return f.template operator()<ND, 1, 1, false>();
+        if (p.waves == 2) return f.template operator()<ND, 2, 1, false>();
+        if constexpr (NT == 2) {
+            if (p.tiles == 2) return f.template operator()<ND, 4, 2, false>();
         }
-        return f.template operator()<ND, 4, 1>();
+        return f.template operator()<ND, 4, 1, false>();
     };
     if (dim <= 16)
         tiles.template operator()<1>();
