@@ -21,6 +21,7 @@ __global__ __launch_bounds__(64 * W, attn_waves(AttnPass::rows, ND)) void rows_k
     __shared__ __attribute__((aligned(16))) char lds[S::kBuffers * S::kBytes];
     S stream{lds};
     stream.clear();
+    stagger();
     const int lane = threadIdx.x & 63, m = lane & 15, h = lane >> 4;
 
     T::each_piece((int64_t)a.batch * a.kv_heads * plan.own * plan.splits, [&](int64_t piece) {
@@ -94,6 +95,7 @@ __global__ __launch_bounds__(64 * W, attn_waves(AttnPass::keys, ND)) void keys_k
     __shared__ __attribute__((aligned(16))) char lds[S::kBuffers * S::kBytes];
     S stream{lds};
     stream.clear();
+    stagger();
     const int lane = threadIdx.x & 63, m = lane & 15, h = lane >> 4;
 
     T::each_piece((int64_t)a.batch * a.kv_heads * plan.own * plan.splits, [&](int64_t piece) {

@@ -10,46 +10,53 @@
 namespace emu {
 namespace {
 
+// The arrays of both sides, the keys' first.
 struct ImageArrays {
-    emu_heads_t of[4];
-    int n;
-    int64_t tiles;       // per sequence and key head
-    char* to;
+    emu_heads_t of[7];
+    int keys, all;
+    int64_t key_tiles, row_tiles;   // per sequence and key head
+    char *to_keys, *to_rows;
 };
 
-// One workgroup per tile: the keys' tiles, then the rows'.
+// A workgroup makes one array's part of an image, eight elements a thread.
+// (The rows' ends are written too: whole lines.)
 template <int KS>
-__global__ __launch_bounds__(256) void images_kernel(AttnArgs a, ImageArrays keys, ImageArrays rows)
+__global__ __launch_bounds__(kAttnTile * (4 * KS + 1)) void images_kernel(AttnArgs a, ImageArrays x)
 {
-    constexpr int RS = 32 * KS + 8, GROUPS = kAttnTile * 4 * KS;   // of eight elements
-    const int64_t heads = (int64_t)a.batch * a.kv_heads, key_tiles = keys.n > 0 ? heads * keys.tiles : 0;
-    const int64_t all = key_tiles + (rows.n > 0 ? heads * rows.tiles : 0);
-    for (int64_t tile = blockIdx.x; tile < all; tile += gridDim.x) {
-        const bool is_key = tile < key_tiles;
-        const ImageArrays& x = is_key ? keys : rows;
-        const int64_t mine = is_key ? tile : tile - key_tiles, head = mine / x.tiles, first = (mine - head * x.tiles) * kAttnTile;
-        const int b = (int)(head / a.kv_heads), g = (int)(head - (int64_t)b * a.kv_heads);
-        const int limit = keys_of(a, b);
-        uint16_t* const image = reinterpret_cast<uint16_t*>(x.to + mine * attn_image_bytes(32 * KS, x.n));
-        for (int i = threadIdx.x; i < GROUPS; i += 256) {
-            const int row = i / (4 * KS), col = i % (4 * KS) * 8;
-            const int64_t r = first + row;
-            const bool there = col < a.dim && (is_key ? r < a.keys && key_term(a, b, (int)r, limit) != minus_inf() : r < a.rows);
-            const RowAt at = is_key ? RowAt{0, 0} : row_at(a, g, there ? r : 0);
-            for (int n = 0; n < x.n; ++n) {
-                f32x4_t u = {}, v = {};
-                if (there && x.of[n].data != nullptr) {
-                    const float* const p = is_key ? key_ptr(x.of[n], b, g, r) : row_ptr(x.of[n], b, at);
-                    u = load4(p, col, a.dim);
-                    v = load4(p, col + 4, a.dim);
-                }
-                const Split8 s = split8<true>(u, v);
+    constexpr int RS = 32 * KS + 8;
+    const int n = blockIdx.y;
+    const bool is_key = n < x.keys;
+    emu_heads_t from = x.of[0];   // (chosen, not indexed: arguments stay in scalar registers)
 #pragma unroll
-                for (int p = 0; p < 3; ++p)
-                    *reinterpret_cast<bf16x8_t*>(image + ((n * 3 + p) * kAttnTile + row) * RS + col) = s.p[p];
+    for (int i = 1; i < 7; ++i)
+        if (n == i) from = x.of[i];
+    const int64_t tiles = is_key ? x.key_tiles : x.row_tiles, all = (int64_t)a.batch * a.kv_heads * tiles;
+    const int row = threadIdx.x / (RS / 8), col = threadIdx.x % (RS / 8) * 8;
+    for (int64_t tile = blockIdx.x; tile < all; tile += gridDim.x) {
+        const int64_t head = tile / tiles, r = (tile - head * tiles) * kAttnTile + row;
+        const int b = (int)(head / a.kv_heads), g = (int)(head - (int64_t)b * a.kv_heads);
+        f32x4_t u = {}, v = {};
+        if (col < a.dim && from.data != nullptr) {
+            if (is_key ? r < a.keys && key_term(a, b, (int)r, keys_of(a, b)) != minus_inf() : r < a.rows) {
+                const float* const p = is_key ? key_ptr(from, b, g, r) : row_ptr(from, b, row_at(a, g, r));
+                u = load4(p, col, a.dim);
+                v = load4(p, col + 4, a.dim);
             }
         }
+        const Split8 s = split8<true>(u, v);
+        char* const image = is_key ? x.to_keys + tile * attn_image_bytes(32 * KS, x.keys)
+                                   : x.to_rows + tile * attn_image_bytes(32 * KS, x.all - x.keys);
+        uint16_t* const to = reinterpret_cast<uint16_t*>(image) + ((is_key ? n : n - x.keys) * 3 * kAttnTile + row) * RS + col;
+#pragma unroll
+        for (int p = 0; p < 3; ++p) *reinterpret_cast<bf16x8_t*>(to + p * kAttnTile * RS) = s.p[p];
     }
+}
+
+template <int KS>
+void launch_images(const AttnArgs& a, const ImageArrays& x, hipStream_t s)
+{
+    const int64_t tiles = x.key_tiles > x.row_tiles ? x.key_tiles : x.row_tiles, all = (int64_t)a.batch * a.kv_heads * tiles;
+    images_kernel<KS><<<dim3((unsigned)(all < 65536 ? all : 65536), x.all), kAttnTile * (4 * KS + 1), 0, s>>>(a, x);
 }
 
 int64_t tiles_of(int64_t n) { return (n + kAttnTile - 1) / kAttnTile; }
@@ -68,26 +75,24 @@ size_t attn_row_images(const AttnArgs& a, int m)
 hipError_t launch_attn_images(const AttnArgs& a, int n, const emu_heads_t* keys, void* key_images, int m,
                               const emu_heads_t* rows, void* row_images, hipStream_t s)
 {
-    ImageArrays k{}, r{};
-    for (int i = 0; i < n; ++i) k.of[i] = keys[i];
-    for (int i = 0; i < m; ++i) r.of[i] = rows[i];
-    k.n = n;
-    r.n = m;
-    k.tiles = tiles_of(a.keys);
-    r.tiles = tiles_of(a.rows);
-    k.to = static_cast<char*>(key_images);
-    r.to = static_cast<char*>(row_images);
-    const int64_t all = (int64_t)a.batch * a.kv_heads * ((n > 0 ? k.tiles : 0) + (m > 0 ? r.tiles : 0));
-    if (all == 0) return hipSuccess;
-    const unsigned grid = (unsigned)(all < 65536 ? all : 65536);
+    ImageArrays x{};
+    for (int i = 0; i < n; ++i) x.of[i] = keys[i];
+    for (int i = 0; i < m; ++i) x.of[n + i] = rows[i];
+    x.keys = n;
+    x.all = n + m;
+    x.key_tiles = n > 0 ? tiles_of(a.keys) : 0;
+    x.row_tiles = m > 0 ? tiles_of(a.rows) : 0;
+    x.to_keys = static_cast<char*>(key_images);
+    x.to_rows = static_cast<char*>(row_images);
+    if (x.all == 0 || x.key_tiles + x.row_tiles == 0) return hipSuccess;
     if (a.dim <= 32)
-        images_kernel<1><<<grid, 256, 0, s>>>(a, k, r);
+        launch_images<1>(a, x, s);
     else if (a.dim <= 64)
-        images_kernel<2><<<grid, 256, 0, s>>>(a, k, r);
+        launch_images<2>(a, x, s);
     else if (a.dim <= 96)
-        images_kernel<3><<<grid, 256, 0, s>>>(a, k, r);
+        launch_images<3>(a, x, s);
     else
-        images_kernel<4><<<grid, 256, 0, s>>>(a, k, r);
+        launch_images<4>(a, x, s);
     return hipGetLastError();
 }
 
