@@ -17,17 +17,6 @@ constexpr int kMostSplits = 64;
 constexpr int kImageTeams = 2;   // teams that stream the same side, from which on it is split beforehand
 constexpr float kSlack = 4.0f;
 
-// Partial results of a split: rows' results, then their maxima and sums.
-struct ForwardPartial {
-    float* o;    // [splits][rows of the call][dim]
-    float* ml;   // [splits][rows of the call][2]
-};
-__host__ __device__ __forceinline__ ForwardPartial forward_partial(const AttnArgs& a, const AttnPlan& p, float* at)
-{
-    const int64_t n = (int64_t)a.batch * a.queries * a.heads;
-    return {at + 2 * p.splits * n, at};
-}
-
 template <int ND, int W, int NQ, bool IMAGES>
 __global__ __launch_bounds__(64 * W, attn_waves(AttnPass::forward, ND)) void forward_kernel(AttnArgs a, AttnPlan plan, emu_heads_t q, emu_heads_t k,
                                                          emu_heads_t v, const char* images, float* out, float* stats,
@@ -249,12 +238,19 @@ size_t attn_bias_partial(const AttnArgs& a, const AttnPlan& p)
 hipError_t launch_attn_forward(const AttnArgs& a, const AttnPlan& p, emu_heads_t q, emu_heads_t k, emu_heads_t v,
                                const void* images, float* out, float* stats, float* partial, hipStream_t s)
 {
-    with_shape<AttnPass::forward>(a.dim, p, [&]<int ND, int W, int NQ, bool IMAGES>() {
-        const int64_t n = (int64_t)a.batch * a.kv_heads * p.own * p.splits;
-        forward_kernel<ND, W, NQ, IMAGES><<<Team<W>::grid(n), 64 * W, 0, s>>>(a, p, q, k, v, static_cast<const char*>(images), out,
-                                                                                stats, partial);
-    });
-    hipError_t e = hipGetLastError();
+    hipError_t e = hipSuccess;
+    if (p.waves == 1) {
+        e = launch_attn_few(a, p, q, k, v, out, stats, partial, s);
+    } else {
+        with_shape<AttnPass::forward>(a.dim, p, [&]<int ND, int W, int NQ, bool IMAGES>() {
+            if constexpr (W > 1) {
+                const int64_t n = (int64_t)a.batch * a.kv_heads * p.own * p.splits;
+                forward_kernel<ND, W, NQ, IMAGES><<<Team<W>::grid(n), 64 * W, 0, s>>>(
+                    a, p, q, k, v, static_cast<const char*>(images), out, stats, partial);
+            }
+        });
+        e = hipGetLastError();
+    }
     if (e != hipSuccess || p.splits == 1) return e;
     const unsigned grid = join_grid((int64_t)a.batch * a.queries * a.heads);
     if (a.dim <= 32)

@@ -309,7 +309,8 @@ emu_status_t emu_rotary(int64_t batch, int64_t tokens, int64_t heads, int64_t di
     if (batch < 0 || tokens < 0 || heads < 0 || dim < 0 || pairs < 0 || pairs > dim / 2 ||
         ((int)layout != EMU_ROTARY_HALF && (int)layout != EMU_ROTARY_INTERLEAVED) || !std::isfinite(magnitude))
         return EMU_STATUS_INVALID_VALUE;
-    if (batch > kMaxSize || tokens > kMaxSize || heads > kMaxSize || dim > kMaxSize) return EMU_STATUS_NOT_SUPPORTED;
+    if (batch > kMaxSize || tokens > kMaxSize || heads > kMaxSize || dim > EMU_ROTARY_MAX_DIM || heads * dim > kMaxSize)
+        return EMU_STATUS_NOT_SUPPORTED;
     if (batch == 0 || tokens == 0 || heads == 0 || dim == 0) return EMU_STATUS_SUCCESS;
     if (x.data == nullptr || y == nullptr || (pairs > 0 && (positions == nullptr || turns == nullptr)))
         return EMU_STATUS_INVALID_VALUE;

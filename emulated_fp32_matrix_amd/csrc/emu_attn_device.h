@@ -165,4 +165,15 @@ __device__ __forceinline__ int64_t key_index(const AttnArgs& a, int b, int g, in
     return ((int64_t)b * a.keys + j) * a.kv_heads + g;
 }
 
+// Partial results of a split: rows' results, then their maxima and sums.
+struct ForwardPartial {
+    float* o;    // [splits][rows of the call][dim]
+    float* ml;   // [splits][rows of the call][2]
+};
+__host__ __device__ __forceinline__ ForwardPartial forward_partial(const AttnArgs& a, const AttnPlan& p, float* at)
+{
+    const int64_t n = (int64_t)a.batch * a.queries * a.heads;
+    return {at + 2 * p.splits * n, at};
+}
+
 }  // namespace emu

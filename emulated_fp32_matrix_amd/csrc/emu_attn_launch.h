@@ -75,6 +75,10 @@ size_t attn_forward_partial(const AttnArgs& a, const AttnPlan& p);
 hipError_t launch_attn_forward(const AttnArgs& a, const AttnPlan& p, emu_heads_t q, emu_heads_t k, emu_heads_t v,
                                const void* images, float* out, float* stats, float* partial, hipStream_t s);
 
+// Its first launch where a team is one wave (at most 16 rows).
+hipError_t launch_attn_few(const AttnArgs& a, const AttnPlan& p, emu_heads_t q, emu_heads_t k, emu_heads_t v, float* out,
+                           float* stats, float* partial, hipStream_t s);
+
 // Floats of partial sums (0 for one split): of a result with the queries'
 // shape, of one with the keys' shape, of the bias gradient.
 size_t attn_rows_partial(const AttnArgs& a, const AttnPlan& p);

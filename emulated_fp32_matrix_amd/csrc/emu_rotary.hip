@@ -3,9 +3,7 @@
 // Bound by memory: an element is read and written once.  The angle is the
 // product of the position and the frequency, a 64-bit fraction of a turn,
 // modulo 2^64: what is left of it is exact at any position, where an FP32
-// angle of a million radians has lost all of its fraction.  A thread makes the
-// cosine and sine of its pairs once and takes them through the heads of its
-// token.
+// angle of a million radians has lost all of its fraction.
 #include "emu_attn_launch.h"
 #include "emu_block_device.h"
 
@@ -30,57 +28,86 @@ __device__ __forceinline__ Turn turn_of(uint64_t turn, float f, bool inverse)
     return {cos * f, sin * f};
 }
 
-// Work items of a token and head: groups of four elements, rotated ones first.
-// HALF: group i is elements 4 i .. and pairs + 4 i ..; INTERLEAVED: pairs 2 i,
-// 2 i + 1; then the rest of the head in groups of four.
+constexpr int kTokens = 32;   // most tokens of a workgroup
+constexpr int kTurns = 1024;  // and cosines of them
+
+// A workgroup's tokens: first their cosines and sines, shared by all heads,
+// then the heads in groups of four elements (HALF: elements 4 i .. and pairs +
+// 4 i ..; INTERLEAVED: pairs 2 i, 2 i + 1; then what is copied), as they follow
+// each other in memory, kAtOnce groups of a thread requested together.
+// blockIdx.y: which of the chunks of `chunk` groups, of heads too wide to
+// share their cosines at once.
 template <int LAYOUT>
-__global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a, int groups, int copies, int heads_each, int head_parts)
+__global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a, int tokens_each, int groups, int copies, int chunk)
 {
-    const int64_t n = a.batch * a.tokens * head_parts * (groups + copies);
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-        const int64_t at = i / (groups + copies);
-        const int group = (int)(i - at * (groups + copies));
-        const int64_t token_at = at / head_parts;
-        const int h0 = (int)(at - token_at * head_parts) * heads_each;
-        const int64_t b = token_at / a.tokens, t = token_at - b * a.tokens;
-        const int h1 = h0 + heads_each < a.heads ? h0 + heads_each : a.heads;
-        const float* x = a.x.data + (b * a.x.batch + t * a.x.token);
-        float* y = a.y + (b * a.tokens + t) * a.heads * a.dim;
-        if (group >= groups) {
-            const int col = 2 * a.pairs + 4 * (group - groups);
-            for (int h = h0; h < h1; ++h) store4(y + (int64_t)h * a.dim, col, a.dim, load4(x + h * a.x.head, col, a.dim));
-            continue;
+    constexpr int N = LAYOUT == EMU_ROTARY_HALF ? 4 : 2, kAtOnce = 4;   // pairs of a group
+    __shared__ Turn turns[kTurns];
+    __shared__ int64_t from[kTokens];
+    const int64_t all = a.batch * a.tokens;
+    const int g0 = blockIdx.y * chunk, rest = groups + copies - g0, here = rest < chunk ? rest : chunk;
+    const int turned = g0 >= groups ? 0 : groups - g0 < here ? groups - g0 : here;
+    for (int64_t first = (int64_t)blockIdx.x * tokens_each; first < all; first += (int64_t)gridDim.x * tokens_each) {
+        const int count = (int)(all - first < tokens_each ? all - first : tokens_each);
+        __syncthreads();   // the previous tokens' have been read
+        for (int i = threadIdx.x; i < count * N * turned; i += 256) {
+            const int token = (int)((unsigned)i / (unsigned)(N * turned)), pair = i - token * N * turned + N * g0;
+            const int64_t b = (first + token) / a.tokens, t = first + token - b * a.tokens;
+            const uint64_t pos = pair < a.pairs ? (uint64_t)a.positions[b * a.pos_b + t * a.pos_t] : 0;
+            turns[i] = turn_of(pair < a.pairs ? pos * a.turns[pair] : 0, a.magnitude, a.inverse != 0);
         }
-        const uint64_t pos = (uint64_t)a.positions[b * a.pos_b + t * a.pos_t];
-        constexpr int N = LAYOUT == EMU_ROTARY_HALF ? 4 : 2;
-        Turn turn[N];
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-            const int pair = N * group + e;
-            turn[e] = turn_of(pair < a.pairs ? pos * a.turns[pair] : 0, a.magnitude, a.inverse != 0);
+        if ((int)threadIdx.x < count) {
+            const int64_t b = (first + threadIdx.x) / a.tokens, t = first + threadIdx.x - b * a.tokens;
+            from[threadIdx.x] = b * a.x.batch + t * a.x.token;
         }
-        for (int h = h0; h < h1; ++h) {
-            const float* xr = x + h * a.x.head;
-            float* yr = y + (int64_t)h * a.dim;
-            if constexpr (LAYOUT == EMU_ROTARY_HALF) {
-                const f32x4_t p = load4(xr, 4 * group, a.pairs), q = load4(xr + a.pairs, 4 * group, a.pairs);
-                f32x4_t u, v;
+        __syncthreads();
+        const int per_token = a.heads * here, n = count * per_token;
+        for (int i0 = threadIdx.x; i0 < n; i0 += 256 * kAtOnce) {
+            f32x4_t p[kAtOnce], q[kAtOnce];
+            int token[kAtOnce], group[kAtOnce];
+            float* y[kAtOnce];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    u[e] = __builtin_fmaf(p[e], turn[e].cos, -(q[e] * turn[e].sin));
-                    v[e] = __builtin_fmaf(p[e], turn[e].sin, q[e] * turn[e].cos);
+            for (int k = 0; k < kAtOnce; ++k) {
+                const int i = i0 + 256 * k < n ? i0 + 256 * k : i0;
+                token[k] = (int)((unsigned)i / (unsigned)per_token);
+                const int in = i - token[k] * per_token, head = (int)((unsigned)in / (unsigned)here);
+                group[k] = in - head * here;
+                const float* const x = a.x.data + (from[token[k]] + head * a.x.head);
+                y[k] = a.y + ((first + token[k]) * a.heads + head) * a.dim;
+                const int g = g0 + group[k];
+                if (group[k] >= turned) {
+                    p[k] = load4(x, 2 * a.pairs + 4 * (g - groups), a.dim);
+                } else if constexpr (LAYOUT == EMU_ROTARY_HALF) {
+                    p[k] = load4(x, 4 * g, a.pairs);
+                    q[k] = load4(x + a.pairs, 4 * g, a.pairs);
+                } else {
+                    p[k] = load4(x, 4 * g, 2 * a.pairs);
                 }
-                store4(yr, 4 * group, a.pairs, u);
-                store4(yr + a.pairs, 4 * group, a.pairs, v);
-            } else {
-                const f32x4_t p = load4(xr, 4 * group, 2 * a.pairs);
-                f32x4_t u;
+            }
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    u[2 * e] = __builtin_fmaf(p[2 * e], turn[e].cos, -(p[2 * e + 1] * turn[e].sin));
-                    u[2 * e + 1] = __builtin_fmaf(p[2 * e], turn[e].sin, p[2 * e + 1] * turn[e].cos);
+            for (int k = 0; k < kAtOnce; ++k) {
+                if (i0 + 256 * k >= n) continue;
+                const int g = g0 + group[k];
+                const Turn* const turn = turns + (token[k] * turned + group[k]) * N;
+                if (group[k] >= turned) {
+                    store4(y[k], 2 * a.pairs + 4 * (g - groups), a.dim, p[k]);
+                } else if constexpr (LAYOUT == EMU_ROTARY_HALF) {
+                    f32x4_t u, v;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        u[e] = __builtin_fmaf(p[k][e], turn[e].cos, -(q[k][e] * turn[e].sin));
+                        v[e] = __builtin_fmaf(p[k][e], turn[e].sin, q[k][e] * turn[e].cos);
+                    }
+                    store4(y[k], 4 * g, a.pairs, u);
+                    store4(y[k] + a.pairs, 4 * g, a.pairs, v);
+                } else {
+                    f32x4_t u;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        u[2 * e] = __builtin_fmaf(p[k][2 * e], turn[e].cos, -(p[k][2 * e + 1] * turn[e].sin));
+                        u[2 * e + 1] = __builtin_fmaf(p[k][2 * e], turn[e].sin, p[k][2 * e + 1] * turn[e].cos);
+                    }
+                    store4(y[k], 4 * g, 2 * a.pairs, u);
                 }
-                store4(yr, 4 * group, 2 * a.pairs, u);
             }
         }
     }
@@ -90,18 +117,24 @@ __global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a, int groups, i
 
 hipError_t launch_rotary(const RotaryArgs& a, hipStream_t s)
 {
-    const int groups = a.layout == EMU_ROTARY_HALF ? (a.pairs + 3) / 4 : (a.pairs + 1) / 2;
-    const int copies = (a.dim - 2 * a.pairs + 3) / 4;
-    // heads that share a thread's cosines, fewer where threads are few
-    int each = a.heads;
-    while (each > 1 && a.batch * a.tokens * ((a.heads + each - 1) / each) * (groups + copies) < 256 * 1024) each = (each + 1) / 2;
-    const int parts = (a.heads + each - 1) / each;
-    const int64_t wgs = (a.batch * a.tokens * parts * (groups + copies) + 255) / 256;
-    const unsigned grid = (unsigned)(wgs < 65536 ? wgs : 65536);
+    const int pairs = a.layout == EMU_ROTARY_HALF ? 4 : 2;   // of a group
+    const int groups = (a.pairs + pairs - 1) / pairs;
+    const int copies = (int)(((int64_t)a.dim - 2 * a.pairs + 3) / 4);
+    // groups at once, and tokens: 16 KB of elements (or what is there for 1,024
+    // workgroups), as far as their cosines fit
+    const int chunk = groups + copies < kTurns / 4 ? groups + copies : kTurns / 4;
+    const int64_t all = a.batch * a.tokens, work = (int64_t)a.heads * chunk;
+    int64_t each = 1024 / work;
+    if (each > (all + 1023) / 1024) each = (all + 1023) / 1024;
+    if (each > kTokens) each = kTokens;
+    if (each * chunk * pairs > kTurns) each = kTurns / (chunk * pairs);
+    if (each < 1) each = 1;
+    const int64_t wgs = (all + each - 1) / each;
+    const dim3 grid((unsigned)(wgs < ((int64_t)1 << 20) ? wgs : (int64_t)1 << 20), (unsigned)((groups + copies + chunk - 1) / chunk));
     if (a.layout == EMU_ROTARY_HALF)
-        rotary_kernel<EMU_ROTARY_HALF><<<grid, 256, 0, s>>>(a, groups, copies, each, parts);
+        rotary_kernel<EMU_ROTARY_HALF><<<grid, 256, 0, s>>>(a, (int)each, groups, copies, chunk);
     else
-        rotary_kernel<EMU_ROTARY_INTERLEAVED><<<grid, 256, 0, s>>>(a, groups, copies, each, parts);
+        rotary_kernel<EMU_ROTARY_INTERLEAVED><<<grid, 256, 0, s>>>(a, (int)each, groups, copies, chunk);
     return hipGetLastError();
 }
 

@@ -137,9 +137,11 @@ emu_status_t emu_cross_attention_backward2(const emu_attention_t* a, emu_heads_t
  * is dense.
  * Errors: EMU_STATUS_INVALID_VALUE for a negative size, 2 * pairs > dim, a
  * bad layout, NULL arrays that have elements, a magnitude that is not finite;
- * EMU_STATUS_NOT_SUPPORTED for batch, tokens, heads or dim above 2^30, or a
- * device that is not gfx950.
+ * EMU_STATUS_NOT_SUPPORTED for batch, tokens or heads * dim above 2^30, dim
+ * above EMU_ROTARY_MAX_DIM, or a device that is not gfx950.
  */
+#define EMU_ROTARY_MAX_DIM 65536
+
 typedef enum {
     EMU_ROTARY_HALF = 0,
     EMU_ROTARY_INTERLEAVED = 1

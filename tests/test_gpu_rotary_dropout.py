@@ -31,7 +31,8 @@ def rotate(x, positions, frequencies, layout, magnitude, inverse=False):
 @pytest.mark.parametrize("batch,tokens,heads,dim,part,start,scaling", [
     (1, 1, 1, 2, 2, 0, None), (2, 5, 3, 7, 6, 11, None), (1, 33, 8, 32, 32, 0, "linear"), (3, 17, 4, 64, 24, 5000, "base"),
     (2, 40, 2, 128, 128, 1000003, "parts"), (4, 1, 16, 64, 64, -70001, None), (1, 2000, 5, 50, 50, 2 ** 40, None),
-    (2, 3, 2, 33, 10, 3, "parts"), (700, 9, 12, 96, 64, 100, None)])
+    (2, 3, 2, 33, 10, 3, "parts"), (700, 9, 12, 96, 64, 100, None),
+    (2, 3, 2, 2600, 2500, 7, None), (1, 2, 1, 1030, 1030, 7, "base"), (2, 300, 1, 6, 4, 0, None), (3, 11, 70, 8, 8, 1, None)])
 def test_rotary(layout, batch, tokens, heads, dim, part, start, scaling):
     g = torch.Generator(device=DEV).manual_seed(dim)
     x = torch.randn(batch, tokens, heads, dim, generator=g, device=DEV).requires_grad_(True)
