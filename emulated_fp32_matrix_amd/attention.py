@@ -226,9 +226,12 @@ class EmuCrossAttention(torch.nn.Module):
                  norm=True, eps=1e-5, mode="AUTO", device=None):
         super().__init__()
         kv_heads = heads if kv_heads is None else kv_heads
-        head_dim = dim // heads if head_dim is None else head_dim
         if heads < 1 or kv_heads < 1 or heads % kv_heads:
             raise ValueError(f"heads must be a multiple of kv_heads, not {heads} and {kv_heads}")
+        if head_dim is None:
+            if dim % heads:
+                raise ValueError(f"{dim} features do not divide into {heads} heads: give head_dim")
+            head_dim = dim // heads
         if not 1 <= head_dim <= MAX_DIM:
             raise ValueError(f"heads must be 1 to {MAX_DIM} wide, not {head_dim}")
         _mode_of(mode)
