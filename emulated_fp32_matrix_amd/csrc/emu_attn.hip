@@ -17,13 +17,13 @@ constexpr int kMostSplits = 64;
 constexpr int kImageTeams = 2;   // teams that stream the same side, from which on it is split beforehand
 constexpr float kSlack = 4.0f;
 
-template <int ND, int W, int NQ, bool IMAGES>
-__global__ __launch_bounds__(64 * W, attn_waves(AttnPass::forward, ND)) void forward_kernel(AttnArgs a, AttnPlan plan, emu_heads_t q, emu_heads_t k,
+template <int ND, int NQ, bool IMAGES>
+__global__ __launch_bounds__(64 * kTeam, attn_waves(AttnPass::forward, ND, IMAGES)) void forward_kernel(AttnArgs a, AttnPlan plan, emu_heads_t q, emu_heads_t k,
                                                          emu_heads_t v, const char* images, float* out, float* stats,
                                                          float* partial)
 {
-    using T = Team<W>;
-    using S = Stream<ND, W, 2, 1, true, IMAGES>;
+    using T = Team<kTeam>;
+    using S = Stream<ND, 2, 1, true, IMAGES>;
     __shared__ __attribute__((aligned(16))) char lds[S::kBuffers * S::kBytes];
     S stream{lds};
     stream.clear();
@@ -39,7 +39,7 @@ __global__ __launch_bounds__(64 * W, attn_waves(AttnPass::forward, ND)) void for
         Split8 own[NQ][Heads<ND>::KS];
         f32x4_t acc[NQ][ND];
         float most[NQ], sum[NQ];
-        const int64_t r0 = (at.own * W + T::wave()) * (16 * NQ) + m;
+        const int64_t r0 = (at.own * kTeam + T::wave()) * (16 * NQ) + m;
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
             const int64_t r = r0 + 16 * n;
@@ -137,8 +137,7 @@ __global__ __launch_bounds__(64 * W, attn_waves(AttnPass::forward, ND)) void for
 // The ranges' results of a row, joined in order: a workgroup per row, COLS
 // columns of it by 256 / COLS groups of ranges.
 template <int COLS>
-__global__ __launch_bounds__(256) void join_forward_kernel(AttnArgs a, AttnPlan plan, float* partial, float* out,
-                                                           float* stats)
+__global__ __launch_bounds__(256) void join_many_kernel(AttnArgs a, AttnPlan plan, float* partial, float* out, float* stats)
 {
     constexpr int GROUPS = 256 / COLS;
     __shared__ float parts[GROUPS][COLS];
@@ -178,14 +177,56 @@ __global__ __launch_bounds__(256) void join_forward_kernel(AttnArgs a, AttnPlan 
     }
 }
 
-__global__ __launch_bounds__(256) void join_kernel(int64_t n, int64_t splits, int64_t inner, const float* in, float* out)
+// The same of up to kFewSplits ranges: a thread per four columns.
+constexpr int kFewSplits = 8;
+
+__global__ __launch_bounds__(256) void join_few_kernel(AttnArgs a, AttnPlan plan, float* partial, float* out, float* stats)
 {
+    const int64_t rows = (int64_t)a.batch * a.queries * a.heads;
+    const ForwardPartial from = forward_partial(a, plan, partial);
+    const int quads = (a.dim + 3) / 4;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * quads; i += (int64_t)gridDim.x * 256) {
+        const int64_t row = i / quads;
+        const int col = (int)(i - row * quads) * 4;
+        float most = minus_inf(), m[kFewSplits];
+#pragma unroll
+        for (int s = 0; s < kFewSplits; ++s) {
+            m[s] = s < plan.splits ? from.ml[2 * (s * rows + row)] : minus_inf();
+            most = __builtin_fmaxf(most, m[s]);
+        }
+        const float safe = most == minus_inf() ? 0.0f : most;
+        float sum = 0.0f;
+        f32x4_t acc = {};
+#pragma unroll
+        for (int s = 0; s < kFewSplits; ++s) {
+            if (s >= plan.splits) continue;
+            const float f = exp_of(m[s] - safe);
+            sum = __builtin_fmaf(from.ml[2 * (s * rows + row) + 1], f, sum);
+            acc = acc + load4(from.o + (s * rows + row) * a.dim, col, a.dim) * f;
+        }
+        const float over = sum == 0.0f ? 0.0f : 1.0f / sum;
+        store4(out + row * a.dim, col, a.dim, acc * over);
+        if (stats != nullptr && col == 0) {
+            stats[2 * row] = safe;
+            stats[2 * row + 1] = over;
+        }
+    }
+}
+
+// blockIdx.y: which of the sums.
+__global__ __launch_bounds__(256) void join_kernel(AttnJoins j)
+{
+    AttnJoin x = j.of[0];   // (chosen, not indexed: arguments stay in scalar registers)
+#pragma unroll
+    for (int i = 1; i < kAttnJoins; ++i)
+        if (blockIdx.y == i) x = j.of[i];
+    const int64_t n = x.outer * x.inner;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-        const int64_t o = i / inner;
-        const float* at = in + o * splits * inner + (i - o * inner);
+        const int64_t o = x.outer == 1 ? 0 : i / x.inner;
+        const float* at = x.in + o * x.splits * x.inner + (i - o * x.inner);
         float sum = at[0];
-        for (int64_t s = 1; s < splits; ++s) sum = sum + at[s * inner];
-        out[i] = sum;
+        for (int64_t s = 1; s < x.splits; ++s) sum = sum + at[s * x.inner];
+        x.out[i] = sum;
     }
 }
 
@@ -209,12 +250,13 @@ AttnPlan attn_plan(const AttnArgs& a, AttnPass pass)
     const bool keys = pass == AttnPass::keys || pass == AttnPass::second_keys;
     const int64_t own = keys ? a.keys : a.rows, other = keys ? a.rows : a.keys;
     AttnPlan p{};
-    p.waves = own <= 16 ? 1 : own <= 32 ? 2 : 4;
+    // (the forward pass has a kernel of its own for few rows)
+    p.waves = pass == AttnPass::forward && own <= 16 ? 1 : 4;
     p.tiles = own <= 64 ? 1 : attn_tiles(pass, a.dim);
     const int64_t each = p.waves * p.tiles * 16;
     p.own = (own + each - 1) / each;
     p.images = p.waves == 4 && p.own >= kImageTeams;
-    p.splits = splits_for((int64_t)a.batch * a.kv_heads * p.own * p.waves, other, p.waves == 1 ? 128 : 256);
+    p.splits = splits_for((int64_t)a.batch * a.kv_heads * p.own * p.waves, other, p.images ? 256 : 128);
     return p;
 }
 
@@ -242,31 +284,40 @@ hipError_t launch_attn_forward(const AttnArgs& a, const AttnPlan& p, emu_heads_t
     if (p.waves == 1) {
         e = launch_attn_few(a, p, q, k, v, out, stats, partial, s);
     } else {
-        with_shape<AttnPass::forward>(a.dim, p, [&]<int ND, int W, int NQ, bool IMAGES>() {
-            if constexpr (W > 1) {
-                const int64_t n = (int64_t)a.batch * a.kv_heads * p.own * p.splits;
-                forward_kernel<ND, W, NQ, IMAGES><<<Team<W>::grid(n), 64 * W, 0, s>>>(
-                    a, p, q, k, v, static_cast<const char*>(images), out, stats, partial);
-            }
+        with_shape<AttnPass::forward>(a.dim, p, [&]<int ND, int NQ, bool IMAGES>() {
+            const int64_t n = (int64_t)a.batch * a.kv_heads * p.own * p.splits;
+            forward_kernel<ND, NQ, IMAGES><<<Team<kTeam>::grid(n), 64 * kTeam, 0, s>>>(
+                a, p, q, k, v, static_cast<const char*>(images), out, stats, partial);
         });
         e = hipGetLastError();
     }
     if (e != hipSuccess || p.splits == 1) return e;
-    const unsigned grid = join_grid((int64_t)a.batch * a.queries * a.heads);
-    if (a.dim <= 32)
-        join_forward_kernel<32><<<grid, 256, 0, s>>>(a, p, partial, out, stats);
+    const int64_t rows = (int64_t)a.batch * a.queries * a.heads;
+    const unsigned grid = join_grid(rows);
+    if (p.splits <= kFewSplits)
+        join_few_kernel<<<join_grid((rows * ((a.dim + 3) / 4) + 255) / 256), 256, 0, s>>>(a, p, partial, out, stats);
+    else if (a.dim <= 32)
+        join_many_kernel<32><<<grid, 256, 0, s>>>(a, p, partial, out, stats);
     else if (a.dim <= 64)
-        join_forward_kernel<64><<<grid, 256, 0, s>>>(a, p, partial, out, stats);
+        join_many_kernel<64><<<grid, 256, 0, s>>>(a, p, partial, out, stats);
     else
-        join_forward_kernel<128><<<grid, 256, 0, s>>>(a, p, partial, out, stats);
+        join_many_kernel<128><<<grid, 256, 0, s>>>(a, p, partial, out, stats);
     return hipGetLastError();
 }
 
-hipError_t launch_attn_join(int64_t outer, int64_t splits, int64_t inner, const float* in, float* out, hipStream_t s)
+hipError_t launch_attn_joins(const AttnJoins& joins, hipStream_t s)
 {
-    const int64_t n = outer * inner;
-    if (n == 0) return hipSuccess;
-    join_kernel<<<join_grid((n + 255) / 256), 256, 0, s>>>(n, splits, inner, in, out);
+    AttnJoins j{};
+    int64_t most = 0;
+    for (int i = 0; i < joins.n; ++i) {
+        const AttnJoin& x = joins.of[i];
+        const int64_t n = x.outer * x.inner;
+        if (x.out == nullptr || x.in == x.out || n == 0) continue;
+        j.of[j.n++] = x;
+        if (n > most) most = n;
+    }
+    if (j.n == 0) return hipSuccess;
+    join_kernel<<<dim3(join_grid((most + 255) / 256), j.n), 256, 0, s>>>(j);
     return hipGetLastError();
 }
 

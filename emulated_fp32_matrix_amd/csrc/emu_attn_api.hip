@@ -104,7 +104,7 @@ struct ForwardSpace {
 };
 size_t forward_bytes(const AttnArgs& a)
 {
-    return !has_rows(a) || emu::attn_whole(a, 0) ? 0 : ForwardSpace(a, nullptr).bytes;
+    return !has_rows(a) || emu::attn_whole(a) ? 0 : ForwardSpace(a, nullptr).bytes;
 }
 
 struct BackwardSpace {
@@ -117,7 +117,7 @@ struct BackwardSpace {
         Layout l(ws);
         delta = dq = dk = dv = db = nullptr;
         key_images = row_images = nullptr;
-        if (emu::attn_whole(a, 1)) {
+        if (emu::attn_whole(a)) {
             db = l.take(emu::attn_whole_partial(a));
             bytes = l.bytes;
             return;
@@ -143,7 +143,7 @@ struct SecondSpace {
         Layout l(ws);
         delta = sums = go = gq = gk = gv = gb = nullptr;
         key_images = row_images = nullptr;
-        if (emu::attn_whole(a, 2)) {
+        if (emu::attn_whole(a)) {
             gb = l.take(emu::attn_whole_partial(a));
             bytes = l.bytes;
             return;
@@ -205,7 +205,7 @@ emu_status_t emu_cross_attention(const emu_attention_t* in, emu_heads_t q, emu_h
     if (!has_rows(a)) return EMU_STATUS_SUCCESS;
     if (bad_workspace(workspace, workspace_bytes, forward_bytes(a))) return EMU_STATUS_INVALID_VALUE;
     if (!on_gfx950()) return EMU_STATUS_NOT_SUPPORTED;
-    if (emu::attn_whole(a, 0)) return from_hip(emu::launch_whole_forward(a, q, k, v, out, stats, stream_of(stream)));
+    if (emu::attn_whole(a)) return from_hip(emu::launch_whole_forward(a, q, k, v, out, stats, stream_of(stream)));
     const ForwardSpace w(a, workspace);
     const emu_heads_t keys[] = {k, v};
     hipError_t e = w.plan.images ? emu::launch_attn_images(a, 2, keys, w.images, 0, nullptr, nullptr, stream_of(stream)) : hipSuccess;
@@ -242,7 +242,7 @@ emu_status_t emu_cross_attention_backward(const emu_attention_t* in, emu_heads_t
     const hipStream_t s = stream_of(stream);
     if (!rows) return zero_keys(a, dk, dv, dbias, s);
     const BackwardSpace w(a, workspace);
-    if (emu::attn_whole(a, 1))
+    if (emu::attn_whole(a))
         return from_hip(emu::launch_whole_backward(a, dout, q, k, v, stats, dq, dk, dv, dbias, w.db, s));
     const emu_heads_t key_side[] = {k, v}, row_side[] = {q, dout};
     hipError_t e = emu::launch_attn_images(a, w.rows.images && dq != nullptr ? 2 : 0, key_side, w.key_images,
@@ -287,7 +287,7 @@ emu_status_t emu_cross_attention_backward2(const emu_attention_t* in, emu_heads_
     if (!rows) return zero_keys(a, gk, gv, gbias, s);
     const SecondSpace w(a, workspace);
     const emu::AttnSeconds x{vq, vk, vv, vbias, vbias_batch, vbias_key, dout, q, k, v, out, stats};
-    if (emu::attn_whole(a, 2)) return from_hip(emu::launch_whole_second(a, x, gdout, gq, gk, gv, gbias, w.gb, s));
+    if (emu::attn_whole(a)) return from_hip(emu::launch_whole_second(a, x, gdout, gq, gk, gv, gbias, w.gb, s));
     const emu_heads_t key_side[] = {k, v, vk, vv}, row_side[] = {q, dout, vq};
     hipError_t e = emu::launch_attn_images(a, w.rows.images ? 4 : 0, key_side, w.key_images,
                                            w.keys.images && keys_wanted ? 3 : 0, row_side, w.row_images, s);

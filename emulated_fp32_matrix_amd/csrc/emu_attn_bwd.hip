@@ -11,13 +11,13 @@
 namespace emu {
 namespace {
 
-template <int ND, int W, int NQ, bool IMAGES>
-__global__ __launch_bounds__(64 * W, attn_waves(AttnPass::rows, ND)) void rows_kernel(AttnArgs a, AttnPlan plan, emu_heads_t dout, emu_heads_t q,
+template <int ND, int NQ, bool IMAGES>
+__global__ __launch_bounds__(64 * kTeam, attn_waves(AttnPass::rows, ND, IMAGES)) void rows_kernel(AttnArgs a, AttnPlan plan, emu_heads_t dout, emu_heads_t q,
                                                       emu_heads_t k, emu_heads_t v, const char* images, const float* out,
                                                       const float* stats, float* delta, float* dq, float* partial)
 {
-    using T = Team<W>;
-    using S = Stream<ND, W, 2, 1, true, IMAGES>;
+    using T = Team<kTeam>;
+    using S = Stream<ND, 2, 1, true, IMAGES>;
     __shared__ __attribute__((aligned(16))) char lds[S::kBuffers * S::kBytes];
     S stream{lds};
     stream.clear();
@@ -33,7 +33,7 @@ __global__ __launch_bounds__(64 * W, attn_waves(AttnPass::rows, ND)) void rows_k
         Split8 oq[NQ][Heads<ND>::KS], od[NQ][Heads<ND>::KS];
         f32x4_t acc[NQ][ND];
         float top[NQ], over[NQ], del[NQ];
-        const int64_t r0 = (at.own * W + T::wave()) * (16 * NQ) + m;
+        const int64_t r0 = (at.own * kTeam + T::wave()) * (16 * NQ) + m;
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
             const int64_t r = r0 + 16 * n;
@@ -85,13 +85,13 @@ __global__ __launch_bounds__(64 * W, attn_waves(AttnPass::rows, ND)) void rows_k
     });
 }
 
-template <int ND, int W, int NT, bool IMAGES>
-__global__ __launch_bounds__(64 * W, attn_waves(AttnPass::keys, ND)) void keys_kernel(AttnArgs a, AttnPlan plan, emu_heads_t dout, emu_heads_t q,
+template <int ND, int NT, bool IMAGES>
+__global__ __launch_bounds__(64 * kTeam, attn_waves(AttnPass::keys, ND, IMAGES)) void keys_kernel(AttnArgs a, AttnPlan plan, emu_heads_t dout, emu_heads_t q,
                                                       emu_heads_t k, emu_heads_t v, const char* images,
                                                       const float* stats, const float* delta, float* dk, float* dv, float* db)
 {
-    using T = Team<W>;
-    using S = Stream<ND, W, 2, 3, false, IMAGES>;
+    using T = Team<kTeam>;
+    using S = Stream<ND, 2, 3, false, IMAGES>;
     __shared__ __attribute__((aligned(16))) char lds[S::kBuffers * S::kBytes];
     S stream{lds};
     stream.clear();
@@ -107,7 +107,7 @@ __global__ __launch_bounds__(64 * W, attn_waves(AttnPass::keys, ND)) void keys_k
         Split8 ok[NT][Heads<ND>::KS], ov[NT][Heads<ND>::KS];
         f32x4_t ak[NT][ND], av[NT][ND];
         float add[NT], bias[NT];
-        const int64_t j0 = (at.own * W + T::wave()) * (16 * NT) + m;
+        const int64_t j0 = (at.own * kTeam + T::wave()) * (16 * NT) + m;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const int64_t j = j0 + 16 * n;
@@ -120,7 +120,7 @@ __global__ __launch_bounds__(64 * W, attn_waves(AttnPass::keys, ND)) void keys_k
         clear(ak);
         clear(av);
         // (a team whose keys all take no part has zeros to write)
-        if (at.own * W * 16 * NT >= limit) hi = lo;
+        if (at.own * kTeam * 16 * NT >= limit) hi = lo;
 
         // maxima, 1 / sums, deltas; behind the last row p = e^-inf 0
         const auto number = [&](int64_t first, float* to) {
@@ -187,13 +187,13 @@ hipError_t launch_attn_backward_rows(const AttnArgs& a, const AttnPlan& p, emu_h
                                      emu_heads_t k, emu_heads_t v, const float* out, const float* stats,
                                      const void* images, float* delta, float* dq, float* partial, hipStream_t s)
 {
-    with_shape<AttnPass::rows>(a.dim, p, [&]<int ND, int W, int NQ, bool IMAGES>() {
+    with_shape<AttnPass::rows>(a.dim, p, [&]<int ND, int NQ, bool IMAGES>() {
         const int64_t n = (int64_t)a.batch * a.kv_heads * p.own * p.splits;
-        rows_kernel<ND, W, NQ, IMAGES><<<Team<W>::grid(n), 64 * W, 0, s>>>(a, p, dout, q, k, v, static_cast<const char*>(images), out, stats, delta, dq, partial);
+        rows_kernel<ND, NQ, IMAGES><<<Team<kTeam>::grid(n), 64 * kTeam, 0, s>>>(a, p, dout, q, k, v, static_cast<const char*>(images), out, stats, delta, dq, partial);
     });
     hipError_t e = hipGetLastError();
-    if (e == hipSuccess && p.splits > 1 && dq != nullptr)
-        e = launch_attn_join(1, p.splits, (int64_t)a.batch * a.queries * a.heads * a.dim, partial, dq, s);
+    if (e == hipSuccess && p.splits > 1)
+        e = launch_attn_joins({1, {{1, p.splits, (int64_t)a.batch * a.queries * a.heads * a.dim, partial, dq}}}, s);
     return e;
 }
 
@@ -206,16 +206,15 @@ hipError_t launch_attn_backward_keys(const AttnArgs& a, const AttnPlan& p, emu_h
     float* const to_k = dk != nullptr && cut ? partial_k : dk;
     float* const to_v = dv != nullptr && cut ? partial_v : dv;
     float* const to_b = join_bias ? partial_b : dbias;
-    with_shape<AttnPass::keys>(a.dim, p, [&]<int ND, int W, int NT, bool IMAGES>() {
+    with_shape<AttnPass::keys>(a.dim, p, [&]<int ND, int NT, bool IMAGES>() {
         const int64_t n = (int64_t)a.batch * a.kv_heads * p.own * p.splits;
-        keys_kernel<ND, W, NT, IMAGES><<<Team<W>::grid(n), 64 * W, 0, s>>>(a, p, dout, q, k, v, static_cast<const char*>(images), stats, delta, to_k, to_v, to_b);
+        keys_kernel<ND, NT, IMAGES><<<Team<kTeam>::grid(n), 64 * kTeam, 0, s>>>(a, p, dout, q, k, v, static_cast<const char*>(images), stats, delta, to_k, to_v, to_b);
     });
     hipError_t e = hipGetLastError();
     const int64_t n = (int64_t)a.batch * a.keys * a.kv_heads * a.dim;
-    if (e == hipSuccess && cut && dk != nullptr) e = launch_attn_join(1, p.splits, n, partial_k, dk, s);
-    if (e == hipSuccess && cut && dv != nullptr) e = launch_attn_join(1, p.splits, n, partial_v, dv, s);
-    if (e == hipSuccess && join_bias)
-        e = launch_attn_join(a.batch, (int64_t)p.splits * a.kv_heads, a.keys, partial_b, dbias, s);
+    if (e == hipSuccess)
+        e = launch_attn_joins({3, {{1, p.splits, n, to_k, dk}, {1, p.splits, n, to_v, dv},
+                                   {a.batch, (int64_t)p.splits * a.kv_heads, a.keys, to_b, dbias}}}, s);
     return e;
 }
 

@@ -14,12 +14,12 @@
 namespace emu {
 namespace {
 
-template <int ND, int W, int NQ, bool IMAGES, bool SUMS>
-__global__ __launch_bounds__(64 * W, attn_waves(AttnPass::second_rows, ND)) void rows_kernel(AttnArgs a, AttnPlan plan, AttnSeconds x, const char* images, float* delta, float* sums,
+template <int ND, int NQ, bool IMAGES, bool SUMS>
+__global__ __launch_bounds__(64 * kTeam, attn_waves(AttnPass::second_rows, ND, IMAGES)) void rows_kernel(AttnArgs a, AttnPlan plan, AttnSeconds x, const char* images, float* delta, float* sums,
                                                       float* go, float* gq)
 {
-    using T = Team<W>;
-    using S = Stream<ND, W, 4, 2, true, IMAGES>;
+    using T = Team<kTeam>;
+    using S = Stream<ND, 4, 2, true, IMAGES>;
     constexpr int KS = Heads<ND>::KS;
     __shared__ __attribute__((aligned(16))) char lds[S::kBuffers * S::kBytes];
     S stream{lds};
@@ -36,7 +36,7 @@ __global__ __launch_bounds__(64 * W, attn_waves(AttnPass::second_rows, ND)) void
 
         Split8 oq[NQ][KS], od[NQ][KS], oa[NQ][KS];
         float top[NQ], over[NQ], del[NQ], mean[NQ], tmean[NQ];   // SUMS: the last two are this range's sums
-        const int64_t r0 = (at.own * W + T::wave()) * (16 * NQ) + m;
+        const int64_t r0 = (at.own * kTeam + T::wave()) * (16 * NQ) + m;
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
             const int64_t r = r0 + 16 * n;
@@ -140,12 +140,12 @@ __global__ __launch_bounds__(64 * W, attn_waves(AttnPass::second_rows, ND)) void
     });
 }
 
-template <int ND, int W, int NT, bool IMAGES>
-__global__ __launch_bounds__(64 * W, attn_waves(AttnPass::second_keys, ND)) void keys_kernel(AttnArgs a, AttnPlan plan, AttnSeconds x, const char* images, const float* delta,
+template <int ND, int NT, bool IMAGES>
+__global__ __launch_bounds__(64 * kTeam, attn_waves(AttnPass::second_keys, ND, IMAGES)) void keys_kernel(AttnArgs a, AttnPlan plan, AttnSeconds x, const char* images, const float* delta,
                                                       const float* sums, int sum_splits, float* gk, float* gv, float* gb)
 {
-    using T = Team<W>;
-    using S = Stream<ND, W, 3, 5, false, IMAGES>;
+    using T = Team<kTeam>;
+    using S = Stream<ND, 3, 5, false, IMAGES>;
     constexpr int KS = Heads<ND>::KS;
     __shared__ __attribute__((aligned(16))) char lds[S::kBuffers * S::kBytes];
     S stream{lds};
@@ -163,7 +163,7 @@ __global__ __launch_bounds__(64 * W, attn_waves(AttnPass::second_keys, ND)) void
         Split8 ok[NT][KS], ov[NT][KS], ovk[NT][KS], ovv[NT][KS];
         f32x4_t ak[NT][ND], av[NT][ND];
         float add[NT], vadd[NT], bias[NT];
-        const int64_t j0 = (at.own * W + T::wave()) * (16 * NT) + m;
+        const int64_t j0 = (at.own * kTeam + T::wave()) * (16 * NT) + m;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const int64_t j = j0 + 16 * n;
@@ -180,7 +180,7 @@ __global__ __launch_bounds__(64 * W, attn_waves(AttnPass::second_keys, ND)) void
         clear(ak);
         clear(av);
         // (a team whose keys all take no part has zeros to write)
-        if (at.own * W * 16 * NT >= limit) hi = lo;
+        if (at.own * kTeam * 16 * NT >= limit) hi = lo;
 
         // maxima, 1 / sums, deltas, g, t; behind the last row p = e^-inf 0
         const auto number = [&](int64_t first, float* to) {
@@ -269,8 +269,8 @@ int64_t pieces(const AttnArgs& a, const AttnPlan& p) { return (int64_t)a.batch *
 hipError_t launch_attn_second_sums(const AttnArgs& a, const AttnPlan& p, const AttnSeconds& x, const void* images,
                                    float* delta, float* sums, hipStream_t s)
 {
-    with_shape<AttnPass::second_rows>(a.dim, p, [&]<int ND, int W, int NQ, bool IMAGES>() {
-        rows_kernel<ND, W, NQ, IMAGES, true><<<Team<W>::grid(pieces(a, p)), 64 * W, 0, s>>>(a, p, x, static_cast<const char*>(images), delta, sums, nullptr, nullptr);
+    with_shape<AttnPass::second_rows>(a.dim, p, [&]<int ND, int NQ, bool IMAGES>() {
+        rows_kernel<ND, NQ, IMAGES, true><<<Team<kTeam>::grid(pieces(a, p)), 64 * kTeam, 0, s>>>(a, p, x, static_cast<const char*>(images), delta, sums, nullptr, nullptr);
     });
     return hipGetLastError();
 }
@@ -282,14 +282,13 @@ hipError_t launch_attn_second_rows(const AttnArgs& a, const AttnPlan& p, const A
     const bool cut = p.splits > 1;
     float* const to_o = gdout != nullptr && cut ? partial_o : gdout;
     float* const to_q = gq != nullptr && cut ? partial_q : gq;
-    with_shape<AttnPass::second_rows>(a.dim, p, [&]<int ND, int W, int NQ, bool IMAGES>() {
-        rows_kernel<ND, W, NQ, IMAGES, false><<<Team<W>::grid(pieces(a, p)), 64 * W, 0, s>>>(
+    with_shape<AttnPass::second_rows>(a.dim, p, [&]<int ND, int NQ, bool IMAGES>() {
+        rows_kernel<ND, NQ, IMAGES, false><<<Team<kTeam>::grid(pieces(a, p)), 64 * kTeam, 0, s>>>(
             a, p, x, static_cast<const char*>(images), const_cast<float*>(delta), const_cast<float*>(sums), to_o, to_q);
     });
     hipError_t e = hipGetLastError();
     const int64_t n = (int64_t)a.batch * a.queries * a.heads * a.dim;
-    if (e == hipSuccess && cut && gdout != nullptr) e = launch_attn_join(1, p.splits, n, partial_o, gdout, s);
-    if (e == hipSuccess && cut && gq != nullptr) e = launch_attn_join(1, p.splits, n, partial_q, gq, s);
+    if (e == hipSuccess) e = launch_attn_joins({2, {{1, p.splits, n, to_o, gdout}, {1, p.splits, n, to_q, gq}}}, s);
     return e;
 }
 
@@ -301,15 +300,14 @@ hipError_t launch_attn_second_keys(const AttnArgs& a, const AttnPlan& p, const A
     float* const to_k = gk != nullptr && cut ? partial_k : gk;
     float* const to_v = gv != nullptr && cut ? partial_v : gv;
     float* const to_b = join_bias ? partial_b : gbias;
-    with_shape<AttnPass::second_keys>(a.dim, p, [&]<int ND, int W, int NT, bool IMAGES>() {
-        keys_kernel<ND, W, NT, IMAGES><<<Team<W>::grid(pieces(a, p)), 64 * W, 0, s>>>(a, p, x, static_cast<const char*>(images), delta, sums, sum_splits, to_k, to_v, to_b);
+    with_shape<AttnPass::second_keys>(a.dim, p, [&]<int ND, int NT, bool IMAGES>() {
+        keys_kernel<ND, NT, IMAGES><<<Team<kTeam>::grid(pieces(a, p)), 64 * kTeam, 0, s>>>(a, p, x, static_cast<const char*>(images), delta, sums, sum_splits, to_k, to_v, to_b);
     });
     hipError_t e = hipGetLastError();
     const int64_t n = (int64_t)a.batch * a.keys * a.kv_heads * a.dim;
-    if (e == hipSuccess && cut && gk != nullptr) e = launch_attn_join(1, p.splits, n, partial_k, gk, s);
-    if (e == hipSuccess && cut && gv != nullptr) e = launch_attn_join(1, p.splits, n, partial_v, gv, s);
-    if (e == hipSuccess && join_bias)
-        e = launch_attn_join(a.batch, (int64_t)p.splits * a.kv_heads, a.keys, partial_b, gbias, s);
+    if (e == hipSuccess)
+        e = launch_attn_joins({3, {{1, p.splits, n, to_k, gk}, {1, p.splits, n, to_v, gv},
+                                   {a.batch, (int64_t)p.splits * a.kv_heads, a.keys, to_b, gbias}}}, s);
     return e;
 }
 

@@ -37,14 +37,16 @@ constexpr int attn_tiles(AttnPass pass, int dim)
 }
 // Waves of a SIMD that the registers are divided among: one where even a tile
 // each of wide heads does not fit half of them.
-constexpr int attn_waves(AttnPass pass, int nd)
+constexpr int attn_waves(AttnPass pass, int nd, bool images)
 {
-    return nd >= 8 && (pass == AttnPass::second_rows || pass == AttnPass::second_keys) ? 1 : nd >= 8 && pass == AttnPass::keys ? 1 : 2;
+    const bool second = pass == AttnPass::second_rows || pass == AttnPass::second_keys;
+    if (nd >= 8) return second || pass == AttnPass::keys ? 1 : 2;
+    return nd >= 5 && second && (pass == AttnPass::second_keys || !images) ? 1 : 2;
 }
 
-// How a pass is cut into pieces of work: a team of `waves` waves takes
-// `tiles` tiles of 16 (of its own side) per wave and one of `splits` ranges of
-// the other side.
+// How a pass is cut into pieces of work: a team of `waves` waves (4; 1 in the
+// forward pass of few rows) takes `tiles` tiles of 16 (of its own side) per
+// wave and one of `splits` ranges of the other side.
 // images: the other side is split beforehand (attn_images).
 struct AttnPlan {
     int waves, tiles, splits, images;
@@ -114,9 +116,9 @@ hipError_t launch_attn_second_keys(const AttnArgs& a, const AttnPlan& p, const A
                                    const float* sums, int sum_splits, float* gk, float* gv, float* gbias,
                                    float* partial_k, float* partial_v, float* partial_b, hipStream_t s);
 
-// Short sequences, each direction in one launch: whether a call's are (order
-// as above), and the launches.  partial: floats of attn_whole_partial().
-bool attn_whole(const AttnArgs& a, int order);
+// Short sequences, each direction in one launch: whether a call's are, and
+// the launches.  partial: floats of attn_whole_partial().
+bool attn_whole(const AttnArgs& a);
 inline size_t attn_whole_partial(const AttnArgs& a)
 {
     return a.kv_heads > 1 ? (size_t)a.batch * a.keys * a.kv_heads : 0;
@@ -130,7 +132,18 @@ hipError_t launch_whole_second(const AttnArgs& a, const AttnSeconds& x, float* g
                                float* gbias, float* partial, hipStream_t s);
 
 // out[o][i] = sum over s of in[o][s][i], s in order; outer x inner results.
-hipError_t launch_attn_join(int64_t outer, int64_t splits, int64_t inner, const float* in, float* out, hipStream_t s);
+// Several at once; out null, or in itself: nothing to do.
+struct AttnJoin {
+    int64_t outer, splits, inner;
+    const float* in;
+    float* out;
+};
+constexpr int kAttnJoins = 3;
+struct AttnJoins {
+    int n;
+    AttnJoin of[kAttnJoins];
+};
+hipError_t launch_attn_joins(const AttnJoins& joins, hipStream_t s);
 
 struct RotaryArgs {
     int64_t batch, tokens;

@@ -238,9 +238,11 @@ struct StreamRows {
     int offset;
 };
 
-template <int ND, int W, int N, int X, bool KEYS, bool IMAGES>
+constexpr int kTeam = 4;   // waves that share a streamed tile
+
+template <int ND, int N, int X, bool KEYS, bool IMAGES>
 struct Stream {
-    using T = Team<W>;
+    using T = Team<kTeam>;
     static constexpr int RS = Heads<ND>::RS, kPiece = kStreamRows * RS, kArray = 3 * kPiece;
     // threads along a row (a power of two), a thread's rows and the distance between them
     static constexpr int kQuads = Heads<ND>::KS == 3 ? 32 : 8 * Heads<ND>::KS, kStep = T::kThreads / kQuads < kStreamRows ? T::kThreads / kQuads : kStreamRows;
@@ -249,7 +251,7 @@ struct Stream {
     static constexpr int kBytes = kArrays + X * kStreamRows * 4;
     static constexpr bool kAhead = N * kEach <= 8;
     static constexpr int kHalf = 80 * 1024;   // of a compute unit's LDS
-    static constexpr bool kTwo = IMAGES ? 2 * kBytes <= kHalf || (kBytes > kHalf && 2 * kBytes <= 2 * kHalf) : W > 1 && kAhead && 2 * kBytes <= kHalf;
+    static constexpr bool kTwo = IMAGES ? 2 * kBytes <= kHalf || (kBytes > kHalf && 2 * kBytes <= 2 * kHalf) : kAhead && 2 * kBytes <= kHalf;
     static constexpr int kBuffers = kTwo ? 2 : 1;
     static_assert(kBytes % 16 == 0, "buffers stay aligned");
     static_assert(RS == attn_image_row(16 * ND), "images are tiles as they lie in LDS");
@@ -269,8 +271,8 @@ struct Stream {
             const uint32_t to = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)buffer;
             const char* const from = images + (first / kStreamRows) * kArrays;
 #pragma unroll
-            for (int c = 0; c < (kArrays / 1024 + W - 1) / W; ++c) {
-                const int chunk = c * W + T::wave();
+            for (int c = 0; c < (kArrays / 1024 + kTeam - 1) / kTeam; ++c) {
+                const int chunk = c * kTeam + T::wave();
                 if (chunk < kArrays / 1024) copy16_to_lds(to + chunk * 1024, from, (uint32_t)(chunk * 1024 + (threadIdx.x & 63) * 16));
             }
         };
@@ -478,19 +480,17 @@ struct Terms {
     }
 };
 
-// f.template operator()<ND, W, NT, IMAGES>() for a head and plan.
+// f.template operator()<ND, NT, IMAGES>() for a head and plan.
 template <AttnPass PASS, class F>
 inline void with_shape(int dim, const AttnPlan& p, F&& f)
 {
     const auto tiles = [&]<int ND>() {
         constexpr int NT = attn_tiles(PASS, 16 * ND);
-        if (p.images) return f.template operator()<ND, 4, NT, true>();
-        if (p.waves == 1) return f.template operator()<ND, 1, 1, false>();
-        if (p.waves == 2) return f.template operator()<ND, 2, 1, false>();
+        if (p.images) return f.template operator()<ND, NT, true>();
         if constexpr (NT == 2) {
-            if (p.tiles == 2) return f.template operator()<ND, 4, 2, false>();
+            if (p.tiles == 2) return f.template operator()<ND, 2, false>();
         }
-        return f.template operator()<ND, 4, 1, false>();
+        return f.template operator()<ND, 1, false>();
     };
     if (dim <= 16)
         tiles.template operator()<1>();

@@ -384,21 +384,21 @@ __global__ __launch_bounds__(256, NT < 3 && ND * NT <= 4 ? 2 : 1) void second_ke
 }
 
 // f.template operator()<ND, NT>() for what attn_whole() takes.
-template <int MOST, class F>
+template <class F>
 void with_whole(const AttnArgs& a, F&& f)
 {
     const int64_t n = a.rows > a.keys ? a.rows : a.keys;
     const auto tiles = [&]<int ND>() {
         if (n <= 16) return f.template operator()<ND, 1>();
-        if constexpr (ND < 4 || MOST == 3) {
-            if (n > 32) return f.template operator()<ND, 3>();
-        }
-        return f.template operator()<ND, 2>();
+        if (n <= 32) return f.template operator()<ND, 2>();
+        return f.template operator()<ND, 3>();
     };
     if (a.dim <= 16)
         tiles.template operator()<1>();
     else if (a.dim <= 32)
         tiles.template operator()<2>();
+    else if (a.dim <= 48)
+        tiles.template operator()<3>();
     else
         tiles.template operator()<4>();
 }
@@ -406,7 +406,7 @@ void with_whole(const AttnArgs& a, F&& f)
 hipError_t join_bias(const AttnArgs& a, float* db, const float* partial, hipStream_t s)
 {
     hipError_t e = hipGetLastError();
-    if (e == hipSuccess && db != nullptr && a.kv_heads > 1) e = launch_attn_join(a.batch, a.kv_heads, a.keys, partial, db, s);
+    if (e == hipSuccess && a.kv_heads > 1) e = launch_attn_joins({1, {{a.batch, a.kv_heads, a.keys, partial, db}}}, s);
     return e;
 }
 
@@ -414,16 +414,12 @@ unsigned whole_grid(const AttnArgs& a) { return T::grid((int64_t)a.batch * a.kv_
 
 }  // namespace
 
-bool attn_whole(const AttnArgs& a, int order)
-{
-    const int64_t n = a.rows > a.keys ? a.rows : a.keys;
-    return a.dim <= 64 && n <= (a.dim > 32 && order == 2 ? 32 : 48);
-}
+bool attn_whole(const AttnArgs& a) { return a.dim <= 64 && a.rows <= 48 && a.keys <= 48; }
 
 hipError_t launch_whole_forward(const AttnArgs& a, emu_heads_t q, emu_heads_t k, emu_heads_t v, float* out, float* stats,
                                 hipStream_t s)
 {
-    with_whole<3>(a, [&]<int ND, int NT>() { forward_kernel<ND, NT><<<whole_grid(a), 256, 0, s>>>(a, q, k, v, out, stats); });
+    with_whole(a, [&]<int ND, int NT>() { forward_kernel<ND, NT><<<whole_grid(a), 256, 0, s>>>(a, q, k, v, out, stats); });
     return hipGetLastError();
 }
 
@@ -432,7 +428,7 @@ hipError_t launch_whole_backward(const AttnArgs& a, emu_heads_t dout, emu_heads_
                                  hipStream_t s)
 {
     float* const to_b = dbias != nullptr && a.kv_heads > 1 ? partial : dbias;
-    with_whole<3>(a, [&]<int ND, int NT>() {
+    with_whole(a, [&]<int ND, int NT>() {
         backward_kernel<ND, NT><<<whole_grid(a), 256, 0, s>>>(a, dout, q, k, v, stats, dq, dk, dv, to_b);
     });
     return join_bias(a, dbias, partial, s);
@@ -442,7 +438,7 @@ hipError_t launch_whole_second(const AttnArgs& a, const AttnSeconds& x, float* g
                                float* gbias, float* partial, hipStream_t s)
 {
     float* const to_b = gbias != nullptr && a.kv_heads > 1 ? partial : gbias;
-    with_whole<2>(a, [&]<int ND, int NT>() {
+    with_whole(a, [&]<int ND, int NT>() {
         second_kernel<ND, NT><<<whole_grid(a), 256, 0, s>>>(a, x, gdout, gq, gk, gv, to_b);
     });
     return join_bias(a, gbias, partial, s);
