@@ -56,7 +56,7 @@ __global__ __launch_bounds__(64 * kTeam, attn_waves(AttnPass::forward, ND, IMAGE
             f32x4_t s[2][NQ];
 #pragma unroll
             for (int n = 0; n < NQ; ++n) s[0][n] = s[1][n] = f32x4_t{};
-            scores<ND, S::kPiece, NQ>(arrays, m, h, own, s);
+            scores<ND, S::kPiece, true, NQ>(arrays, m, h, own, s);
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -90,7 +90,6 @@ __global__ __launch_bounds__(64 * kTeam, attn_waves(AttnPass::forward, ND, IMAGE
                     for (int t = 0; t < ND; ++t) acc[n][t] = acc[n][t] * old;
                 }
             }
-            Split8 w[NQ];
 #pragma unroll
             for (int n = 0; n < NQ; ++n) {
                 const float safe = most[n] == minus_inf() ? 0.0f : most[n];   // (no key so far: all of e^(-inf - 0) = 0)
@@ -103,9 +102,8 @@ __global__ __launch_bounds__(64 * kTeam, attn_waves(AttnPass::forward, ND, IMAGE
                         here = here + s[t][n][j];
                     }
                 sum[n] = sum[n] + here;
-                w[n] = split8(s[0][n], s[1][n]);
             }
-            results<ND, S::kPiece, NQ>(arrays + S::kArray, m, h, w, acc);
+            results<ND, S::kPiece, true, NQ>(arrays + S::kArray, m, h, s, acc);
         }, k, v);
 
 #pragma unroll
@@ -233,13 +231,20 @@ __global__ __launch_bounds__(256) void join_kernel(AttnJoins j)
 unsigned join_grid(int64_t groups) { return (unsigned)(groups < 65536 ? groups : 65536); }
 
 // Ranges of the other side: enough pieces for 2,048 waves (256 compute units
-// of 8), none shorter than `least` of the streamed side.
-int splits_for(int64_t waves, int64_t other, int64_t least)
+// of 8), none shorter than `least` of the streamed side. Where sequences differ
+// in length (`ragged`) twice as many, of 512 and more: 21 x 8 x 200 rows x up
+// to 1,918 keys x 48 forward 115 -> 97 us with three ranges; ranges of 259 keys
+// instead of 388 cost 14 x 771 rows x up to 777 keys 39 -> 44.
+int splits_for(int64_t waves, int64_t other, int64_t least, bool ragged)
 {
-    int64_t s = waves > 0 ? 2048 / waves : 1;
-    const int64_t most = other / least;
-    if (s > most) s = most;
-    if (s > kMostSplits) s = kMostSplits;
+    const int64_t n = waves > 0 ? waves : 1;
+    const auto limited = [](int64_t s, int64_t most) { return s < most ? s : most; };
+    int64_t s = limited(2048 / n, other / least);
+    if (ragged) {
+        const int64_t more = limited(4096 / n, other / 512);
+        s = s > more ? s : more;
+    }
+    s = limited(s, kMostSplits);
     return s < 1 ? 1 : (int)s;
 }
 
@@ -256,7 +261,8 @@ AttnPlan attn_plan(const AttnArgs& a, AttnPass pass)
     const int64_t each = p.waves * p.tiles * 16;
     p.own = (own + each - 1) / each;
     p.images = p.waves == 4 && p.own >= kImageTeams;
-    p.splits = splits_for((int64_t)a.batch * a.kv_heads * p.own * p.waves, other, p.images ? 256 : 128);
+    p.splits = splits_for((int64_t)a.batch * a.kv_heads * p.own * p.waves, other, p.images ? 256 : 128,
+                          !keys && a.lengths != nullptr);
     return p;
 }
 

@@ -56,8 +56,8 @@ __global__ __launch_bounds__(64 * kTeam, attn_waves(AttnPass::rows, ND, IMAGES))
             f32x4_t s[2][NQ], dp[2][NQ];
 #pragma unroll
             for (int n = 0; n < NQ; ++n) s[0][n] = s[1][n] = dp[0][n] = dp[1][n] = f32x4_t{};
-            scores<ND, S::kPiece, NQ>(arrays, m, h, oq, s);
-            scores<ND, S::kPiece, NQ>(arrays + S::kArray, m, h, od, dp);
+            scores<ND, S::kPiece, true, NQ>(arrays, m, h, oq, s);
+            scores<ND, S::kPiece, true, NQ>(arrays + S::kArray, m, h, od, dp);
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -67,10 +67,7 @@ __global__ __launch_bounds__(64 * kTeam, attn_waves(AttnPass::rows, ND, IMAGES))
                         const float p = exp_of(__builtin_fmaf(s[t][n][j], a.scale, term.of[t][j]) - top[n]) * over[n];
                         s[t][n][j] = p * (dp[t][n][j] - del[n]);
                     }
-            Split8 w[NQ];
-#pragma unroll
-            for (int n = 0; n < NQ; ++n) w[n] = split8(s[0][n], s[1][n]);
-            results<ND, S::kPiece, NQ>(arrays, m, h, w, acc);
+            results<ND, S::kPiece, true, NQ>(arrays, m, h, s, acc);
         }, k, v);
 
         if (dq == nullptr) return;
@@ -134,8 +131,8 @@ __global__ __launch_bounds__(64 * kTeam, attn_waves(AttnPass::keys, ND, IMAGES))
             f32x4_t s[2][NT], dp[2][NT];
 #pragma unroll
             for (int n = 0; n < NT; ++n) s[0][n] = s[1][n] = dp[0][n] = dp[1][n] = f32x4_t{};
-            scores<ND, S::kPiece, NT>(arrays, m, h, ok, s);
-            scores<ND, S::kPiece, NT>(arrays + S::kArray, m, h, ov, dp);
+            scores<ND, S::kPiece, false, NT>(arrays, m, h, ok, s);
+            scores<ND, S::kPiece, false, NT>(arrays + S::kArray, m, h, ov, dp);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 const float* const row = numbers + 16 * t + 4 * h;
@@ -152,13 +149,8 @@ __global__ __launch_bounds__(64 * kTeam, attn_waves(AttnPass::keys, ND, IMAGES))
                         bias[n] = bias[n] + dp[t][n][j];
                     }
             }
-            Split8 w[NT];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) w[n] = split8(s[0][n], s[1][n]);
-            results<ND, S::kPiece, NT>(arrays + S::kArray, m, h, w, av);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) w[n] = split8(dp[0][n], dp[1][n]);
-            results<ND, S::kPiece, NT>(arrays, m, h, w, ak);
+            results<ND, S::kPiece, false, NT>(arrays + S::kArray, m, h, s, av);
+            results<ND, S::kPiece, false, NT>(arrays, m, h, dp, ak);
         }, q, dout);
 
 #pragma unroll

@@ -79,11 +79,11 @@ __global__ __launch_bounds__(64 * kTeam, attn_waves(AttnPass::second_rows, ND, I
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int n = 0; n < NQ; ++n) s[t][n] = dp[t][n] = gg[t][n] = ee[t][n] = f32x4_t{};
-            scores<ND, S::kPiece, NQ>(tk, m, h, oq, s);
-            scores<ND, S::kPiece, NQ>(tk, m, h, oa, gg);
-            scores<ND, S::kPiece, NQ>(tvk, m, h, oq, gg);
-            scores<ND, S::kPiece, NQ>(tv, m, h, od, dp);
-            scores<ND, S::kPiece, NQ>(tvv, m, h, od, ee);
+            scores<ND, S::kPiece, ND <= 4, NQ>(tk, m, h, oq, s);
+            scores<ND, S::kPiece, ND <= 4, NQ>(tk, m, h, oa, gg);
+            scores<ND, S::kPiece, ND <= 4, NQ>(tvk, m, h, oq, gg);
+            scores<ND, S::kPiece, ND <= 4, NQ>(tv, m, h, od, dp);
+            scores<ND, S::kPiece, ND <= 4, NQ>(tvv, m, h, od, ee);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 const f32x4_t vadd = *reinterpret_cast<const f32x4_t*>(numbers + kStreamRows + 16 * t + 4 * h);
@@ -107,16 +107,10 @@ __global__ __launch_bounds__(64 * kTeam, attn_waves(AttnPass::second_rows, ND, I
                     }
             }
             if constexpr (!SUMS) {
-                Split8 w[NQ];
-                const auto add = [&](const f32x4_t (&x)[2][NQ], const uint16_t* tile, f32x4_t (&acc)[NQ][ND]) {
-#pragma unroll
-                    for (int n = 0; n < NQ; ++n) w[n] = split8(x[0][n], x[1][n]);
-                    results<ND, S::kPiece, NQ>(tile, m, h, w, acc);
-                };
-                add(gg, tv, ao);    // H v
-                add(s, tvv, ao);    // p vv
-                add(ee, tk, aq);    // U k
-                add(dp, tvk, aq);   // ds vk
+                results<ND, S::kPiece, ND <= 4, NQ>(tv, m, h, gg, ao);    // H v
+                results<ND, S::kPiece, ND <= 4, NQ>(tvv, m, h, s, ao);    // p vv
+                results<ND, S::kPiece, ND <= 4, NQ>(tk, m, h, ee, aq);    // U k
+                results<ND, S::kPiece, ND <= 4, NQ>(tvk, m, h, dp, aq);   // ds vk
             }
         }, x.k, x.v, x.vk, x.vv);
 
@@ -204,11 +198,11 @@ __global__ __launch_bounds__(64 * kTeam, attn_waves(AttnPass::second_keys, ND, I
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int n = 0; n < NT; ++n) s[t][n] = dp[t][n] = gg[t][n] = ee[t][n] = f32x4_t{};
-            scores<ND, S::kPiece, NT>(tq, m, h, ok, s);
-            scores<ND, S::kPiece, NT>(ta, m, h, ok, gg);
-            scores<ND, S::kPiece, NT>(tq, m, h, ovk, gg);
-            scores<ND, S::kPiece, NT>(td, m, h, ov, dp);
-            scores<ND, S::kPiece, NT>(td, m, h, ovv, ee);
+            scores<ND, S::kPiece, false, NT>(tq, m, h, ok, s);
+            scores<ND, S::kPiece, false, NT>(ta, m, h, ok, gg);
+            scores<ND, S::kPiece, false, NT>(tq, m, h, ovk, gg);
+            scores<ND, S::kPiece, false, NT>(td, m, h, ov, dp);
+            scores<ND, S::kPiece, false, NT>(td, m, h, ovv, ee);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 const float* const nums = numbers + 16 * t + 4 * h;
@@ -232,15 +226,9 @@ __global__ __launch_bounds__(64 * kTeam, attn_waves(AttnPass::second_keys, ND, I
                         bias[n] = bias[n] + ee[t][n][j];
                     }
             }
-            Split8 w[NT];
-            const auto sum = [&](const f32x4_t (&x)[2][NT], const uint16_t* tile, f32x4_t (&acc)[NT][ND]) {
-#pragma unroll
-                for (int n = 0; n < NT; ++n) w[n] = split8(x[0][n], x[1][n]);
-                results<ND, S::kPiece, NT>(tile, m, h, w, acc);
-            };
-            sum(gg, td, av);   // H dout
-            sum(ee, tq, ak);   // U q
-            sum(dp, ta, ak);   // ds vq
+            results<ND, S::kPiece, false, NT>(td, m, h, gg, av);   // H dout
+            results<ND, S::kPiece, false, NT>(tq, m, h, ee, ak);   // U q
+            results<ND, S::kPiece, false, NT>(ta, m, h, dp, ak);   // ds vq
         }, x.q, x.dout, x.vq);
 
 #pragma unroll

@@ -35,9 +35,11 @@ __global__ __launch_bounds__(kAttnTile * (4 * KS + 1)) void images_kernel(AttnAr
     for (int64_t tile = blockIdx.x; tile < all; tile += gridDim.x) {
         const int64_t head = tile / tiles, r = (tile - head * tiles) * kAttnTile + row;
         const int b = (int)(head / a.kv_heads), g = (int)(head - (int64_t)b * a.kv_heads);
+        const int limit = is_key ? keys_of(a, b) : 0;
+        if (is_key && r - row >= limit) continue;   // (not read)
         f32x4_t u = {}, v = {};
         if (col < a.dim && from.data != nullptr) {
-            if (is_key ? r < a.keys && key_term(a, b, (int)r, keys_of(a, b)) != minus_inf() : r < a.rows) {
+            if (is_key ? r < a.keys && key_term(a, b, (int)r, limit) != minus_inf() : r < a.rows) {
                 const float* const p = is_key ? key_ptr(from, b, g, r) : row_ptr(from, b, row_at(a, g, r));
                 u = load4(p, col, a.dim);
                 v = load4(p, col + 4, a.dim);

@@ -109,70 +109,103 @@ __device__ __forceinline__ void load_own(Split8 (&f)[Heads<ND>::KS], const float
                      : split8(f32x4_t{}, f32x4_t{});
 }
 
+// The A operands of a step: of the two tiles of 16 rows (scores), or of two
+// tiles of d (results).
+struct Step {
+    bf16x8_t a[2][3];
+};
+
+// AHEAD: the next step's operands are requested before the present step's
+// products begin, which then hide the reads; for passes whose registers hold
+// two steps. (Matrix instructions and reads of LDS keep their order across
+// this; arithmetic, memory and LDS writes pass.)
+template <bool AHEAD>
+__device__ __forceinline__ void keep_order()
+{
+    if constexpr (AHEAD) __builtin_amdgcn_sched_barrier(0x2 | 0x4 | 0x10 | 0x200);
+}
+
 // acc[t][n] += (streamed rows 16 t .. of `tile`) . own[n]; PS: elements of a
 // piece
-template <int ND, int PS, int NT>
+template <int ND, int PS, bool AHEAD, int NT>
 __device__ __forceinline__ void scores(const uint16_t* tile, int m, int h, const Split8 (&own)[NT][Heads<ND>::KS],
                                        f32x4_t (&acc)[2][NT])
 {
-    constexpr int RS = Heads<ND>::RS;
+    constexpr int RS = Heads<ND>::RS, KS = Heads<ND>::KS;
     const uint16_t* const at = tile + m * RS + 8 * h;
     f32x4_t* to[2][NT];
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int n = 0; n < NT; ++n) to[t][n] = &acc[t][n];
-#pragma unroll
-    for (int c = 0; c < Heads<ND>::KS; ++c) {
-        bf16x8_t a[2][3];
-        const Split8* b[NT];
+    const auto load = [&](int c, Step& s) {
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int i = 0; i < 3; ++i) a[t][i] = *reinterpret_cast<const bf16x8_t*>(at + i * PS + 16 * t * RS + 32 * c);
+            for (int i = 0; i < 3; ++i) s.a[t][i] = *reinterpret_cast<const bf16x8_t*>(at + i * PS + 16 * t * RS + 32 * c);
+    };
+    Step step[2];
+    if (AHEAD) load(0, step[0]);
+#pragma unroll
+    for (int c = 0; c < KS; ++c) {
+        if (!AHEAD) load(c, step[c & 1]);
+        if (AHEAD && c + 1 < KS) load(c + 1, step[(c + 1) & 1]);
+        keep_order<AHEAD>();
+        const Split8* b[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n) b[n] = &own[n][c];
-        product6<2, NT>(a, b, to);
+        product6<2, NT>(step[c & 1].a, b, to);
     }
 }
 
-// acc[n] += (the 32 streamed rows at `tile`)^T . w[n]
-template <int ND, int PS, int NT>
-__device__ __forceinline__ void results(const uint16_t* tile, int m, int h, const Split8 (&w)[NT], f32x4_t (&acc)[NT][ND])
+// acc[n] += (the 32 streamed rows at `tile`)^T . w[n], w from two score tiles
+template <int ND, int PS, bool AHEAD, int NT>
+__device__ __forceinline__ void results(const uint16_t* tile, int m, int h, const f32x4_t (&x)[2][NT], f32x4_t (&acc)[NT][ND])
 {
     typedef __attribute__((address_space(3))) i16x4_t lds_t;
-    constexpr int RS = Heads<ND>::RS, PAIRS = ND / 2;
+    constexpr int RS = Heads<ND>::RS, STEPS = (ND + 1) / 2;
     const uint16_t* const at = tile + (4 * h + (m >> 2)) * RS + 4 * (m & 3);
-    const Split8* b[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) b[n] = &w[n];
-    const auto load = [&](int t, bf16x8_t (&a)[3]) {
-#pragma unroll
-        for (int i = 0; i < 3; ++i) {
-            const i16x4_t u = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t*)(at + i * PS + 16 * t));
-            const i16x4_t v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t*)(at + i * PS + 16 * RS + 16 * t));
-            a[i] = __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(u, v, 0, 1, 2, 3, 4, 5, 6, 7));
-        }
-    };
-#pragma unroll
-    for (int p = 0; p < PAIRS; ++p) {
-        bf16x8_t a[2][3];
-        f32x4_t* to[2][NT];
+    const auto load = [&](int p, Step& s) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            load(2 * p + t, a[t]);
+            if (2 * p + t >= ND) continue;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) to[t][n] = &acc[n][2 * p + t];
+            for (int i = 0; i < 3; ++i) {
+                const uint16_t* const from = at + i * PS + 16 * (2 * p + t);
+                const i16x4_t u = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t*)from);
+                const i16x4_t v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t*)(from + 16 * RS));
+                s.a[t][i] = __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(u, v, 0, 1, 2, 3, 4, 5, 6, 7));
+            }
         }
-        product6<2, NT>(a, b, to);
-    }
-    if constexpr (ND % 2 == 1) {
-        bf16x8_t a[1][3];
-        f32x4_t* to[1][NT];
-        load(ND - 1, a[0]);
+    };
+    Step step[2];
+    if (AHEAD) load(0, step[0]);
+    Split8 w[NT];
+    const Split8* b[NT];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) to[0][n] = &acc[n][ND - 1];
-        product6<1, NT>(a, b, to);
+    for (int n = 0; n < NT; ++n) {
+        w[n] = split8(x[0][n], x[1][n]);
+        b[n] = &w[n];
+    }
+#pragma unroll
+    for (int p = 0; p < STEPS; ++p) {
+        if (!AHEAD) load(p, step[p & 1]);
+        if (AHEAD && p + 1 < STEPS) load(p + 1, step[(p + 1) & 1]);
+        keep_order<AHEAD>();
+        if (2 * p + 1 < ND) {
+            f32x4_t* to[2][NT];
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) to[t][n] = &acc[n][2 * p + t];
+            product6<2, NT>(step[p & 1].a, b, to);
+        } else {
+            f32x4_t* to[1][NT];
+            const bf16x8_t one[1][3] = {{step[p & 1].a[0][0], step[p & 1].a[0][1], step[p & 1].a[0][2]}};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) to[0][n] = &acc[n][2 * p < ND ? 2 * p : 0];
+            product6<1, NT>(one, b, to);
+        }
     }
 }
 
