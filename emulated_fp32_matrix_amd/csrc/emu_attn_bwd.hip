@@ -131,8 +131,8 @@ __global__ __launch_bounds__(64 * kTeam, attn_waves(AttnPass::keys, ND, IMAGES))
             f32x4_t s[2][NT], dp[2][NT];
 #pragma unroll
             for (int n = 0; n < NT; ++n) s[0][n] = s[1][n] = dp[0][n] = dp[1][n] = f32x4_t{};
-            scores<ND, S::kPiece, false, NT>(arrays, m, h, ok, s);
-            scores<ND, S::kPiece, false, NT>(arrays + S::kArray, m, h, ov, dp);
+            scores<ND, S::kPiece, NT == 1, NT>(arrays, m, h, ok, s);
+            scores<ND, S::kPiece, NT == 1, NT>(arrays + S::kArray, m, h, ov, dp);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 const float* const row = numbers + 16 * t + 4 * h;
@@ -149,8 +149,8 @@ __global__ __launch_bounds__(64 * kTeam, attn_waves(AttnPass::keys, ND, IMAGES))
                         bias[n] = bias[n] + dp[t][n][j];
                     }
             }
-            results<ND, S::kPiece, false, NT>(arrays + S::kArray, m, h, s, av);
-            results<ND, S::kPiece, false, NT>(arrays, m, h, dp, ak);
+            results<ND, S::kPiece, NT == 1, NT>(arrays + S::kArray, m, h, s, av);
+            results<ND, S::kPiece, NT == 1, NT>(arrays, m, h, dp, ak);
         }, q, dout);
 
 #pragma unroll

@@ -33,7 +33,7 @@ enum class AttnPass { forward, rows, keys, second_rows, second_keys };
 // a SIMD.
 constexpr int attn_tiles(AttnPass pass, int dim)
 {
-    return dim <= (pass == AttnPass::forward ? 96 : pass == AttnPass::rows || pass == AttnPass::keys ? 64 : 32) ? 2 : 1;
+    return dim <= (pass == AttnPass::forward ? 96 : pass == AttnPass::rows ? 64 : 32) ? 2 : 1;
 }
 // Waves of a SIMD that the registers are divided among: one where even a tile
 // each of wide heads does not fit half of them.
