@@ -55,9 +55,17 @@ struct AttnPlan {
 AttnPlan attn_plan(const AttnArgs& a, AttnPass pass);
 
 // Tiles of 32 streamed rows of n arrays as they lie in LDS, split into three
-// BF16 pieces: [array][piece][row][attn_image_row], in whole KB.
+// BF16 pieces: [array][piece][row][attn_image_row], in whole KB. Group i of
+// eight elements of row r lies at group i ^ attn_image_place(steps of 32 in a
+// row, r): with rows of whole 128 bytes, eight neighbouring rows' group i at
+// eight places, and four rows' pairs of groups at four; in rows of 64 (or 192)
+// bytes, which alternate between the banks' halves, four and two.
 constexpr int kAttnTile = 32;
-constexpr int attn_image_row(int dim) { return (dim + 31) / 32 * 32 + 8; }
+constexpr int attn_image_row(int dim) { return (dim + 31) / 32 * 32; }
+constexpr __host__ __device__ int attn_image_place(int steps, int r)
+{
+    return steps % 2 == 0 ? 2 * (r & 3) + (r >> 2 & 1) : 2 * (r >> 1 & 1) + (r >> 2 & 1);
+}
 constexpr int64_t attn_image_bytes(int dim, int n)
 {
     return ((int64_t)n * 3 * kAttnTile * attn_image_row(dim) * 2 + 1023) / 1024 * 1024;

@@ -4,7 +4,7 @@
 // and ends, and the keys that take no part out of their loops, which copy the
 // images as they are.
 //
-// Bound by memory: 4 bytes read and 6 to 7.5 written per element.
+// Bound by memory: 4 bytes read and 6 written per element.
 #include "emu_attn_split.h"
 
 namespace emu {
@@ -19,11 +19,10 @@ struct ImageArrays {
 };
 
 // A workgroup makes one array's part of an image, eight elements a thread.
-// (The rows' ends are written too: whole lines.)
 template <int KS>
-__global__ __launch_bounds__(kAttnTile * (4 * KS + 1)) void images_kernel(AttnArgs a, ImageArrays x)
+__global__ __launch_bounds__(kAttnTile * 4 * KS) void images_kernel(AttnArgs a, ImageArrays x)
 {
-    constexpr int RS = 32 * KS + 8;
+    constexpr int RS = 32 * KS;
     const int n = blockIdx.y;
     const bool is_key = n < x.keys;
     emu_heads_t from = x.of[0];   // (chosen, not indexed: arguments stay in scalar registers)
@@ -48,7 +47,8 @@ __global__ __launch_bounds__(kAttnTile * (4 * KS + 1)) void images_kernel(AttnAr
         const Split8 s = split8<true>(u, v);
         char* const image = is_key ? x.to_keys + tile * attn_image_bytes(32 * KS, x.keys)
                                    : x.to_rows + tile * attn_image_bytes(32 * KS, x.all - x.keys);
-        uint16_t* const to = reinterpret_cast<uint16_t*>(image) + ((is_key ? n : n - x.keys) * 3 * kAttnTile + row) * RS + col;
+        uint16_t* const to = reinterpret_cast<uint16_t*>(image) + ((is_key ? n : n - x.keys) * 3 * kAttnTile + row) * RS +
+                             8 * (col / 8 ^ attn_image_place(KS, row));
 #pragma unroll
         for (int p = 0; p < 3; ++p) *reinterpret_cast<bf16x8_t*>(to + p * kAttnTile * RS) = s.p[p];
     }
@@ -58,7 +58,7 @@ template <int KS>
 void launch_images(const AttnArgs& a, const ImageArrays& x, hipStream_t s)
 {
     const int64_t tiles = x.key_tiles > x.row_tiles ? x.key_tiles : x.row_tiles, all = (int64_t)a.batch * a.kv_heads * tiles;
-    images_kernel<KS><<<dim3((unsigned)(all < 65536 ? all : 65536), x.all), kAttnTile * (4 * KS + 1), 0, s>>>(a, x);
+    images_kernel<KS><<<dim3((unsigned)(all < 65536 ? all : 65536), x.all), kAttnTile * 4 * KS, 0, s>>>(a, x);
 }
 
 int64_t tiles_of(int64_t n) { return (n + kAttnTile - 1) / kAttnTile; }

@@ -92,11 +92,13 @@ __device__ __forceinline__ void product6(const bf16x8_t (&a)[K][3], const Split8
 }
 
 // ND tiles of 16 cover a head; scores take KS steps of 32 of it. A tile in LDS
-// has [array][piece][row][RS]: RS is eight more than a multiple of 32, so that
-// the 16 rows of a score's reads lie on different banks.
+// has [array][piece][row][RS], with a row's groups of eight elements (16 bytes)
+// exchanged by its number (attn_image_place), so that neither the 16-byte reads
+// of eight rows (scores) nor the transposing reads of four (results) meet in a
+// bank: with rows of RS + 8 in plain order the latter took twice as long.
 template <int ND>
 struct Heads {
-    static constexpr int KS = (ND + 1) / 2, RS = 32 * KS + 8;
+    static constexpr int KS = (ND + 1) / 2, RS = 32 * KS;
 };
 
 // A wave's own row as the B operand of scores; not `valid`: zeros.
@@ -132,7 +134,8 @@ __device__ __forceinline__ void scores(const uint16_t* tile, int m, int h, const
                                        f32x4_t (&acc)[2][NT])
 {
     constexpr int RS = Heads<ND>::RS, KS = Heads<ND>::KS;
-    const uint16_t* const at = tile + m * RS + 8 * h;
+    const uint16_t* const at = tile + m * RS;
+    const int place = 8 * (h ^ attn_image_place(KS, m));
     f32x4_t* to[2][NT];
 #pragma unroll
     for (int t = 0; t < 2; ++t)
@@ -142,7 +145,7 @@ __device__ __forceinline__ void scores(const uint16_t* tile, int m, int h, const
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int i = 0; i < 3; ++i) s.a[t][i] = *reinterpret_cast<const bf16x8_t*>(at + i * PS + 16 * t * RS + 32 * c);
+            for (int i = 0; i < 3; ++i) s.a[t][i] = *reinterpret_cast<const bf16x8_t*>(at + (place ^ 32 * c) + i * PS + 16 * t * RS);
     };
     Step step[2];
     if (AHEAD) load(0, step[0]);
@@ -164,14 +167,15 @@ __device__ __forceinline__ void results(const uint16_t* tile, int m, int h, cons
 {
     typedef __attribute__((address_space(3))) i16x4_t lds_t;
     constexpr int RS = Heads<ND>::RS, STEPS = (ND + 1) / 2;
-    const uint16_t* const at = tile + (4 * h + (m >> 2)) * RS + 4 * (m & 3);
+    const int row = 4 * h + (m >> 2), place = 8 * ((m >> 1 & 1) ^ attn_image_place(Heads<ND>::KS, row));
+    const uint16_t* const at = tile + row * RS + 4 * (m & 1);
     const auto load = [&](int p, Step& s) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             if (2 * p + t >= ND) continue;
 #pragma unroll
             for (int i = 0; i < 3; ++i) {
-                const uint16_t* const from = at + i * PS + 16 * (2 * p + t);
+                const uint16_t* const from = at + (place ^ 16 * (2 * p + t)) + i * PS;
                 const i16x4_t u = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t*)from);
                 const i16x4_t v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t*)(from + 16 * RS));
                 s.a[t][i] = __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(u, v, 0, 1, 2, 3, 4, 5, 6, 7));
@@ -428,8 +432,11 @@ struct Stream {
                     for (int e = 0; e < kEach; ++e) {
                         const Split4 s = split4(tiles[i].v[e]);
 #pragma unroll
-                        for (int p = 0; p < 3; ++p)
-                            *reinterpret_cast<u32x2_t*>(arrays + i * kArray + p * kPiece + (row() + e * kStep) * RS + col()) = s.p[p];
+                        for (int p = 0; p < 3; ++p) {
+                            const int r = row() + e * kStep;
+                            uint16_t* const to = arrays + i * kArray + p * kPiece + r * RS;
+                            *reinterpret_cast<u32x2_t*>(to + 8 * (col() / 8 ^ attn_image_place(Heads<ND>::KS, r)) + col() % 8) = s.p[p];
+                        }
                     }
                 }
                 if (T::thread() < kStreamRows) {
