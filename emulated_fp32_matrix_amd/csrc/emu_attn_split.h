@@ -94,8 +94,9 @@ __device__ __forceinline__ void product6(const bf16x8_t (&a)[K][3], const Split8
 // ND tiles of 16 cover a head; scores take KS steps of 32 of it. A tile in LDS
 // has [array][piece][row][RS], with a row's groups of eight elements (16 bytes)
 // exchanged by its number (attn_image_place), so that neither the 16-byte reads
-// of eight rows (scores) nor the transposing reads of four (results) meet in a
-// bank: with rows of RS + 8 in plain order the latter took twice as long.
+// of sixteen rows (scores) nor the transposing reads of eight (results) meet in
+// a bank. With rows of RS + 8 in plain order the latter took twice as long: 384
+// us of 2 x 16 x 2,048 x 4,096 x 64 forward for 366, 783 by keys for 675.
 template <int ND>
 struct Heads {
     static constexpr int KS = (ND + 1) / 2, RS = 32 * KS;
