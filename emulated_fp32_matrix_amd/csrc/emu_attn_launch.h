@@ -57,15 +57,16 @@ AttnPlan attn_plan(const AttnArgs& a, AttnPass pass);
 // Tiles of 32 streamed rows of n arrays as they lie in LDS, split into three
 // BF16 pieces: [array][piece][row][attn_image_row], in whole KB. Group i of
 // eight elements of row r lies at group i ^ attn_image_place(steps of 32 in a
-// row, r). LDS has 64 banks of 4 bytes: rows of 128 bytes alternate between
-// their halves, so the rows of one half (r, r + 2, ..) have group i at eight
-// places, and eight rows their pairs of groups at four a half; rows of 64 (or
-// 192) bytes take the banks' quarters, which leaves four places and two.
+// row, r). LDS has 64 banks of 4 bytes: a row of 256 bytes takes them all, so 16
+// rows have group i at 16 places and eight rows their pairs of groups at eight;
+// rows of 128 bytes alternate between the banks' halves, which leaves eight
+// places and four; rows of 64 (or 192) take their quarters: four and two.
 constexpr int kAttnTile = 32;
 constexpr int attn_image_row(int dim) { return (dim + 31) / 32 * 32; }
 constexpr __host__ __device__ int attn_image_place(int steps, int r)
 {
-    return steps % 2 == 0 ? 2 * (r >> 1 & 3) + (r >> 3 & 1) : 2 * (r >> 2 & 1) + (r >> 3 & 1);
+    const int shift = steps % 4 == 0 ? 0 : steps % 2 == 0 ? 1 : 2;   // rows beside each other
+    return 2 * ((r & 7) >> shift) + (r >> 3 & 1);
 }
 constexpr int64_t attn_image_bytes(int dim, int n)
 {
