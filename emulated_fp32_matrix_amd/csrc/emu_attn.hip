@@ -230,22 +230,42 @@ __global__ __launch_bounds__(256) void join_kernel(AttnJoins j)
 
 unsigned join_grid(int64_t groups) { return (unsigned)(groups < 65536 ? groups : 65536); }
 
-// Ranges of the other side: enough pieces for 2,048 waves (256 compute units
-// of 8), none shorter than `least` of the streamed side. Where sequences differ
-// in length (`ragged`) twice as many, of 512 and more: 21 x 8 x 200 rows x up
-// to 1,918 keys x 48 forward 115 -> 97 us with three ranges; ranges of 259 keys
-// instead of 388 cost 14 x 771 rows x up to 777 keys 39 -> 44.
-int splits_for(int64_t waves, int64_t other, int64_t least, bool ragged)
+// Ranges of the other side for a wave each of few rows: as many as make 2,048
+// waves (256 compute units of 8), none shorter than 128 keys.
+int few_splits(int64_t waves, int64_t other)
 {
-    const int64_t n = waves > 0 ? waves : 1;
-    const auto limited = [](int64_t s, int64_t most) { return s < most ? s : most; };
-    int64_t s = limited(2048 / n, other / least);
-    if (ragged) {
-        const int64_t more = limited(4096 / n, other / 512);
-        s = s > more ? s : more;
+    int64_t s = 2048 / waves;
+    if (s > other / 128) s = other / 128;
+    return s < 1 ? 1 : s > kMostSplits ? kMostSplits : (int)s;
+}
+
+// Ranges of the other side for teams: the number with the least time, in tiles
+// of the streamed side. The compute units have `resident` teams each at once;
+// such a round takes a range and about 6 tiles' time to begin and end a piece,
+// a last one with a compute unit per team 0.8 of it (0.67 to 0.88 measured).
+// The join takes 2 tiles' time and 0.003 a piece. Of sequences that differ in
+// length (`ragged`) the long ones end last, by half a range on average.
+// Measured against at least 256 of the other side a range and 2,048 waves: 3 x
+// 8 heads of 333 x 515 x 40, forward 27 -> 23 us, second order by rows 89 -> 71;
+// 7 x 6 of 257 x 777 x 80 ragged, second order by keys 143 -> 137; 21 x 8 of 200
+// x 1,918 x 48 ragged, second order by rows 657 -> 614.
+int splits_for(int64_t teams, int64_t other, int resident, bool ragged)
+{
+    constexpr int kUnits = 256;
+    const int64_t tiles = (other + kStreamRows - 1) / kStreamRows, slots = kUnits * resident;
+    int best = 1;
+    double least = 0.0;
+    for (int s = 1; s <= kMostSplits && (s == 1 || s <= tiles); ++s) {
+        const int64_t n = teams * s, rest = n % slots, range = (tiles + s - 1) / s;
+        const double rounds = (double)(n / slots) + (rest == 0 ? 0.0 : rest <= kUnits && resident > 1 ? 0.8 : 1.0);
+        const double time = rounds * (double)(range + 6) + (ragged ? 0.5 * (double)range : 0.0) + (s > 1 ? 2.0 + 0.003 * (double)n : 0.0);
+        if (s == 1 || time < least) {
+            best = s;
+            least = time;
+        }
+        if (n > 8 * slots) break;   // (the join alone costs more from here)
     }
-    s = limited(s, kMostSplits);
-    return s < 1 ? 1 : (int)s;
+    return best;
 }
 
 }  // namespace
@@ -261,8 +281,10 @@ AttnPlan attn_plan(const AttnArgs& a, AttnPass pass)
     const int64_t each = p.waves * p.tiles * 16;
     p.own = (own + each - 1) / each;
     p.images = p.waves == 4 && p.own >= kImageTeams;
-    p.splits = splits_for((int64_t)a.batch * a.kv_heads * p.own * p.waves, other, p.images ? 256 : 128,
-                          !keys && a.lengths != nullptr);
+    const int64_t pieces = (int64_t)a.batch * a.kv_heads * p.own;
+    p.splits = pieces == 0      ? 1
+               : p.waves == 1 ? few_splits(pieces, other)
+                              : splits_for(pieces, other, attn_waves(pass, (a.dim + 15) / 16, p.images), !keys && a.lengths != nullptr);
     return p;
 }
 
