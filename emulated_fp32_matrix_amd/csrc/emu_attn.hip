@@ -23,7 +23,7 @@ __global__ __launch_bounds__(64 * kTeam, attn_waves(AttnPass::forward, ND, IMAGE
                                                          float* partial)
 {
     using T = Team<kTeam>;
-    using S = Stream<ND, 2, 1, true, IMAGES>;
+    using S = Stream<ND, 2, 1, true, IMAGES, attn_waves(AttnPass::forward, ND, IMAGES)>;
     __shared__ __attribute__((aligned(16))) char lds[S::kBuffers * S::kBytes];
     S stream{lds};
     stream.clear();

@@ -17,7 +17,7 @@ __global__ __launch_bounds__(64 * kTeam, attn_waves(AttnPass::rows, ND, IMAGES))
                                                       const float* stats, float* delta, float* dq, float* partial)
 {
     using T = Team<kTeam>;
-    using S = Stream<ND, 2, 1, true, IMAGES>;
+    using S = Stream<ND, 2, 1, true, IMAGES, attn_waves(AttnPass::rows, ND, IMAGES)>;
     __shared__ __attribute__((aligned(16))) char lds[S::kBuffers * S::kBytes];
     S stream{lds};
     stream.clear();
@@ -88,7 +88,7 @@ __global__ __launch_bounds__(64 * kTeam, attn_waves(AttnPass::keys, ND, IMAGES))
                                                       const float* stats, const float* delta, float* dk, float* dv, float* db)
 {
     using T = Team<kTeam>;
-    using S = Stream<ND, 2, 3, false, IMAGES>;
+    using S = Stream<ND, 2, 3, false, IMAGES, attn_waves(AttnPass::keys, ND, IMAGES)>;
     __shared__ __attribute__((aligned(16))) char lds[S::kBuffers * S::kBytes];
     S stream{lds};
     stream.clear();

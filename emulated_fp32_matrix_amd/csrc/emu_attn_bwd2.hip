@@ -19,7 +19,8 @@ __global__ __launch_bounds__(64 * kTeam, attn_waves(AttnPass::second_rows, ND, I
                                                       float* go, float* gq)
 {
     using T = Team<kTeam>;
-    using S = Stream<ND, 4, 2, true, IMAGES>;
+    using S = Stream<ND, 4, 2, true, IMAGES, attn_waves(AttnPass::second_rows, ND, IMAGES)>;
+    constexpr bool AHEAD = ND <= 4 || attn_waves(AttnPass::second_rows, ND, IMAGES) == 1;
     constexpr int KS = Heads<ND>::KS;
     __shared__ __attribute__((aligned(16))) char lds[S::kBuffers * S::kBytes];
     S stream{lds};
@@ -79,11 +80,11 @@ __global__ __launch_bounds__(64 * kTeam, attn_waves(AttnPass::second_rows, ND, I
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int n = 0; n < NQ; ++n) s[t][n] = dp[t][n] = gg[t][n] = ee[t][n] = f32x4_t{};
-            scores<ND, S::kPiece, ND <= 4, NQ>(tk, m, h, oq, s);
-            scores<ND, S::kPiece, ND <= 4, NQ>(tk, m, h, oa, gg);
-            scores<ND, S::kPiece, ND <= 4, NQ>(tvk, m, h, oq, gg);
-            scores<ND, S::kPiece, ND <= 4, NQ>(tv, m, h, od, dp);
-            scores<ND, S::kPiece, ND <= 4, NQ>(tvv, m, h, od, ee);
+            scores<ND, S::kPiece, AHEAD, NQ>(tk, m, h, oq, s);
+            scores<ND, S::kPiece, AHEAD, NQ>(tk, m, h, oa, gg);
+            scores<ND, S::kPiece, AHEAD, NQ>(tvk, m, h, oq, gg);
+            scores<ND, S::kPiece, AHEAD, NQ>(tv, m, h, od, dp);
+            scores<ND, S::kPiece, AHEAD, NQ>(tvv, m, h, od, ee);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 const f32x4_t vadd = *reinterpret_cast<const f32x4_t*>(numbers + kStreamRows + 16 * t + 4 * h);
@@ -107,10 +108,10 @@ __global__ __launch_bounds__(64 * kTeam, attn_waves(AttnPass::second_rows, ND, I
                     }
             }
             if constexpr (!SUMS) {
-                results<ND, S::kPiece, ND <= 4, NQ>(tv, m, h, gg, ao);    // H v
-                results<ND, S::kPiece, ND <= 4, NQ>(tvv, m, h, s, ao);    // p vv
-                results<ND, S::kPiece, ND <= 4, NQ>(tk, m, h, ee, aq);    // U k
-                results<ND, S::kPiece, ND <= 4, NQ>(tvk, m, h, dp, aq);   // ds vk
+                results<ND, S::kPiece, AHEAD, NQ>(tv, m, h, gg, ao);    // H v
+                results<ND, S::kPiece, AHEAD, NQ>(tvv, m, h, s, ao);    // p vv
+                results<ND, S::kPiece, AHEAD, NQ>(tk, m, h, ee, aq);    // U k
+                results<ND, S::kPiece, AHEAD, NQ>(tvk, m, h, dp, aq);   // ds vk
             }
         }, x.k, x.v, x.vk, x.vv);
 
@@ -139,7 +140,8 @@ __global__ __launch_bounds__(64 * kTeam, attn_waves(AttnPass::second_keys, ND, I
                                                       const float* sums, int sum_splits, float* gk, float* gv, float* gb)
 {
     using T = Team<kTeam>;
-    using S = Stream<ND, 3, 5, false, IMAGES>;
+    using S = Stream<ND, 3, 5, false, IMAGES, attn_waves(AttnPass::second_keys, ND, IMAGES)>;
+    constexpr bool AHEAD = attn_waves(AttnPass::second_keys, ND, IMAGES) == 1;
     constexpr int KS = Heads<ND>::KS;
     __shared__ __attribute__((aligned(16))) char lds[S::kBuffers * S::kBytes];
     S stream{lds};
@@ -198,11 +200,11 @@ __global__ __launch_bounds__(64 * kTeam, attn_waves(AttnPass::second_keys, ND, I
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int n = 0; n < NT; ++n) s[t][n] = dp[t][n] = gg[t][n] = ee[t][n] = f32x4_t{};
-            scores<ND, S::kPiece, false, NT>(tq, m, h, ok, s);
-            scores<ND, S::kPiece, false, NT>(ta, m, h, ok, gg);
-            scores<ND, S::kPiece, false, NT>(tq, m, h, ovk, gg);
-            scores<ND, S::kPiece, false, NT>(td, m, h, ov, dp);
-            scores<ND, S::kPiece, false, NT>(td, m, h, ovv, ee);
+            scores<ND, S::kPiece, AHEAD, NT>(tq, m, h, ok, s);
+            scores<ND, S::kPiece, AHEAD, NT>(ta, m, h, ok, gg);
+            scores<ND, S::kPiece, AHEAD, NT>(tq, m, h, ovk, gg);
+            scores<ND, S::kPiece, AHEAD, NT>(td, m, h, ov, dp);
+            scores<ND, S::kPiece, AHEAD, NT>(td, m, h, ovv, ee);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 const float* const nums = numbers + 16 * t + 4 * h;
@@ -226,9 +228,9 @@ __global__ __launch_bounds__(64 * kTeam, attn_waves(AttnPass::second_keys, ND, I
                         bias[n] = bias[n] + ee[t][n][j];
                     }
             }
-            results<ND, S::kPiece, false, NT>(td, m, h, gg, av);   // H dout
-            results<ND, S::kPiece, false, NT>(tq, m, h, ee, ak);   // U q
-            results<ND, S::kPiece, false, NT>(ta, m, h, dp, ak);   // ds vq
+            results<ND, S::kPiece, AHEAD, NT>(td, m, h, gg, av);   // H dout
+            results<ND, S::kPiece, AHEAD, NT>(tq, m, h, ee, ak);   // U q
+            results<ND, S::kPiece, AHEAD, NT>(ta, m, h, dp, ak);   // ds vq
         }, x.q, x.dout, x.vq);
 
 #pragma unroll

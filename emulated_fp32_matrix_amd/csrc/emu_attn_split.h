@@ -264,7 +264,7 @@ __device__ __forceinline__ void stagger()
 // reads the arrays themselves and splits them on the way; where registers
 // allow, the next tile is requested before the present one is used.
 // Two buffers in LDS, so that one barrier a tile does, where they leave room
-// for two workgroups, or one buffer alone does not.
+// for the RESIDENT workgroups that registers hold, or one buffer alone does not.
 
 constexpr int kStreamRows = kAttnTile;
 
@@ -278,7 +278,7 @@ struct StreamRows {
 
 constexpr int kTeam = 4;   // waves that share a streamed tile
 
-template <int ND, int N, int X, bool KEYS, bool IMAGES>
+template <int ND, int N, int X, bool KEYS, bool IMAGES, int RESIDENT>
 struct Stream {
     using T = Team<kTeam>;
     static constexpr int RS = Heads<ND>::RS, kPiece = kStreamRows * RS, kArray = 3 * kPiece;
@@ -288,8 +288,8 @@ struct Stream {
     static constexpr int kArrays = IMAGES ? (int)attn_image_bytes(16 * ND, N) : N * kArray * 2;
     static constexpr int kBytes = kArrays + X * kStreamRows * 4;
     static constexpr bool kAhead = N * kEach <= 8;
-    static constexpr int kHalf = 80 * 1024;   // of a compute unit's LDS
-    static constexpr bool kTwo = IMAGES ? 2 * kBytes <= kHalf || (kBytes > kHalf && 2 * kBytes <= 2 * kHalf) : kAhead && 2 * kBytes <= kHalf;
+    static constexpr int kLds = 160 * 1024, kShare = kLds / RESIDENT;   // a compute unit's, a team's
+    static constexpr bool kTwo = (IMAGES || kAhead) && (2 * kBytes <= kShare || (IMAGES && kBytes > kShare && 2 * kBytes <= kLds));
     static constexpr int kBuffers = kTwo ? 2 : 1;
     static_assert(kBytes % 16 == 0, "buffers stay aligned");
     static_assert(RS == attn_image_row(16 * ND), "images are tiles as they lie in LDS");
