@@ -30,7 +30,7 @@ __global__ __launch_bounds__(64 * kTeam, attn_waves(AttnPass::forward, ND, IMAGE
     stagger();
     const int lane = threadIdx.x & 63, m = lane & 15, h = lane >> 4;
 
-    T::each_piece((int64_t)a.batch * a.kv_heads * plan.own * plan.splits, [&](int64_t piece) {
+    T::each_piece(pieces_of(a, plan), plan.run, [&](int64_t piece) {
         const Piece at = piece_of(a, plan, piece);
         const int limit = keys_of(a, at.b);
         int64_t lo, hi;
@@ -285,6 +285,10 @@ AttnPlan attn_plan(const AttnArgs& a, AttnPass pass)
     p.splits = pieces == 0      ? 1
                : p.waves == 1 ? few_splits(pieces, other)
                               : splits_for(pieces, other, attn_waves(pass, (a.dim + 15) / 16, p.images), !keys && a.lengths != nullptr);
+    // a key head's pieces, if there are 16 such runs for each XCD; a wave's few
+    // rows share their keys with no other piece
+    const int64_t head = p.own * p.splits, even = pieces * p.splits / 128;
+    p.run = p.waves == 1 ? 1 : head < even ? head : even < 1 ? 1 : even;
     return p;
 }
 
@@ -313,8 +317,7 @@ hipError_t launch_attn_forward(const AttnArgs& a, const AttnPlan& p, emu_heads_t
         e = launch_attn_few(a, p, q, k, v, out, stats, partial, s);
     } else {
         with_shape<AttnPass::forward>(a.dim, p, [&]<int ND, int NQ, bool IMAGES>() {
-            const int64_t n = (int64_t)a.batch * a.kv_heads * p.own * p.splits;
-            forward_kernel<ND, NQ, IMAGES><<<Team<kTeam>::grid(n), 64 * kTeam, 0, s>>>(
+            forward_kernel<ND, NQ, IMAGES><<<Team<kTeam>::grid(pieces_of(a, p), p.run), 64 * kTeam, 0, s>>>(
                 a, p, q, k, v, static_cast<const char*>(images), out, stats, partial);
         });
         e = hipGetLastError();

@@ -24,7 +24,7 @@ __global__ __launch_bounds__(64 * kTeam, attn_waves(AttnPass::rows, ND, IMAGES))
     stagger();
     const int lane = threadIdx.x & 63, m = lane & 15, h = lane >> 4;
 
-    T::each_piece((int64_t)a.batch * a.kv_heads * plan.own * plan.splits, [&](int64_t piece) {
+    T::each_piece(pieces_of(a, plan), plan.run, [&](int64_t piece) {
         const Piece at = piece_of(a, plan, piece);
         const int limit = keys_of(a, at.b);
         int64_t lo, hi;
@@ -95,7 +95,7 @@ __global__ __launch_bounds__(64 * kTeam, attn_waves(AttnPass::keys, ND, IMAGES))
     stagger();
     const int lane = threadIdx.x & 63, m = lane & 15, h = lane >> 4;
 
-    T::each_piece((int64_t)a.batch * a.kv_heads * plan.own * plan.splits, [&](int64_t piece) {
+    T::each_piece(pieces_of(a, plan), plan.run, [&](int64_t piece) {
         const Piece at = piece_of(a, plan, piece);
         const int limit = keys_of(a, at.b);
         int64_t lo, hi;
@@ -180,8 +180,7 @@ hipError_t launch_attn_backward_rows(const AttnArgs& a, const AttnPlan& p, emu_h
                                      const void* images, float* delta, float* dq, float* partial, hipStream_t s)
 {
     with_shape<AttnPass::rows>(a.dim, p, [&]<int ND, int NQ, bool IMAGES>() {
-        const int64_t n = (int64_t)a.batch * a.kv_heads * p.own * p.splits;
-        rows_kernel<ND, NQ, IMAGES><<<Team<kTeam>::grid(n), 64 * kTeam, 0, s>>>(a, p, dout, q, k, v, static_cast<const char*>(images), out, stats, delta, dq, partial);
+        rows_kernel<ND, NQ, IMAGES><<<Team<kTeam>::grid(pieces_of(a, p), p.run), 64 * kTeam, 0, s>>>(a, p, dout, q, k, v, static_cast<const char*>(images), out, stats, delta, dq, partial);
     });
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && p.splits > 1)
@@ -199,8 +198,7 @@ hipError_t launch_attn_backward_keys(const AttnArgs& a, const AttnPlan& p, emu_h
     float* const to_v = dv != nullptr && cut ? partial_v : dv;
     float* const to_b = join_bias ? partial_b : dbias;
     with_shape<AttnPass::keys>(a.dim, p, [&]<int ND, int NT, bool IMAGES>() {
-        const int64_t n = (int64_t)a.batch * a.kv_heads * p.own * p.splits;
-        keys_kernel<ND, NT, IMAGES><<<Team<kTeam>::grid(n), 64 * kTeam, 0, s>>>(a, p, dout, q, k, v, static_cast<const char*>(images), stats, delta, to_k, to_v, to_b);
+        keys_kernel<ND, NT, IMAGES><<<Team<kTeam>::grid(pieces_of(a, p), p.run), 64 * kTeam, 0, s>>>(a, p, dout, q, k, v, static_cast<const char*>(images), stats, delta, to_k, to_v, to_b);
     });
     hipError_t e = hipGetLastError();
     const int64_t n = (int64_t)a.batch * a.keys * a.kv_heads * a.dim;

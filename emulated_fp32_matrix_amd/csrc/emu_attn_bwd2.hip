@@ -29,7 +29,7 @@ __global__ __launch_bounds__(64 * kTeam, attn_waves(AttnPass::second_rows, ND, I
     const int lane = threadIdx.x & 63, m = lane & 15, h = lane >> 4;
     const int64_t all_rows = (int64_t)a.batch * a.queries * a.heads;
 
-    T::each_piece((int64_t)a.batch * a.kv_heads * plan.own * plan.splits, [&](int64_t piece) {
+    T::each_piece(pieces_of(a, plan), plan.run, [&](int64_t piece) {
         const Piece at = piece_of(a, plan, piece);
         const int limit = keys_of(a, at.b);
         int64_t lo, hi;
@@ -150,7 +150,7 @@ __global__ __launch_bounds__(64 * kTeam, attn_waves(AttnPass::second_keys, ND, I
     const int lane = threadIdx.x & 63, m = lane & 15, h = lane >> 4;
     const int64_t all_rows = (int64_t)a.batch * a.queries * a.heads;
 
-    T::each_piece((int64_t)a.batch * a.kv_heads * plan.own * plan.splits, [&](int64_t piece) {
+    T::each_piece(pieces_of(a, plan), plan.run, [&](int64_t piece) {
         const Piece at = piece_of(a, plan, piece);
         const int limit = keys_of(a, at.b);
         int64_t lo, hi;
@@ -252,15 +252,13 @@ __global__ __launch_bounds__(64 * kTeam, attn_waves(AttnPass::second_keys, ND, I
     });
 }
 
-int64_t pieces(const AttnArgs& a, const AttnPlan& p) { return (int64_t)a.batch * a.kv_heads * p.own * p.splits; }
-
 }  // namespace
 
 hipError_t launch_attn_second_sums(const AttnArgs& a, const AttnPlan& p, const AttnSeconds& x, const void* images,
                                    float* delta, float* sums, hipStream_t s)
 {
     with_shape<AttnPass::second_rows>(a.dim, p, [&]<int ND, int NQ, bool IMAGES>() {
-        rows_kernel<ND, NQ, IMAGES, true><<<Team<kTeam>::grid(pieces(a, p)), 64 * kTeam, 0, s>>>(a, p, x, static_cast<const char*>(images), delta, sums, nullptr, nullptr);
+        rows_kernel<ND, NQ, IMAGES, true><<<Team<kTeam>::grid(pieces_of(a, p), p.run), 64 * kTeam, 0, s>>>(a, p, x, static_cast<const char*>(images), delta, sums, nullptr, nullptr);
     });
     return hipGetLastError();
 }
@@ -273,7 +271,7 @@ hipError_t launch_attn_second_rows(const AttnArgs& a, const AttnPlan& p, const A
     float* const to_o = gdout != nullptr && cut ? partial_o : gdout;
     float* const to_q = gq != nullptr && cut ? partial_q : gq;
     with_shape<AttnPass::second_rows>(a.dim, p, [&]<int ND, int NQ, bool IMAGES>() {
-        rows_kernel<ND, NQ, IMAGES, false><<<Team<kTeam>::grid(pieces(a, p)), 64 * kTeam, 0, s>>>(
+        rows_kernel<ND, NQ, IMAGES, false><<<Team<kTeam>::grid(pieces_of(a, p), p.run), 64 * kTeam, 0, s>>>(
             a, p, x, static_cast<const char*>(images), const_cast<float*>(delta), const_cast<float*>(sums), to_o, to_q);
     });
     hipError_t e = hipGetLastError();
@@ -291,7 +289,7 @@ hipError_t launch_attn_second_keys(const AttnArgs& a, const AttnPlan& p, const A
     float* const to_v = gv != nullptr && cut ? partial_v : gv;
     float* const to_b = join_bias ? partial_b : gbias;
     with_shape<AttnPass::second_keys>(a.dim, p, [&]<int ND, int NT, bool IMAGES>() {
-        keys_kernel<ND, NT, IMAGES><<<Team<kTeam>::grid(pieces(a, p)), 64 * kTeam, 0, s>>>(a, p, x, static_cast<const char*>(images), delta, sums, sum_splits, to_k, to_v, to_b);
+        keys_kernel<ND, NT, IMAGES><<<Team<kTeam>::grid(pieces_of(a, p), p.run), 64 * kTeam, 0, s>>>(a, p, x, static_cast<const char*>(images), delta, sums, sum_splits, to_k, to_v, to_b);
     });
     hipError_t e = hipGetLastError();
     const int64_t n = (int64_t)a.batch * a.keys * a.kv_heads * a.dim;

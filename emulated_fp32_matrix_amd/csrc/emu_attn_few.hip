@@ -60,7 +60,7 @@ __global__ __launch_bounds__(256, ND <= 4 ? 2 : 1) void few_kernel(AttnArgs a, A
                                                                    emu_heads_t v, float* out, float* stats, float* partial)
 {
     const int lane = threadIdx.x & 63, m = lane & 15, h = lane >> 4;
-    T::each_piece((int64_t)a.batch * a.kv_heads * plan.own * plan.splits, [&](int64_t piece) {
+    T::each_piece(pieces_of(a, plan), plan.run, [&](int64_t piece) {
         const Piece at = piece_of(a, plan, piece);
         const int limit = keys_of(a, at.b);
         int64_t lo, hi;
@@ -152,7 +152,7 @@ __global__ __launch_bounds__(256, ND <= 4 ? 2 : 1) void few_kernel(AttnArgs a, A
 hipError_t launch_attn_few(const AttnArgs& a, const AttnPlan& p, emu_heads_t q, emu_heads_t k, emu_heads_t v, float* out,
                            float* stats, float* partial, hipStream_t s)
 {
-    const unsigned grid = T::grid((int64_t)a.batch * a.kv_heads * p.own * p.splits);
+    const unsigned grid = T::grid(pieces_of(a, p), p.run);
     const auto run = [&]<int ND>() {
         if (a.dim == 16 * ND)
             few_kernel<ND, true><<<grid, 256, 0, s>>>(a, p, q, k, v, out, stats, partial);

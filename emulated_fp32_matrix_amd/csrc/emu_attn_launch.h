@@ -51,6 +51,7 @@ constexpr int attn_waves(AttnPass pass, int nd, bool images)
 struct AttnPlan {
     int waves, tiles, splits, images;
     int64_t own;             // pieces along the team's own side
+    int64_t run;             // neighbouring pieces that go to one XCD
 };
 AttnPlan attn_plan(const AttnArgs& a, AttnPass pass);
 

@@ -18,6 +18,9 @@ namespace {
 
 using T = Team<1, 4>;
 
+// (neighbouring heads lie beside each other in memory)
+__host__ __device__ __forceinline__ int64_t whole_run(const AttnArgs& a) { return ((int64_t)a.batch * a.kv_heads + 31) / 32; }
+
 template <int ND, int NT>
 struct Whole {
     static constexpr int LD = Head<ND>::LD, LM = 16 * NT + 4;
@@ -179,7 +182,7 @@ __global__ __launch_bounds__(256) void forward_kernel(AttnArgs a, emu_heads_t q,
     __shared__ __attribute__((aligned(16))) float lds[4][W::kFloats];
     const int lane = threadIdx.x & 63, m = lane & 15, h = lane >> 4;
     const W w{m, h, lds[T::index()]};
-    T::each_piece((int64_t)a.batch * a.kv_heads, [&](int64_t piece) {
+    T::each_piece((int64_t)a.batch * a.kv_heads, whole_run(a), [&](int64_t piece) {
         const Problem<ND, NT> p(a, piece, m, h);
         typename W::Frag fq, fk, fv, acc;
         typename W::Mat s;
@@ -234,7 +237,7 @@ __global__ __launch_bounds__(256, NT < 3 && ND * NT <= 4 ? 3 : ND * NT <= 8 ? 2 
     __shared__ __attribute__((aligned(16))) float lds[4][W::kFloats];
     const int lane = threadIdx.x & 63, m = lane & 15, h = lane >> 4;
     const W w{m, h, lds[T::index()]};
-    T::each_piece((int64_t)a.batch * a.kv_heads, [&](int64_t piece) {
+    T::each_piece((int64_t)a.batch * a.kv_heads, whole_run(a), [&](int64_t piece) {
         const Problem<ND, NT> p(a, piece, m, h);
         typename W::Frag fq, fk, fv, fd, acc;
         typename W::Mat s, ds;
@@ -291,7 +294,7 @@ __global__ __launch_bounds__(256, NT < 3 && ND * NT <= 4 ? 2 : 1) void second_ke
     __shared__ __attribute__((aligned(16))) float lds[4][W::kFloats];
     const int lane = threadIdx.x & 63, m = lane & 15, h = lane >> 4;
     const W w{m, h, lds[T::index()]};
-    T::each_piece((int64_t)a.batch * a.kv_heads, [&](int64_t piece) {
+    T::each_piece((int64_t)a.batch * a.kv_heads, whole_run(a), [&](int64_t piece) {
         const Problem<ND, NT> p(a, piece, m, h);
         typename W::Frag fq, fk, fv, fd, fvq, fvk, fvv, acc;
         typename W::Mat s, ds, gg, ee;
@@ -410,7 +413,7 @@ hipError_t join_bias(const AttnArgs& a, float* db, const float* partial, hipStre
     return e;
 }
 
-unsigned whole_grid(const AttnArgs& a) { return T::grid((int64_t)a.batch * a.kv_heads); }
+unsigned whole_grid(const AttnArgs& a) { return T::grid((int64_t)a.batch * a.kv_heads, whole_run(a)); }
 
 }  // namespace
 
