@@ -3,18 +3,24 @@
 // One pass over the keys with the running maximum and sum of the softmax: a
 // wave keeps 16 or 32 rows, their queries in registers as the B operand and
 // their results as accumulators (emu_attn_device.h), on split operands
-// (emu_attn_split.h). A team's tile of keys and values is split once, on its
-// way to LDS, for all of its rows.
+// (emu_attn_split.h). A team of four waves shares a tile of keys and values in
+// LDS, split once for all of its rows.
 //
-// Few rows are cut along the keys: each range leaves a maximum, a sum and an
-// unscaled result, and a second launch joins them in order.
+// Where there are few pieces of work, or sequences of different lengths, they
+// are cut along the keys: each range leaves a maximum, a sum and an unscaled
+// result, and a second launch joins them in order.
+//
+// Bound by the matrix units at the power limit: 2 x 16 heads of 2,048 x 4,096 x
+// 64, 68.7 GFLOP, in 327 to 410 us by the clock that the power leaves (168 to
+// 210 TFLOP/s; FP32 library product 153), the matrix units busy half of the
+// time and the vector units, for the softmax and the splits of its weights, the
+// other half.
 #include "emu_attn_split.h"
 
 namespace emu {
 namespace {
 
 constexpr int kMostSplits = 64;
-constexpr int kImageTeams = 2;   // teams that stream the same side, from which on it is split beforehand
 constexpr float kSlack = 4.0f;
 
 template <int ND, int NQ, bool IMAGES>
@@ -27,7 +33,6 @@ __global__ __launch_bounds__(64 * kTeam, attn_waves(AttnPass::forward, ND, IMAGE
     __shared__ __attribute__((aligned(16))) char lds[S::kBuffers * S::kBytes];
     S stream{lds};
     stream.clear();
-    stagger();
     const int lane = threadIdx.x & 63, m = lane & 15, h = lane >> 4;
 
     T::each_piece(pieces_of(a, plan), plan.run, [&](int64_t piece) {
@@ -230,6 +235,13 @@ __global__ __launch_bounds__(256) void join_kernel(AttnJoins j)
 
 unsigned join_grid(int64_t groups) { return (unsigned)(groups < 65536 ? groups : 65536); }
 
+// Teams that stream the same side, from which on it is split beforehand. The
+// splitting itself costs a launch and the bytes, and each team saves a fifth of
+// its time: 8 x 8 heads of 250 x 1,000 x 64 (two teams) forward 44 us without, 35
+// + 17 with, by rows 60 and 47 + 11; 2 x 16 of 2,048 x 4,096 x 64 (16 teams)
+// forward 497 and 399 + 32, by keys 970 and 759 + 12.
+constexpr int image_teams(AttnPass pass) { return pass == AttnPass::forward ? 4 : 2; }
+
 // Ranges of the other side for a wave each of few rows: as many as make 2,048
 // waves (256 compute units of 8), none shorter than 128 keys.
 int few_splits(int64_t waves, int64_t other)
@@ -275,12 +287,14 @@ AttnPlan attn_plan(const AttnArgs& a, AttnPass pass)
     const bool keys = pass == AttnPass::keys || pass == AttnPass::second_keys;
     const int64_t own = keys ? a.keys : a.rows, other = keys ? a.rows : a.keys;
     AttnPlan p{};
-    // (the forward pass has a kernel of its own for few rows)
+    // The forward pass has a kernel of its own for few rows: 16 rows of 8 x 8
+    // heads over 2,048 keys of 64 in 21 us, with tiles of 64 rows 31; a query's
+    // four heads over up to 8,192 keys 22 and 47.
     p.waves = pass == AttnPass::forward && own <= 16 ? 1 : 4;
     p.tiles = own <= 64 ? 1 : attn_tiles(pass, a.dim);
     const int64_t each = p.waves * p.tiles * 16;
     p.own = (own + each - 1) / each;
-    p.images = p.waves == 4 && p.own >= kImageTeams;
+    p.images = p.waves == 4 && p.own >= image_teams(pass);
     const int64_t pieces = (int64_t)a.batch * a.kv_heads * p.own;
     p.splits = pieces == 0      ? 1
                : p.waves == 1 ? few_splits(pieces, other)

@@ -29,14 +29,25 @@ struct AttnArgs {
 // and over keys, and that one's (its rows' sums and results share a plan).
 enum class AttnPass { forward, rows, keys, second_rows, second_keys };
 
-// Tiles of 16 of its own side that a wave's registers hold while two waves fit
-// a SIMD.
+// Tiles of 16 of its own side that a wave keeps, while two waves fit a SIMD:
+// with two, a streamed operand read from LDS serves both. 2 x 16 heads of 2,048
+// x 4,096 x 64: forward 437 us with one and 399 with two, by rows 613 and 534;
+// 96 wide forward 155 and 138; 32 wide second order by rows 706 and 622 (2 x 16
+// heads of 2,000 x 2,048). The passes over keys keep two results, and two tiles
+// of them leave no registers to read ahead: 887 us, with one 783; 32 wide the
+// same.
 constexpr int attn_tiles(AttnPass pass, int dim)
 {
-    return dim <= (pass == AttnPass::forward ? 96 : pass == AttnPass::rows ? 64 : 32) ? 2 : 1;
+    switch (pass) {
+    case AttnPass::forward: return dim <= 96 ? 2 : 1;
+    case AttnPass::rows: return dim <= 64 ? 2 : 1;
+    case AttnPass::second_rows: return dim <= 32 ? 2 : 1;
+    default: return 1;
+    }
 }
 // Waves of a SIMD that the registers are divided among: one where even a tile
-// each of wide heads does not fit half of them.
+// each of wide heads does not fit half of them (more than a few registers would
+// go to memory in every step).
 constexpr int attn_waves(AttnPass pass, int nd, bool images)
 {
     const bool second = pass == AttnPass::second_rows || pass == AttnPass::second_keys;

