@@ -245,12 +245,14 @@ emu_status_t emu_cross_attention_backward(const emu_attention_t* in, emu_heads_t
     if (emu::attn_whole(a))
         return from_hip(emu::launch_whole_backward(a, dout, q, k, v, stats, dq, dk, dv, dbias, w.db, s));
     const emu_heads_t key_side[] = {k, v}, row_side[] = {q, dout};
+    emu::AttnJoins joins{};
     hipError_t e = emu::launch_attn_images(a, w.rows.images && dq != nullptr ? 2 : 0, key_side, w.key_images,
                                            w.keys.images && keys_wanted ? 2 : 0, row_side, w.row_images, s);
     if (e == hipSuccess)
-        e = emu::launch_attn_backward_rows(a, w.rows, dout, q, k, v, out, stats, w.key_images, w.delta, dq, w.dq, s);
+        e = emu::launch_attn_backward_rows(a, w.rows, dout, q, k, v, out, stats, w.key_images, w.delta, dq, w.dq, joins, s);
     if (e == hipSuccess && keys_wanted)
-        e = emu::launch_attn_backward_keys(a, w.keys, dout, q, k, v, w.row_images, stats, w.delta, dk, dv, dbias, w.dk, w.dv, w.db, s);
+        e = emu::launch_attn_backward_keys(a, w.keys, dout, q, k, v, w.row_images, stats, w.delta, dk, dv, dbias, w.dk, w.dv, w.db, joins, s);
+    if (e == hipSuccess) e = emu::launch_attn_joins(joins, s);
     return from_hip(e);
 }
 
@@ -289,13 +291,15 @@ emu_status_t emu_cross_attention_backward2(const emu_attention_t* in, emu_heads_
     const emu::AttnSeconds x{vq, vk, vv, vbias, vbias_batch, vbias_key, dout, q, k, v, out, stats};
     if (emu::attn_whole(a)) return from_hip(emu::launch_whole_second(a, x, gdout, gq, gk, gv, gbias, w.gb, s));
     const emu_heads_t key_side[] = {k, v, vk, vv}, row_side[] = {q, dout, vq};
+    emu::AttnJoins joins{};
     hipError_t e = emu::launch_attn_images(a, w.rows.images ? 4 : 0, key_side, w.key_images,
                                            w.keys.images && keys_wanted ? 3 : 0, row_side, w.row_images, s);
     if (e == hipSuccess) e = emu::launch_attn_second_sums(a, w.rows, x, w.key_images, w.delta, w.sums, s);
     if (e == hipSuccess && rows_wanted)
-        e = emu::launch_attn_second_rows(a, w.rows, x, w.key_images, w.delta, w.sums, gdout, gq, w.go, w.gq, s);
+        e = emu::launch_attn_second_rows(a, w.rows, x, w.key_images, w.delta, w.sums, gdout, gq, w.go, w.gq, joins, s);
     if (e == hipSuccess && keys_wanted)
-        e = emu::launch_attn_second_keys(a, w.keys, x, w.row_images, w.delta, w.sums, w.rows.splits, gk, gv, gbias, w.gk, w.gv, w.gb, s);
+        e = emu::launch_attn_second_keys(a, w.keys, x, w.row_images, w.delta, w.sums, w.rows.splits, gk, gv, gbias, w.gk, w.gv, w.gb, joins, s);
+    if (e == hipSuccess) e = emu::launch_attn_joins(joins, s);
     return from_hip(e);
 }
 

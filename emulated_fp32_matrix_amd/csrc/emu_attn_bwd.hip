@@ -179,21 +179,19 @@ __global__ __launch_bounds__(64 * kTeam, attn_waves(AttnPass::keys, ND, IMAGES))
 
 hipError_t launch_attn_backward_rows(const AttnArgs& a, const AttnPlan& p, emu_heads_t dout, emu_heads_t q,
                                      emu_heads_t k, emu_heads_t v, const float* out, const float* stats,
-                                     const void* images, float* delta, float* dq, float* partial, hipStream_t s)
+                                     const void* images, float* delta, float* dq, float* partial, AttnJoins& joins, hipStream_t s)
 {
     with_shape<AttnPass::rows>(a.dim, p, [&]<int ND, int NQ, bool IMAGES>() {
         rows_kernel<ND, NQ, IMAGES><<<Team<kTeam>::grid(pieces_of(a, p), p.run), 64 * kTeam, 0, s>>>(a, p, dout, q, k, v, static_cast<const char*>(images), out, stats, delta, dq, partial);
     });
-    hipError_t e = hipGetLastError();
-    if (e == hipSuccess && p.splits > 1)
-        e = launch_attn_joins({1, {{1, p.splits, (int64_t)a.batch * a.queries * a.heads * a.dim, partial, dq}}}, s);
-    return e;
+    if (p.splits > 1) joins.add({1, p.splits, (int64_t)a.batch * a.queries * a.heads * a.dim, partial, dq});
+    return hipGetLastError();
 }
 
 hipError_t launch_attn_backward_keys(const AttnArgs& a, const AttnPlan& p, emu_heads_t dout, emu_heads_t q,
                                      emu_heads_t k, emu_heads_t v, const void* images, const float* stats,
                                      const float* delta, float* dk, float* dv, float* dbias, float* partial_k, float* partial_v,
-                                     float* partial_b, hipStream_t s)
+                                     float* partial_b, AttnJoins& joins, hipStream_t s)
 {
     const bool cut = p.splits > 1, join_bias = dbias != nullptr && (cut || a.kv_heads > 1);
     float* const to_k = dk != nullptr && cut ? partial_k : dk;
@@ -202,12 +200,11 @@ hipError_t launch_attn_backward_keys(const AttnArgs& a, const AttnPlan& p, emu_h
     with_shape<AttnPass::keys>(a.dim, p, [&]<int ND, int NT, bool IMAGES>() {
         keys_kernel<ND, NT, IMAGES><<<Team<kTeam>::grid(pieces_of(a, p), p.run), 64 * kTeam, 0, s>>>(a, p, dout, q, k, v, static_cast<const char*>(images), stats, delta, to_k, to_v, to_b);
     });
-    hipError_t e = hipGetLastError();
     const int64_t n = (int64_t)a.batch * a.keys * a.kv_heads * a.dim;
-    if (e == hipSuccess)
-        e = launch_attn_joins({3, {{1, p.splits, n, to_k, dk}, {1, p.splits, n, to_v, dv},
-                                   {a.batch, (int64_t)p.splits * a.kv_heads, a.keys, to_b, dbias}}}, s);
-    return e;
+    joins.add({1, p.splits, n, to_k, dk});
+    joins.add({1, p.splits, n, to_v, dv});
+    joins.add({a.batch, (int64_t)p.splits * a.kv_heads, a.keys, to_b, dbias});
+    return hipGetLastError();
 }
 
 }  // namespace emu

@@ -268,7 +268,7 @@ hipError_t launch_attn_second_sums(const AttnArgs& a, const AttnPlan& p, const A
 
 hipError_t launch_attn_second_rows(const AttnArgs& a, const AttnPlan& p, const AttnSeconds& x, const void* images, const float* delta,
                                    const float* sums, float* gdout, float* gq, float* partial_o, float* partial_q,
-                                   hipStream_t s)
+                                   AttnJoins& joins, hipStream_t s)
 {
     const bool cut = p.splits > 1;
     float* const to_o = gdout != nullptr && cut ? partial_o : gdout;
@@ -277,15 +277,15 @@ hipError_t launch_attn_second_rows(const AttnArgs& a, const AttnPlan& p, const A
         rows_kernel<ND, NQ, IMAGES, false><<<Team<kTeam>::grid(pieces_of(a, p), p.run), 64 * kTeam, 0, s>>>(
             a, p, x, static_cast<const char*>(images), const_cast<float*>(delta), const_cast<float*>(sums), to_o, to_q);
     });
-    hipError_t e = hipGetLastError();
     const int64_t n = (int64_t)a.batch * a.queries * a.heads * a.dim;
-    if (e == hipSuccess) e = launch_attn_joins({2, {{1, p.splits, n, to_o, gdout}, {1, p.splits, n, to_q, gq}}}, s);
-    return e;
+    joins.add({1, p.splits, n, to_o, gdout});
+    joins.add({1, p.splits, n, to_q, gq});
+    return hipGetLastError();
 }
 
 hipError_t launch_attn_second_keys(const AttnArgs& a, const AttnPlan& p, const AttnSeconds& x, const void* images, const float* delta,
                                    const float* sums, int sum_splits, float* gk, float* gv, float* gbias,
-                                   float* partial_k, float* partial_v, float* partial_b, hipStream_t s)
+                                   float* partial_k, float* partial_v, float* partial_b, AttnJoins& joins, hipStream_t s)
 {
     const bool cut = p.splits > 1, join_bias = gbias != nullptr && (cut || a.kv_heads > 1);
     float* const to_k = gk != nullptr && cut ? partial_k : gk;
@@ -294,12 +294,11 @@ hipError_t launch_attn_second_keys(const AttnArgs& a, const AttnPlan& p, const A
     with_shape<AttnPass::second_keys>(a.dim, p, [&]<int ND, int NT, bool IMAGES>() {
         keys_kernel<ND, NT, IMAGES><<<Team<kTeam>::grid(pieces_of(a, p), p.run), 64 * kTeam, 0, s>>>(a, p, x, static_cast<const char*>(images), delta, sums, sum_splits, to_k, to_v, to_b);
     });
-    hipError_t e = hipGetLastError();
     const int64_t n = (int64_t)a.batch * a.keys * a.kv_heads * a.dim;
-    if (e == hipSuccess)
-        e = launch_attn_joins({3, {{1, p.splits, n, to_k, gk}, {1, p.splits, n, to_v, gv},
-                                   {a.batch, (int64_t)p.splits * a.kv_heads, a.keys, to_b, gbias}}}, s);
-    return e;
+    joins.add({1, p.splits, n, to_k, gk});
+    joins.add({1, p.splits, n, to_v, gv});
+    joins.add({a.batch, (int64_t)p.splits * a.kv_heads, a.keys, to_b, gbias});
+    return hipGetLastError();
 }
 
 }  // namespace emu

@@ -109,15 +109,34 @@ size_t attn_rows_partial(const AttnArgs& a, const AttnPlan& p);
 size_t attn_keys_partial(const AttnArgs& a, const AttnPlan& p);
 size_t attn_bias_partial(const AttnArgs& a, const AttnPlan& p);
 
+// out[o][i] = sum over s of in[o][s][i], s in order; outer x inner results.
+// Those of a call are one launch; out null, or in itself: nothing to do.
+struct AttnJoin {
+    int64_t outer, splits, inner;
+    const float* in;
+    float* out;
+};
+constexpr int kAttnJoins = 5;
+struct AttnJoins {
+    int n;
+    AttnJoin of[kAttnJoins];
+    void add(const AttnJoin& x)
+    {
+        if (x.out != nullptr && x.in != x.out && x.outer * x.inner > 0) of[n++] = x;
+    }
+};
+hipError_t launch_attn_joins(const AttnJoins& joins, hipStream_t s);
+
+// The passes' results are in place once `joins`, to which they add, has run.
 // delta: a float per row, written by the pass over rows and read by the pass
 // over keys.  dq may be null (then only delta is written).
 hipError_t launch_attn_backward_rows(const AttnArgs& a, const AttnPlan& p, emu_heads_t dout, emu_heads_t q,
                                      emu_heads_t k, emu_heads_t v, const float* out, const float* stats,
-                                     const void* images, float* delta, float* dq, float* partial, hipStream_t s);
+                                     const void* images, float* delta, float* dq, float* partial, AttnJoins& joins, hipStream_t s);
 hipError_t launch_attn_backward_keys(const AttnArgs& a, const AttnPlan& p, emu_heads_t dout, emu_heads_t q,
                                      emu_heads_t k, emu_heads_t v, const void* images, const float* stats,
                                      const float* delta, float* dk, float* dv, float* dbias, float* partial_k, float* partial_v,
-                                     float* partial_b, hipStream_t s);
+                                     float* partial_b, AttnJoins& joins, hipStream_t s);
 
 // The backward pass's backward pass.
 struct AttnSeconds {
@@ -133,10 +152,10 @@ hipError_t launch_attn_second_sums(const AttnArgs& a, const AttnPlan& p, const A
                                    float* delta, float* sums, hipStream_t s);
 hipError_t launch_attn_second_rows(const AttnArgs& a, const AttnPlan& p, const AttnSeconds& t, const void* images, const float* delta,
                                    const float* sums, float* gdout, float* gq, float* partial_o, float* partial_q,
-                                   hipStream_t s);
+                                   AttnJoins& joins, hipStream_t s);
 hipError_t launch_attn_second_keys(const AttnArgs& a, const AttnPlan& p, const AttnSeconds& t, const void* images, const float* delta,
                                    const float* sums, int sum_splits, float* gk, float* gv, float* gbias,
-                                   float* partial_k, float* partial_v, float* partial_b, hipStream_t s);
+                                   float* partial_k, float* partial_v, float* partial_b, AttnJoins& joins, hipStream_t s);
 
 // Short sequences, each direction in one launch: whether a call's are, and
 // the launches.  partial: floats of attn_whole_partial().
@@ -152,20 +171,6 @@ hipError_t launch_whole_backward(const AttnArgs& a, emu_heads_t dout, emu_heads_
                                  hipStream_t s);
 hipError_t launch_whole_second(const AttnArgs& a, const AttnSeconds& x, float* gdout, float* gq, float* gk, float* gv,
                                float* gbias, float* partial, hipStream_t s);
-
-// out[o][i] = sum over s of in[o][s][i], s in order; outer x inner results.
-// Several at once; out null, or in itself: nothing to do.
-struct AttnJoin {
-    int64_t outer, splits, inner;
-    const float* in;
-    float* out;
-};
-constexpr int kAttnJoins = 3;
-struct AttnJoins {
-    int n;
-    AttnJoin of[kAttnJoins];
-};
-hipError_t launch_attn_joins(const AttnJoins& joins, hipStream_t s);
 
 struct RotaryArgs {
     int64_t batch, tokens;

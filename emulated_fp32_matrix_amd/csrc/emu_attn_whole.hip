@@ -412,8 +412,9 @@ void with_whole(const AttnArgs& a, F&& f)
 hipError_t join_bias(const AttnArgs& a, float* db, const float* partial, hipStream_t s)
 {
     hipError_t e = hipGetLastError();
-    if (e == hipSuccess && a.kv_heads > 1) e = launch_attn_joins({1, {{a.batch, a.kv_heads, a.keys, partial, db}}}, s);
-    return e;
+    AttnJoins joins{};
+    if (a.kv_heads > 1) joins.add({a.batch, a.kv_heads, a.keys, partial, db});
+    return e == hipSuccess ? launch_attn_joins(joins, s) : e;
 }
 
 unsigned whole_grid(const AttnArgs& a) { return T::grid((int64_t)a.batch * a.kv_heads, whole_run(a)); }
