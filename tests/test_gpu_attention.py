@@ -110,6 +110,19 @@ def test_against_formulas(shape):
     say([f"{w:.2g}" for w in check(x)])
 
 
+@pytest.mark.parametrize("dim", [10, 32, 45, 64, 72, 96, 116])
+def test_widths(dim):
+    """Every width of the kernels, where several teams of waves stream the same side and where one does."""
+    check(make(2, 230, 330, 4, 2, dim, bias=True, lengths=[290, 330]))
+    check(make(3, 60, 57, 2, 2, dim, bias=True, lengths=[57, 1, 33]))
+
+
+@pytest.mark.parametrize("batch,queries,keys,heads", [(40, 250, 70, 1), (3, 65, 4200, 2), (9, 30, 2100, 4), (300, 70, 60, 3)])
+def test_ranges_and_runs(batch, queries, keys, heads):
+    """Few and many pieces of work, one and many ranges, sequences of all lengths."""
+    check(make(batch, queries, keys, heads, heads, 32, lengths=[(keys * i) // (batch - 1) for i in range(batch)]), order=2)
+
+
 @pytest.mark.parametrize("queries,keys,dim", [(5, 7, 16), (32, 32, 32), (40, 300, 64), (1, 3000, 64), (200, 90, 48), (70, 200, 100)])
 def test_rows_without_keys(queries, keys, dim):
     """Masked by the bias, the mask or a length of zero: zeros, and no gradients; the other sequences are not touched."""
