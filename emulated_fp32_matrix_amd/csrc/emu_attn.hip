@@ -33,6 +33,7 @@ __global__ __launch_bounds__(64 * kTeam, attn_waves(AttnPass::forward, ND, IMAGE
     __shared__ __attribute__((aligned(16))) char lds[S::kBuffers * S::kBytes];
     S stream{lds};
     stream.clear();
+    stagger();
     const int lane = threadIdx.x & 63, m = lane & 15, h = lane >> 4;
 
     T::each_piece(pieces_of(a, plan), plan.run, [&](int64_t piece) {

@@ -30,6 +30,7 @@ __global__ __launch_bounds__(64 * kTeam, attn_waves(AttnPass::second_rows, ND, I
     __shared__ __attribute__((aligned(16))) char lds[S::kBuffers * S::kBytes];
     S stream{lds};
     stream.clear();
+    stagger();
     const int lane = threadIdx.x & 63, m = lane & 15, h = lane >> 4;
     const int64_t all_rows = (int64_t)a.batch * a.queries * a.heads;
 
@@ -150,6 +151,7 @@ __global__ __launch_bounds__(64 * kTeam, attn_waves(AttnPass::second_keys, ND, I
     __shared__ __attribute__((aligned(16))) char lds[S::kBuffers * S::kBytes];
     S stream{lds};
     stream.clear();
+    stagger();
     const int lane = threadIdx.x & 63, m = lane & 15, h = lane >> 4;
     const int64_t all_rows = (int64_t)a.batch * a.queries * a.heads;
 
