@@ -304,9 +304,10 @@ AttnPlan attn_plan(const AttnArgs& a, AttnPass pass)
     p.own = (own + each - 1) / each;
     p.images = p.waves == 4 && p.own >= image_teams(pass);
     const int64_t pieces = (int64_t)a.batch * a.kv_heads * p.own;
+    const int nd = a.dim > 96 ? 8 : (a.dim + 15) / 16;   // as with_shape()
     p.splits = pieces == 0      ? 1
                : p.waves == 1 ? few_splits(pieces, other)
-                              : splits_for(pieces, other, attn_waves(pass, (a.dim + 15) / 16, p.images), !keys && a.lengths != nullptr);
+                              : splits_for(pieces, other, attn_waves(pass, nd, p.images), !keys && a.lengths != nullptr);
     // a key head's pieces, if there are 16 such runs for each XCD; a wave's few
     // rows share their keys with no other piece
     const int64_t head = p.own * p.splits, even = pieces * p.splits / 128;
