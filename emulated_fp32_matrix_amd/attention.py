@@ -264,7 +264,7 @@ class EmuCrossAttention(torch.nn.Module):
                 raise ValueError("the block's rotary positions need positions and, with a context, context_positions")
             q, k = self.rotary(q, positions), self.rotary(k, positions if context is None else context_positions)
         o = cross_attention(q, k, v, key_bias, key_mask, lengths).flatten(2)
-        if self.training and self.drop.p > 0.0:
+        if self.drop.training and self.drop.p > 0.0:   # (its own mode: it may be sampled in a block that does not train)
             return self.drop(linear_act(o, self.w_o, self.b_o, mode=self.mode), x)
         return linear_act(o, self.w_o, self.b_o, residual=x, mode=self.mode)
 
