@@ -4,9 +4,11 @@
 // lo = x - hi - mid (R: round to nearest even; exact for |x| from 2^-110, below
 // which the lowest pieces run out of BF16's subnormals), and a product is the
 // six products of pieces down to 2^-16 of it, accumulated in FP32 by
-// v_mfma_f32_16x16x32_bf16. What is left out is at most 2^-25 of |a b|, half
-// of FP32's own rounding. A value beyond BF16's largest finite number has hi =
-// that number; infinities give NaN.
+// v_mfma_f32_16x16x32_bf16. Just above a power of two mid comes near 2^-8 of x
+// and lo near 2^-17, so that what is left out, mid lo of either factor and lo lo,
+// is up to 1.99 2^-25 of |a b| (over all mantissas), below 2^-24: as much as FP32's
+// own rounding of the product. A value beyond BF16's largest finite number has
+// hi = that number; infinities give NaN.
 //
 // Why not the FP32 matrix instruction: it has 1/16 of the rate, 6/16 of it per
 // product, and it keeps its SIMD's vector unit from other waves' work
