@@ -83,6 +83,13 @@ typedef struct {
  * finite, NULL arrays that have elements, a short or misaligned (256 bytes)
  * workspace; EMU_STATUS_NOT_SUPPORTED for dim > EMU_ATTENTION_MAX_DIM, batch,
  * queries * heads or keys above 2^30, or a device that is not gfx950.
+ *
+ * Workspaces (of all three calls): ask for each call's own struct.  The bytes
+ * go by its sizes and by whether lengths is NULL (by nothing else that it
+ * points to), since both decide into how many ranges the work is cut, and they
+ * do not grow evenly with any size: a smaller batch, shorter sequences or the
+ * same sizes with lengths may need more.  A workspace that serves several
+ * calls has to hold the most that any of their structs asks for.
  */
 emu_status_t emu_cross_attention_workspace(const emu_attention_t* a, size_t* bytes);
 emu_status_t emu_cross_attention(const emu_attention_t* a, emu_heads_t q, emu_heads_t k, emu_heads_t v,
