@@ -137,9 +137,10 @@ def clock_under_load(torch, emu, gemms, tensors, mode, max_s=4.0):
 
         def read():
             m = amdsmi.amdsmi_get_gpu_metrics_info(handle)
-            # (a later revision of the table has no accumulation counter; its time stamp is the firmware's)
-            return ((m.get("accumulation_counter"), m.get("firmware_timestamp")), m.get("current_gfxclks"),
-                    m.get("current_socket_power"), m.get("average_gfx_activity"))
+            count = m.get("accumulation_counter")
+            if not isinstance(count, int):   # a later revision of the table has none; its time stamp is the firmware's
+                count = m.get("firmware_timestamp")
+            return count, m.get("current_gfxclks"), m.get("current_socket_power"), m.get("average_gfx_activity")
 
         stream = torch.cuda.current_stream()
         last = read()[0]
