@@ -17,8 +17,11 @@ namespace emu {
 constexpr float kLog2e = 1.44269502162933349609375f;
 __device__ __forceinline__ float minus_inf() { return -__builtin_inff(); }
 
-// e^x, x <= 0.  The product's rounding costs |x| 2^-24 of the value, e^x |x|
-// 2^-24 < 2^-25 of the row's largest: below the rounding of the sums it enters.
+// e^x of a score less its row's maximum, which may lag by up to 1 (kSlack of the
+// forward pass, whose maximum the other passes take over).  The product's
+// rounding, and log2(e)'s own, cost up to 1.22 |x| 2^-24 of the value: for x <= 0
+// less than 2^-25 of the row's largest weight, below the rounding of the sums it
+// enters, and for x up to 1 less than 2^-24 of the weight itself.
 __device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
 
 __device__ __forceinline__ float max_lane16(float x)

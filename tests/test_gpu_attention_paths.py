@@ -5,6 +5,7 @@ climb and fall from tile to tile and from range to range; the results of calls
 that want some of the gradients; masks and lengths of other strides and types.
 Outputs, gradients and the gradients' gradients against the formulas in 64 bits
 (tests/attention_reference.py)."""
+import ctypes
 import math
 
 import pytest
@@ -58,7 +59,7 @@ def _slopes(keys, kind, step):
 # (Weights stay above e^-70, so that none of them is below what FP32 holds and the
 # reference's bound, which is relative, applies.)
 @pytest.mark.parametrize("queries,keys,dim", [(3, 300, 32), (3, 3000, 64), (70, 300, 64), (130, 300, 80), (300, 3000, 32), (20, 40, 32)])
-@pytest.mark.parametrize("kind,step", [("even", 0.0), ("steps", 3.99), ("steps", 4.01)])
+@pytest.mark.parametrize("kind,step", [("even", 0.0), ("steps", 0.99), ("steps", 1.01), ("steps", 3.99), ("steps", 4.01)])
 @pytest.mark.parametrize("falls", [False, True])
 def test_maxima_that_move(queries, keys, dim, kind, step, falls):
     """Running maxima that grow by a little less and a little more than what the
@@ -71,7 +72,10 @@ def test_maxima_that_move(queries, keys, dim, kind, step, falls):
     check(x)
 
 
-@pytest.mark.parametrize("step", [3.9, 3.999, 4.0, 4.001, 4.1])
+STEPS = [0.9, 0.999, 1.0, 1.001, 1.1, 3.9, 3.999, 4.0, 4.001, 4.1]
+
+
+@pytest.mark.parametrize("step", STEPS)
 @pytest.mark.parametrize("queries", [70, 300])
 def test_maximum_that_lags(queries, step):
     """One step after the first tile, of about what passes without a rescale: all
@@ -81,6 +85,28 @@ def test_maximum_that_lags(queries, step):
     j = torch.arange(320, device=DEV)
     x["bias"] = torch.where(j < 32, 0.0, step).expand(2, 320).contiguous()
     check(x)
+
+
+@pytest.mark.parametrize("step", STEPS)
+@pytest.mark.parametrize("batch,queries,dim", [(1, 3, 64), (2048, 3, 32), (1, 300, 64), (1024, 70, 64), (512, 300, 80), (128, 1000, 32)])
+def test_kept_maximum_lags_by_one_at_most(batch, queries, dim, step):
+    """An exponent's rounding grows with its size, so the weights' exponents are
+    taken from a maximum that is at most 1 behind: scores of zero, and biases
+    that are the scores then, exactly.  (Many sequences: one range of keys each.)"""
+    keys = 320
+    q, k = torch.zeros(1, 1, 1, dim, device=DEV).expand(batch, queries, 1, dim), torch.ones(1, 1, 1, dim, device=DEV).expand(batch, keys, 1, dim)
+    bias = torch.where(torch.arange(keys, device=DEV) < 32, 0.0, step)
+    a = attention._Attention(batch=batch, queries=queries, keys=keys, heads=1, kv_heads=1, dim=dim, scale=1.0,
+                             key_bias=bias.data_ptr(), key_bias_batch=0, key_bias_key=1)
+    heads = lambda t: attention._Heads(t.data_ptr(), t.stride(0), t.stride(1), t.stride(2))
+    need = ctypes.c_size_t(0)
+    assert attention._lib.emu_cross_attention_workspace(ctypes.byref(a), ctypes.byref(need)) == 0
+    space = torch.empty(need.value + 256, dtype=torch.uint8, device=DEV)
+    out, stats = torch.empty(batch, queries, 1, dim, device=DEV), torch.empty(batch * queries, 2, device=DEV)
+    assert attention._lib.emu_cross_attention(ctypes.byref(a), heads(q), heads(k), heads(k), out.data_ptr(), stats.data_ptr(),
+                                              space.data_ptr() + 255 & -256, need.value, torch.cuda.current_stream().cuda_stream) == 0
+    lag = bias.max() - stats[:, 0]
+    assert float(lag.min()) >= 0.0 and float(lag.max()) <= 1.0
 
 
 NAMES = ("q", "k", "v", "bias")
