@@ -269,7 +269,10 @@ int few_splits(int64_t waves, int64_t other)
 // such a round takes a range and about 6 tiles' time to begin and end a piece,
 // a last one with a compute unit per team 0.8 of it (0.67 to 0.88 measured).
 // The join takes 2 tiles' time and 0.003 a piece. Of sequences that differ in
-// length (`ragged`) the long ones end last, by half a range on average.
+// length (`ragged`) the long ones end last, by half a range on average. (Of the
+// passes over rows: those over keys are counted with the teams of all keys, also
+// of those past their sequence's length, which leave at once; the host does not
+// know the lengths.)
 // Measured against at least 256 of the other side a range and 2,048 waves: 3 x
 // 8 heads of 333 x 515 x 40, forward 27 -> 23 us, second order by rows 89 -> 71;
 // 7 x 6 of 257 x 777 x 80 ragged, second order by keys 143 -> 137; 21 x 8 of 200

@@ -7,8 +7,9 @@
 // keys are requested before the present ones are used, so that a compute
 // unit's waves keep 64 KB and more on their way. The ranges' results are joined
 // by a second launch (emu_attn.hip). Eight sequences of up to 8,192 keys, 4 key
-// heads of 64 (67 MB) in 20 to 22 us: 3.2 TB/s, since the longest sequence's waves
-// go on alone; and the join 8.
+// heads of 64 (67.6 MB read, 2.2 written) in 20 to 22 us: 3.2 to 3.5 TB/s, since all
+// sequences are cut into the same number of ranges and the longest one's waves go
+// on alone; and the join 4 to 5.
 #include "emu_attn_f32.h"
 
 namespace emu {

@@ -45,9 +45,15 @@ constexpr int attn_tiles(AttnPass pass, int dim)
     default: return 1;
     }
 }
-// Waves of a SIMD that the registers are divided among: one where even a tile
-// each of wide heads does not fit half of them (more than a few registers would
-// go to memory in every step).
+// Waves of a SIMD that the registers are divided among: two, though several
+// kernels then keep up to 65 registers in memory, except where that costs more
+// than the second wave hides. us with one and two: second order over keys of 33
+// to 64 wide heads (58 and 61 of them in memory without images, 13 and 14 with)
+// 2 x 16 heads of 1,000 x 2,048 x 64 whole call 1,051 and 920, 23 x 8 of 1,331 x 60 x
+// 64 513 and 464, 2 x 8 of 2,000 x 50 x 48 113 and 118; the second order's passes of
+// 65 to 96 wide ones 2 x 16 of 1,000 x 2,048 x 96 1,523 and 1,552, 8 x 8 of 300 x 60 x
+// 80 111 and 127, 8 x 8 of 60 x 300 x 96 132 and 169. Above 96 wide the own side alone
+// takes more than half of the registers in the passes that have one here.
 constexpr int attn_waves(AttnPass pass, int nd, bool images)
 {
     const bool second = pass == AttnPass::second_rows || pass == AttnPass::second_keys;

@@ -10,10 +10,12 @@
 // the keys need the weights with the keys across the lanes: those are
 // transposed through the same LDS, which costs less than making them again.
 //
-// Bound by memory: 17,280 x 8 heads of 32 x 32 x 32 forward (2.27 GB) in 442 us,
-// 5.1 TB/s; backward (3.97 GB) in 835, 4.8; second order (6.24 GB) in 1,680, 3.7,
-// where 12 products (709 us at FP32's rate) lie beside the memory (1,283) only in
-// part.
+// Bound by memory: 17,280 x 8 heads of 32 x 32 x 32, a tenth of their keys out of
+// reach and not read, forward (2.16 GB) in 442 us, 4.9 TB/s; backward (3.92 GB) in
+// 835, 4.7; second order (6.19 GB) in 1,680, 3.7, where 12 products (709 us at
+// FP32's rate) lie beside the memory (1,283) only in part. Of three tiles a SIMD has
+// one wave: forward above 48 wide, backward above 32, in the second order at every
+// width (there 56, 138 and 210 registers of 32, 48 and 64 wide heads are in memory).
 #include "emu_attn_f32.h"
 
 namespace emu {
@@ -423,7 +425,9 @@ unsigned whole_grid(const AttnArgs& a) { return T::grid((int64_t)a.batch * a.kv_
 
 // Both ways, us (forward; backward; second order), 2,000 x 8 heads: 32 x 32 x 32
 // 66; 114; 234, by tiles 134; 407; 1,231. 46 x 46 x 64 262; 490; 1,306, by tiles
-// 423; 1,060; 3,110. A fourth tile of 16 would not fit the registers.
+// 423; 1,060; 3,110. (The third tile of 16 does not fit the registers either in the
+// second order of heads above 16 wide, and is the faster way all the same; a fourth
+// was not tried.)
 bool attn_whole(const AttnArgs& a) { return a.dim <= 64 && a.rows <= 48 && a.keys <= 48; }
 
 hipError_t launch_whole_forward(const AttnArgs& a, emu_heads_t q, emu_heads_t k, emu_heads_t v, float* out, float* stats,
