@@ -9,6 +9,8 @@
 // backward pass.  Taking the sums first keeps the differences G - g and T - t
 // whole before they are multiplied; one pass with running results would take
 // them between sums.
+// It costs products: a step of training on forces runs 31 where 19 have to be made
+// (the sums' five again, and the scores in every pass).
 //
 // Bound by the matrix units with few waves beside them, since the own side's
 // pieces and results fill the registers: 2 x 16 heads of 1,000 x 2,048 x 64, 8.4

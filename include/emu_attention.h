@@ -69,13 +69,14 @@ typedef struct {
  * out: [batch][queries][heads][dim], dense.  stats: [batch][queries][heads][2]
  * receives what the backward passes need of each row's softmax, or NULL.
  *
- * Products run on the FP32 matrix instruction where sequences are short (rows
- * and keys up to 48, heads up to 64 wide) and in the forward pass of up to 16
- * rows; elsewhere on BF16 pieces of the operands, six products down to 2^-16
- * each, which leave out less than 2^-24 of a product, FP32's own rounding
- * (more of a factor below 2^-110, whose lowest pieces BF16 does not hold).
- * There an infinite element of a query or of a key or value that takes part
- * gives NaN.  Running maxima, sums and outputs are held in FP32.
+ * Products run on the FP32 matrix instruction where sequences are short (up to
+ * 48 keys and 48 rows of a key head, queries times the heads that share it;
+ * heads up to 64 wide) and in the forward pass of up to 16 rows; elsewhere on
+ * BF16 pieces of the operands, six products down to 2^-16 each, which leave out
+ * less than 2^-24 of a product, FP32's own rounding (more of a factor below
+ * 2^-110, whose lowest pieces BF16 does not hold).  There an infinite element
+ * of a query or of a key or value that takes part gives NaN.  Running maxima,
+ * sums and outputs are held in FP32.
  *
  * batch, queries or heads 0: nothing is done; keys == 0: zeros.
  * Errors: EMU_STATUS_INVALID_VALUE for a negative size, dim < 1, kv_heads < 1
