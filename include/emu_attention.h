@@ -76,7 +76,8 @@ typedef struct {
  * less than 2^-24 of a product, FP32's own rounding (more of a factor below
  * 2^-110, whose lowest pieces BF16 does not hold).  There an infinite element
  * of a query or of a key or value that takes part gives NaN.  Running maxima,
- * sums and outputs are held in FP32.
+ * sums and outputs are held in FP32, the outputs before they are divided by the
+ * weights' sum: values above 2^126 / keys in size may pass FP32's range there.
  *
  * batch, queries or heads 0: nothing is done; keys == 0: zeros.
  * Errors: EMU_STATUS_INVALID_VALUE for a negative size, dim < 1, kv_heads < 1
